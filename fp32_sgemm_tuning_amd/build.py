@@ -40,12 +40,16 @@ UNITS = [
     ("sgemm_lean_ops.hip", VGPR_FORM),
     ("sgemm_lean_split_t.hip", VGPR_FORM),
     ("sgemm_lowp.hip", VGPR_FORM),
+    ("sgemm_group.hip", VGPR_FORM),
+    ("sgemm_xent.hip", VGPR_FORM),
+    ("sgemm_w4.hip", VGPR_FORM),
 ]
 SOURCES = [os.path.join(CSRC, u) for u, _ in UNITS]
 # units rebuilt with the LDS poison for the race-check library (the rest of
 # that library is the normal build's sgemm.o)
 POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u != "sgemm.hip"]
-DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp")] + \
+DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp", "sgemm_lowp.hpp",
+                                                     "sgemm_tile16.hpp")] + \
     [os.path.join(INCLUDE, "sgemm.h")]
 
 ARCH = "gfx950"

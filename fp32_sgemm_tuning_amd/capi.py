@@ -30,6 +30,7 @@ SGEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024 + 16 * 1024
 
 SGEMM_DTYPE_BF16 = 1
 SGEMM_DTYPE_F16 = 2
+SGEMM_DTYPE_F32 = 3
 
 SGEMM_OP_N = 0
 SGEMM_OP_T = 1
@@ -46,7 +47,9 @@ EXPORTS = ("sgemm", "sgemm_ex", "sgemm_select_variant", "sgemm_num_variants",
            "sgemm_cm_strided_batched", "sgemm_lowp", "sgemm_lowp_ex", "sgemm_lowp_select_variant",
            "sgemm_lowp_variant_name", "sgemm_lowp_split_factor", "sgemm_tail_split", "sgemm_lowp_op",
            "sgemm_lowp_strided_batched", "sgemm_workspace_bytes", "sgemm_release_workspaces",
-           "sgemm_noalloc")
+           "sgemm_noalloc", "sgemm_lowp_grouped", "sgemm_lowp_grouped_workspace", "sgemm_lowp_grouped_wgrad",
+           "sgemm_lowp_grouped_wgrad_workspace", "sgemm_lowp_xent", "sgemm_lowp_xent_grad",
+           "sgemm_lowp_xent_workspace", "sgemm_w4", "sgemm_w4_quantize", "sgemm_w4_dequantize")
 
 _lib = None
 
@@ -122,6 +125,20 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.sgemm_tail_split.restype = i
     lib.sgemm_split_factor.argtypes = [i, i, i, i]
     lib.sgemm_split_factor.restype = i
+    for name, args, res in (
+            ("sgemm_lowp_grouped", [i, i, i, i, i, i, f, vp, i, vp, i, ll, vp, f, vp, i, i, vp, ll, vp], i),
+            ("sgemm_lowp_grouped_workspace", [i, i, i, i, i, vp, i, vp, i, ll], ll),
+            ("sgemm_lowp_grouped_wgrad", [i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, ll, i, vp, ll, vp], i),
+            ("sgemm_lowp_grouped_wgrad_workspace", [i, i, i, vp, i, vp, i], ll),
+            ("sgemm_lowp_xent", [i, i, i, i, f, vp, i, vp, i, vp, ll, vp, vp, vp, ll, vp], i),
+            ("sgemm_lowp_xent_grad",
+             [i, i, i, i, f, vp, i, vp, i, vp, ll, vp, vp, i, vp, i, vp, i, vp, ll, vp], i),
+            ("sgemm_lowp_xent_workspace", [i, i, i, vp, i, vp, i, i], ll),
+            ("sgemm_w4", [i, i, i, i, f, vp, i, vp, vp, vp, i, f, vp, i, i, vp], i),
+            ("sgemm_w4_quantize", [i, i, i, vp, i, i, vp, vp, vp, vp], i),
+            ("sgemm_w4_dequantize", [i, i, i, vp, vp, vp, i, vp, i, vp], i)):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = res
     lib.sgemm_strerror.argtypes = [i]
     lib.sgemm_strerror.restype = cp
     lib.sgemm_last_hip_error.argtypes = []
@@ -207,6 +224,54 @@ def sgemm_lowp_strided_batched(dtype, op_a, op_b, M, N, K, alpha, A, lda, sa, B,
 
 def sgemm_lowp_select_variant(M, N, K, A, lda, B, ldb):
     return load().sgemm_lowp_select_variant(M, N, K, A, lda, B, ldb)
+
+
+def sgemm_lowp_grouped(dtype, op_b, groups, M, N, K, alpha, A, lda, B, ldb, stride_b, offsets, beta, C, ldc, dtype_c,
+                       workspace, workspace_bytes, stream):
+    return load().sgemm_lowp_grouped(dtype, op_b, groups, M, N, K, alpha, A, lda, B, ldb, stride_b, offsets, beta, C,
+                                     ldc, dtype_c, workspace, workspace_bytes, stream)
+
+
+def sgemm_lowp_grouped_workspace(op_b, groups, M, N, K, A, lda, B, ldb, stride_b):
+    return load().sgemm_lowp_grouped_workspace(op_b, groups, M, N, K, A, lda, B, ldb, stride_b)
+
+
+def sgemm_lowp_grouped_wgrad(dtype, groups, M, N, K, alpha, A, lda, D, ldd, offsets, beta, C, ldc, stride_c, dtype_c,
+                             workspace, workspace_bytes, stream):
+    return load().sgemm_lowp_grouped_wgrad(dtype, groups, M, N, K, alpha, A, lda, D, ldd, offsets, beta, C, ldc,
+                                           stride_c, dtype_c, workspace, workspace_bytes, stream)
+
+
+def sgemm_lowp_grouped_wgrad_workspace(M, N, K, A, lda, D, ldd):
+    return load().sgemm_lowp_grouped_wgrad_workspace(M, N, K, A, lda, D, ldd)
+
+
+def sgemm_lowp_xent(dtype, M, N, K, alpha, X, ldx, W, ldw, target, ignore_index, loss, lse, workspace,
+                    workspace_bytes, stream):
+    return load().sgemm_lowp_xent(dtype, M, N, K, alpha, X, ldx, W, ldw, target, ignore_index, loss, lse, workspace,
+                                  workspace_bytes, stream)
+
+
+def sgemm_lowp_xent_grad(dtype, M, N, K, alpha, X, ldx, W, ldw, target, ignore_index, lse, dloss, dloss_stride, dX,
+                         lddx, dW, lddw, workspace, workspace_bytes, stream):
+    return load().sgemm_lowp_xent_grad(dtype, M, N, K, alpha, X, ldx, W, ldw, target, ignore_index, lse, dloss,
+                                       dloss_stride, dX, lddx, dW, lddw, workspace, workspace_bytes, stream)
+
+
+def sgemm_lowp_xent_workspace(M, N, K, X, ldx, W, ldw, grad):
+    return load().sgemm_lowp_xent_workspace(M, N, K, X, ldx, W, ldw, grad)
+
+
+def sgemm_w4(dtype, M, N, K, alpha, X, ldx, packed, scales, zeros, group, beta, C, ldc, dtype_c, stream):
+    return load().sgemm_w4(dtype, M, N, K, alpha, X, ldx, packed, scales, zeros, group, beta, C, ldc, dtype_c, stream)
+
+
+def sgemm_w4_quantize(dtype, N, K, W, ldw, group, packed, scales, zeros, stream):
+    return load().sgemm_w4_quantize(dtype, N, K, W, ldw, group, packed, scales, zeros, stream)
+
+
+def sgemm_w4_dequantize(dtype, N, K, packed, scales, zeros, group, W, ldw, stream):
+    return load().sgemm_w4_dequantize(dtype, N, K, packed, scales, zeros, group, W, ldw, stream)
 
 
 def sgemm_lowp_variant_name(variant):

@@ -24,7 +24,7 @@
 #include "sgemm.h"
 #include "sgemm_kernels.hpp"
 
-#define SGEMM_LIB_VERSION 1
+#define SGEMM_LIB_VERSION 2
 
 namespace sgemm_mi355x {
 // Lean direct-to-LDS kernels (sgemm_lean.hip, built with MFMA results in
@@ -63,6 +63,15 @@ int record_hip_error(hipError_t e, const char *what) {
              hipGetErrorString(e), (int)e);
     return SGEMM_STATUS_HIP_ERROR;
 }
+
+}  // namespace
+
+// For the entry points of the other translation units.
+namespace sgemm_mi355x {
+int hip_status(hipError_t e, const char *what) { return record_hip_error(e, what); }
+}  // namespace sgemm_mi355x
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -1650,9 +1659,9 @@ const char *sgemm_strerror(int status) {
         case SGEMM_STATUS_INVALID_VARIANT: return "unknown kernel variant";
         case SGEMM_STATUS_UNSUPPORTED: return "variant needs 16-byte aligned pointers and leading dimensions";
         case SGEMM_STATUS_INVALID_OP: return "operation code is neither SGEMM_OP_N nor SGEMM_OP_T";
-        case SGEMM_STATUS_INVALID_DTYPE: return "input type is neither SGEMM_DTYPE_BF16 nor SGEMM_DTYPE_F16";
+        case SGEMM_STATUS_INVALID_DTYPE: return "element type not taken here";
         case SGEMM_STATUS_SCRATCH_TOO_SMALL:
-            return "sgemm_noalloc: the split of K needs more scratch than SGEMM_NOALLOC_SCRATCH_BYTES";
+            return "scratch or workspace missing, unaligned or smaller than the call needs";
         default: return "unknown status";
     }
 }

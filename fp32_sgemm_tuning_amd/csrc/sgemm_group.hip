@@ -1,0 +1,306 @@
+// Products grouped by rows, 16-bit inputs with FP32 accumulation: the rows
+// of A are in groups (offsets[g] .. offsets[g+1], read on the device), each
+// with a matrix B[g] of its own.
+//
+//   group_rows_kernel   C[rows of g] = alpha * A[rows of g] * op(B[g]) + beta * C
+//   group_k_kernel      C[g] = alpha * A[rows of g]^T * D[rows of g] + beta * C[g]
+//
+// Both run the K loop of sgemm_lowp.hpp on one block tile.  The host does
+// not know the groups' sizes, so the first kernel's grid covers the most
+// tiles that any split of the rows can have, floor((M + g*(BM-1)) / BM) tile
+// rows for g = min(groups, M) groups, and a workgroup finds its tile from
+// the offsets (one wave-wide scan of the groups' tile counts); workgroups
+// past the last tile end at once.
+#include <algorithm>
+
+#include "sgemm_tile16.hpp"
+
+namespace sgemm_mi355x {
+
+struct GroupArgs {
+    const char *A, *B;
+    char *C;
+    long lda, ldb, ldc, strideB, strideC;   // elements
+    const int *offsets;
+    int groups, M, N, K;                    // M: rows of A
+    float alpha, beta;
+};
+
+// Rows of group g, clamped to 0 .. M whatever the offsets hold.
+__device__ __forceinline__ void group_rows(const int *offsets, int g, int M, int &lo, int &rows) {
+    lo = min(max(offsets[g], 0), M);
+    rows = min(max(offsets[g + 1], lo), M) - lo;
+}
+
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// The group and the tile of workgroup `bid`, the groups' tiles one after
+// another; false past the last.  Wave-uniform.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const GroupArgs &p, int tiles_n, int bid, int &g, int &lo, int &rows, int &tm,
+                                          int &tn) {
+    const int lane = threadIdx.x & 63;
+    auto tiles = [&](int base) {
+        int l = 0, r = 0;
+        if (base + lane < p.groups) group_rows(p.offsets, base + lane, p.M, l, r);
+        return (r + BM - 1) / BM;
+    };
+    const int first = tiles(0);
+    int total = wave_sum(first);
+    for (int base = 64; base < p.groups; base += 64) total += wave_sum(tiles(base));
+    total = __builtin_amdgcn_readfirstlane(total) * tiles_n;
+    if (bid >= total) return false;
+    int id = xcd_run(bid, total);
+    for (int base = 0;; base += 64) {
+        const int mine = base ? tiles(base) : first;
+        int upto = mine;                                    // tile rows up to this lane's group
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int below = __shfl_up(upto, d);
+            if (lane >= d) upto += below;
+        }
+        const unsigned long past = __ballot(id < upto * tiles_n);
+        if (past) {
+            const int at = __builtin_ctzl(past);
+            const int count = __builtin_amdgcn_readlane(mine, at);
+            id -= (__builtin_amdgcn_readlane(upto, at) - count) * tiles_n;
+            g = base + at;
+            group_rows(p.offsets, g, p.M, lo, rows);
+            g = __builtin_amdgcn_readfirstlane(g);
+            lo = __builtin_amdgcn_readfirstlane(lo);
+            rows = __builtin_amdgcn_readfirstlane(rows);
+            raster(id, count, tiles_n, tm, tn);
+            return true;
+        }
+        id -= __builtin_amdgcn_readlane(upto, 63) * tiles_n;
+    }
+}
+
+template <class T, bool F16, bool TB, bool OUT16>
+__global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int tiles_n = (p.N + T::BN - 1) / T::BN;
+    int g, lo, rows, tm, tn;
+    if (!find_tile<T::BM>(p, tiles_n, blockIdx.x, g, lo, rows, tm, tn)) return;
+    const Operands16 q = {p.A + 2L * lo * p.lda, p.B + 2L * g * p.strideB, p.lda, p.ldb, rows, p.N, p.K};
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, false, TB>(q, tm * T::BM, tn * T::BN, lds, acc);
+    store_tile<T, F16, OUT16>(acc, tm * T::BM, tn * T::BN, rows, p.N, p.C + (OUT16 ? 2L : 4L) * lo * p.ldc, p.ldc, p.alpha,
+                              p.beta);
+}
+
+// A [M][K] and B [M][N] by rows; C[g] is K x N, the sum runs over the
+// group's rows.  A group's tiles go round the XCDs in runs of their own, so
+// that uneven groups still load the XCDs evenly.
+template <class T, bool F16, bool OUT16>
+__global__ void __launch_bounds__(T::NT) group_k_kernel(GroupArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int tiles_m = (p.K + T::BM - 1) / T::BM, tiles_n = (p.N + T::BN - 1) / T::BN;
+    const int tiles = tiles_m * tiles_n, per = (tiles + 7) >> 3;
+    const int g = blockIdx.x / (8 * per), id = (blockIdx.x & 7) * per + (blockIdx.x - g * 8 * per >> 3);
+    if (id >= tiles) return;
+    int lo, rows, tm, tn;
+    group_rows(p.offsets, g, p.M, lo, rows);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    rows = __builtin_amdgcn_readfirstlane(rows);
+    raster(id, tiles_m, tiles_n, tm, tn);
+    const Operands16 q = {p.A + 2L * lo * p.lda, p.B + 2L * lo * p.ldb, p.lda, p.ldb, p.K, p.N, rows};
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, true, false>(q, tm * T::BM, tn * T::BN, lds, acc);
+    store_tile<T, F16, OUT16>(acc, tm * T::BM, tn * T::BN, p.K, p.N, p.C + (OUT16 ? 2L : 4L) * g * p.strideC, p.ldc,
+                              p.alpha, p.beta);
+}
+
+__global__ void __launch_bounds__(256) pad_rows_kernel(const unsigned short *src, long ld, long stride, int rows,
+                                                       int cols, unsigned short *dst, int rows_out, int chunks) {
+    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+    const long n = (long)rows_out * chunks;
+    src += blockIdx.y * stride;
+    dst += blockIdx.y * n * 8;
+    for (long q = blockIdx.x * 256L + threadIdx.x; q < n; q += gridDim.x * 256L) {
+        const long r = q / chunks;
+        const int c = (int)(q - r * chunks) * 8;
+        u16x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = r < rows && c + e < cols ? src[r * ld + c + e] : (unsigned short)0;
+        reinterpret_cast<u16x8 *>(dst)[q] = v;
+    }
+}
+
+hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, int rows_out,
+                    hipStream_t s) {
+    const int chunks = (cols + 7) / 8;
+    const long n = (long)rows_out * chunks;
+    const long blocks = std::min((n + 255) / 256, std::max(4096L / copies, 16L));
+    return launch_k(pad_rows_kernel, dim3((unsigned)blocks, (unsigned)copies), dim3(256), s,
+                    static_cast<const unsigned short *>(src), ld, stride, rows, cols, static_cast<unsigned short *>(dst),
+                    rows_out, chunks);
+}
+
+namespace {
+
+constexpr int kMaxGroups = 65535;   // launch grid extent of the padded copies
+
+template <class T, bool OUT16>
+hipError_t launch_rows(const GroupArgs &p, bool f16, bool tb, hipStream_t s) {
+    const long groups = std::min(p.groups, p.M);
+    const long grid = (p.M + groups * (T::BM - 1)) / T::BM * ((p.N + T::BN - 1) / T::BN);
+    const dim3 g((unsigned)grid), b(T::NT);
+    if (f16) return tb ? launch_k(group_rows_kernel<T, true, true, OUT16>, g, b, s, p)
+                       : launch_k(group_rows_kernel<T, true, false, OUT16>, g, b, s, p);
+    return tb ? launch_k(group_rows_kernel<T, false, true, OUT16>, g, b, s, p)
+              : launch_k(group_rows_kernel<T, false, false, OUT16>, g, b, s, p);
+}
+
+template <class T, bool OUT16>
+hipError_t launch_k_groups(const GroupArgs &p, bool f16, hipStream_t s) {
+    const long tiles = (long)((p.K + T::BM - 1) / T::BM) * ((p.N + T::BN - 1) / T::BN);
+    const dim3 g((unsigned)(ceil_to(tiles, 8) * p.groups)), b(T::NT);
+    return f16 ? launch_k(group_k_kernel<T, true, OUT16>, g, b, s, p)
+               : launch_k(group_k_kernel<T, false, OUT16>, g, b, s, p);
+}
+
+template <class T>
+hipError_t launch_rows(const GroupArgs &p, bool f16, bool tb, bool out16, hipStream_t s) {
+    return out16 ? launch_rows<T, true>(p, f16, tb, s) : launch_rows<T, false>(p, f16, tb, s);
+}
+
+template <class T>
+hipError_t launch_k_groups(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
+    return out16 ? launch_k_groups<T, true>(p, f16, s) : launch_k_groups<T, false>(p, f16, s);
+}
+
+bool in_dtype(int d) { return d == SGEMM_DTYPE_BF16 || d == SGEMM_DTYPE_F16; }
+
+// Bytes of the zero-padded copies of the operands whose rows are not whole
+// aligned 16-byte chunks; 0 for an operand that is taken as it is.  (A chunk
+// that straddles K holds zeros in the copy, and the K loop reads rows of an
+// untransposed B past K as zeros.)
+struct Copies {
+    long a, b;
+};
+
+Copies rows_copies(bool tb, int groups, int M, int N, int K, const void *A, int lda, const void *B, int ldb,
+                   long long stride_b) {
+    const bool a = !chunk_rows(A, lda, K), b = !chunk_rows(B, ldb, tb ? K : N) || (groups > 1 && stride_b % 8 != 0);
+    return {a ? ceil_to(2L * M * ceil_to(K, 8), 256) : 0,
+            b ? 2L * groups * (tb ? N * ceil_to(K, 8) : K * ceil_to(N, 8)) : 0};
+}
+
+Copies k_copies(int M, int N, int K, const void *A, int lda, const void *D, int ldd) {
+    return {chunk_rows(A, lda, K) ? 0 : ceil_to(2L * M * ceil_to(K, 8), 256),
+            chunk_rows(D, ldd, N) ? 0 : 2L * M * ceil_to(N, 8)};
+}
+
+bool scratch_ok(long need, const void *workspace, long long bytes) {
+    return need == 0 || (workspace != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(workspace) & 15) == 0);
+}
+
+}  // namespace
+}  // namespace sgemm_mi355x
+
+using namespace sgemm_mi355x;
+
+extern "C" {
+
+long long sgemm_lowp_grouped_workspace(int op_b, int groups, int M, int N, int K, const void *A, int lda, const void *B,
+                                       int ldb, long long stride_b) {
+    if (op_b != SGEMM_OP_N && op_b != SGEMM_OP_T) return SGEMM_STATUS_INVALID_OP;
+    if (groups < 0 || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    if (groups == 0 || M == 0 || N == 0 || K == 0) return 0;
+    const Copies c = rows_copies(op_b == SGEMM_OP_T, groups, M, N, K, A, lda, B, ldb, stride_b);
+    return c.a + c.b;
+}
+
+int sgemm_lowp_grouped(int dtype, int op_b, int groups, int M, int N, int K, float alpha, const void *A, int lda,
+                       const void *B, int ldb, long long stride_b, const int *offsets, float beta, void *C, int ldc,
+                       int dtype_c, void *workspace, long long workspace_bytes, void *stream) {
+    if (!in_dtype(dtype) || (dtype_c != dtype && dtype_c != SGEMM_DTYPE_F32)) return SGEMM_STATUS_INVALID_DTYPE;
+    if (op_b != SGEMM_OP_N && op_b != SGEMM_OP_T) return SGEMM_STATUS_INVALID_OP;
+    const bool tb = op_b == SGEMM_OP_T, f16 = dtype == SGEMM_DTYPE_F16, out16 = dtype_c != SGEMM_DTYPE_F32;
+    if (groups < 0 || groups > kMaxGroups || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    if (lda < std::max(K, 1) || ldb < std::max(tb ? K : N, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if (stride_b < 0 || K > kMaxLd16 || N > kMaxLd16) return SGEMM_STATUS_INVALID_DIM;
+    if (((long)M + (long)std::min(groups, M) * 31) / 32 * ((N + 127) / 128) > 0x7fffffffL) return SGEMM_STATUS_INVALID_DIM;
+    if (groups == 0 || M == 0 || N == 0) return SGEMM_STATUS_OK;
+    if (C == nullptr || offsets == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return SGEMM_STATUS_NULL_POINTER;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    GroupArgs p = {static_cast<const char *>(A), static_cast<const char *>(B), static_cast<char *>(C), lda, ldb, ldc,
+                   stride_b, 0, offsets, groups, M, N, K, alpha, beta};
+    if (K > 0) {
+        const Copies c = rows_copies(tb, groups, M, N, K, A, lda, B, ldb, stride_b);
+        if (!scratch_ok(c.a + c.b, workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
+        char *w = static_cast<char *>(workspace);
+        hipError_t e = hipSuccess;
+        if (c.a) {
+            e = pad_rows(A, lda, 0, 1, M, K, w, M, s);
+            p.A = w;
+            p.lda = ceil_to(K, 8);
+        }
+        if (e == hipSuccess && c.b) {
+            const int rows = tb ? N : K, cols = tb ? K : N;
+            e = pad_rows(B, ldb, stride_b, groups, rows, cols, w + c.a, rows, s);
+            p.B = w + c.a;
+            p.ldb = ceil_to(cols, 8);
+            p.strideB = rows * p.ldb;
+        }
+        if (e != hipSuccess) return hip_status(e, "kernel launch");
+    }
+    const long rows = M / groups;           // rows of an average group
+    const hipError_t e = rows <= 32 ? launch_rows<Tile32>(p, f16, tb, out16, s)
+                         : rows <= 512 ? launch_rows<Tile128>(p, f16, tb, out16, s)
+                                       : launch_rows<Tile256>(p, f16, tb, out16, s);
+    return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
+}
+
+long long sgemm_lowp_grouped_wgrad_workspace(int M, int N, int K, const void *A, int lda, const void *D, int ldd) {
+    if (M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    if (M == 0 || N == 0 || K == 0) return 0;
+    const Copies c = k_copies(M, N, K, A, lda, D, ldd);
+    return c.a + c.b;
+}
+
+int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float alpha, const void *A, int lda,
+                             const void *D, int ldd, const int *offsets, float beta, void *C, int ldc,
+                             long long stride_c, int dtype_c, void *workspace, long long workspace_bytes,
+                             void *stream) {
+    if (!in_dtype(dtype) || (dtype_c != dtype && dtype_c != SGEMM_DTYPE_F32)) return SGEMM_STATUS_INVALID_DTYPE;
+    const bool f16 = dtype == SGEMM_DTYPE_F16, out16 = dtype_c != SGEMM_DTYPE_F32;
+    if (groups < 0 || groups > kMaxGroups || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    if (lda < std::max(K, 1) || ldd < std::max(N, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if (K > kMaxLd16 || N > kMaxLd16) return SGEMM_STATUS_INVALID_DIM;
+    if (groups > 1 && K > 0 && N > 0 && stride_c < (K - 1LL) * ldc + N) return SGEMM_STATUS_INVALID_DIM;
+    if ((K + 127L) / 128 * ((N + 127) / 128) + 8 > 0x7fffffffL / std::max(groups, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if (groups == 0 || N == 0 || K == 0) return SGEMM_STATUS_OK;
+    if (C == nullptr || offsets == nullptr || (M > 0 && (A == nullptr || D == nullptr))) return SGEMM_STATUS_NULL_POINTER;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    GroupArgs p = {static_cast<const char *>(A), static_cast<const char *>(D), static_cast<char *>(C), lda, ldd, ldc,
+                   0, stride_c, offsets, groups, M, N, K, alpha, beta};
+    if (M > 0) {
+        const Copies c = k_copies(M, N, K, A, lda, D, ldd);
+        if (!scratch_ok(c.a + c.b, workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
+        char *w = static_cast<char *>(workspace);
+        hipError_t e = hipSuccess;
+        if (c.a) {
+            e = pad_rows(A, lda, 0, 1, M, K, w, M, s);
+            p.A = w;
+            p.lda = ceil_to(K, 8);
+        }
+        if (e == hipSuccess && c.b) {
+            e = pad_rows(D, ldd, 0, 1, M, N, w + c.a, M, s);
+            p.B = w + c.a;
+            p.ldb = ceil_to(N, 8);
+        }
+        if (e != hipSuccess) return hip_status(e, "kernel launch");
+    }
+    const long tiles256 = (K + 255L) / 256 * ((N + 255) / 256) * groups;
+    const hipError_t e = tiles256 >= 256 ? launch_k_groups<Tile256>(p, f16, out16, s)
+                                         : launch_k_groups<Tile128>(p, f16, out16, s);
+    return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
+}
+
+}  // extern "C"

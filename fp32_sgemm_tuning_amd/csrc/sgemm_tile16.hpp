@@ -1,0 +1,149 @@
+// What the kernels built on the 16-bit K loop (sgemm_lowp.hpp) share beyond
+// it: tile shapes, the raster of a tile grid whose height only the device
+// knows, and stores of FP32 accumulators as FP32 or 16-bit values.
+#pragma once
+
+#include "../../include/sgemm.h"
+#include "sgemm_lowp.hpp"
+
+namespace sgemm_mi355x {
+
+// Status of a HIP error for the C ABI, its text kept for
+// sgemm_last_hip_error() (defined with the other entry points).
+int hip_status(hipError_t e, const char *what);
+
+// A block tile: BM x BN outputs, BK-deep K tiles, WM x WN waves, NS stages,
+// PP the alternating schedule (see lowp_accumulate).
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int NS_, bool PP_>
+struct TileShape {
+    static constexpr int BM = BM_, BN = BN_, BK = BK_, WAVES_M = WM_, WAVES_N = WN_, NS = NS_;
+    static constexpr bool PP = PP_;
+    static constexpr int NT = 64 * WM_ * WN_;
+    static constexpr int WM = BM_ / WM_, WN = BN_ / WN_;       // outputs per wave
+    static constexpr int MI = WM / 16, NB = WN / 16;           // 16x16 blocks per wave
+    static constexpr int LDS = NS_ * (BM_ + BN_) * BK_ * 2;
+};
+using Tile32 = TileShape<32, 128, 64, 1, 4, 4, false>;
+using Tile128 = TileShape<128, 128, 64, 2, 4, 4, true>;
+using Tile256 = TileShape<256, 256, 32, 2, 4, 4, true>;
+
+// The operands of one tile's product as lowp_accumulate takes them.
+struct Operands16 {
+    const char *A, *B;
+    long lda, ldb;
+    int M, N, K;
+};
+
+template <class T, bool F16, bool TA, bool TB>
+__device__ __forceinline__ void accumulate16(const Operands16 &q, int m0, int n0, char *lds, f32x4 (&acc)[T::MI][T::NB]) {
+    lowp_accumulate<T::BM, T::BN, T::BK, T::WAVES_M, T::WAVES_N, T::NS, T::PP, true, F16, false, TA, TB>(
+        q, m0, n0, lds, 1, 0, acc);
+}
+
+// Workgroup `bid` of `total`: each of the 8 XCDs, which take workgroups in
+// turn, gets a contiguous run of tiles, so that tiles that share operands
+// share an L2.  A permutation of 0 .. total - 1.
+__device__ __forceinline__ int xcd_run(int bid, int total) {
+    const int per = total >> 3;
+    return bid < (per << 3) ? (bid & 7) * per + (bid >> 3) : bid;
+}
+
+// Tile number `id` of a tiles_m x tiles_n grid, in runs of up to eight tile
+// rows by all tile columns, so that the tiles in flight on an XCD form a
+// compact patch.
+__device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int &tm, int &tn) {
+    constexpr int GM = 8;
+    const int g = id / (GM * tiles_n), in = id - g * GM * tiles_n;
+    const int rows = min(tiles_m - g * GM, GM);
+    tm = g * GM + in % rows;
+    tn = in / rows;
+}
+
+// Four FP32 values rounded to 16 bits (to nearest, ties to even).
+template <bool F16>
+__device__ __forceinline__ i32x2 round16(f32x4 v) {
+    if constexpr (F16) {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(i32x2, __builtin_convertvector(v, h4));
+    } else {
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(i32x2, __builtin_convertvector(v, b4));
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ float widen16(unsigned short bits) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, bits);
+    return __uint_as_float((unsigned)bits << 16);
+}
+
+// Columns col .. col+3 (those below N) of a row of C at `row`, C of FP32 or
+// (OUT16) 16-bit values: v, plus beta times what is there unless beta is 0
+// (then C is not read).  `vec`: 4-element accesses are aligned.
+template <bool F16, bool OUT16>
+__device__ __forceinline__ void store4(char *row, int col, int N, bool vec, float beta, f32x4 v) {
+    if constexpr (OUT16) {
+        unsigned short *dst = reinterpret_cast<unsigned short *>(row) + col;
+        if (beta != 0.f) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (col + r < N) v[r] += beta * widen16<F16>(dst[r]);
+        }
+        const i32x2 o = round16<F16>(v);
+        if (vec && col + 3 < N) {
+            *reinterpret_cast<i32x2 *>(dst) = o;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (col + r < N) dst[r] = (unsigned short)((unsigned)o[r >> 1] >> (16 * (r & 1)));
+        }
+    } else {
+        float *dst = reinterpret_cast<float *>(row) + col;
+        if (vec && col + 3 < N) {
+            if (beta != 0.f) v += *reinterpret_cast<const f32x4 *>(dst) * beta;
+            *reinterpret_cast<f32x4 *>(dst) = v;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (col + r < N) dst[r] = v[r] + (beta != 0.f ? beta * dst[r] : 0.f);
+        }
+    }
+}
+
+// C[rows below M][columns below N] = alpha * acc + beta * C for the tile at
+// (m0, n0): block (mi, nb) of a lane holds row l%16 and columns 4*(l/16)..+3.
+template <class T, bool F16, bool OUT16>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[T::MI][T::NB], int m0, int n0, int M, int N, char *C,
+                                           long ldc, float alpha, float beta) {
+    constexpr int E = OUT16 ? 2 : 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool vec = (reinterpret_cast<uintptr_t>(C) & (4 * E - 1)) == 0 && (ldc & 3) == 0;
+#pragma unroll
+    for (int mi = 0; mi < T::MI; ++mi) {
+        const int row = m0 + (wave / T::WAVES_N) * T::WM + mi * 16 + (lane & 15);
+        if (row >= M) continue;
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) {
+            const int col = n0 + (wave % T::WAVES_N) * T::WN + nb * 16 + 4 * (lane >> 4);
+            store4<F16, OUT16>(C + (long)row * ldc * E, col, N, vec, beta, acc[mi][nb] * alpha);
+        }
+    }
+}
+
+inline long ceil_to(long n, long to) { return (n + to - 1) / to * to; }
+
+// Largest leading dimension of the 16-bit kernels' operands: 256 rows stay
+// within the 31-bit range of a buffer descriptor.
+constexpr int kMaxLd16 = (1 << 22) - 64;
+
+inline bool chunk_rows(const void *p, long ld, long cols) {     // rows of whole 16-byte chunks
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= kMaxLd16;
+}
+
+// dst [copies][rows][cols8] = src [copies][rows][cols] (row length cols8:
+// cols rounded up to whole 16-byte chunks, zeros behind cols); rows from
+// `rows` to `rows_out` are zero.
+hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, int rows_out,
+                    hipStream_t s);
+
+}  // namespace sgemm_mi355x

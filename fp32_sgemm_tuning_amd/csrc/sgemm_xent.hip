@@ -1,0 +1,530 @@
+// The output layer of a language model with its softmax cross entropy:
+// logits l = alpha * X * W^T for rows X [M,K] and a vocabulary W [N,K] in 16
+// bits, lse_i = log(sum_v exp(l_iv)), loss_i = lse_i - l_{i,target_i}, and
+// the gradients of sum(dloss_i * loss_i)
+//
+//   dX = alpha * diag(dloss) * P * W,  dW = alpha * P^T * diag(dloss) * X,
+//   P_iv = exp(l_iv - lse_i) - [v == target_i]
+//
+// without the M x N logits ever being in memory.  Rows whose target is the
+// ignored index take no part: xent_compact_kernel lists the others and, if
+// there is an ignored row, copies them side by side, so no product is spent
+// on them and nothing they hold (NaN, Inf) reaches dW.
+//
+// Forward: each block tile of the logits stays in the accumulators;
+// xent_stats_kernel writes per row the tile's maximum and sum of
+// exp(l - maximum), and xent_join_kernel joins a row's tiles.
+//
+// Backward, for one piece of the vocabulary after the other:
+// xent_dlogits_kernel forms the piece of the logits again and stores
+// P_iv * dloss_i / max|dloss| in 16 bits, then xent_dx_kernel adds its
+// product with the piece of W to an FP32 sum, and xent_dw_kernel writes the
+// piece of dW.  P lies in [-1, 1] and the scaled dloss too, so no 16-bit
+// range is left whatever the loss is scaled by; the factor max|dloss| is put
+// back in FP32.  Rounding this product to the inputs' 16 bits is what lets
+// the two gradient products run on the 16-bit matrix instructions; it is off
+// by at most half a step of each term (bf16 2^-8, fp16 2^-11 relative to
+// the term), the size of the gradients' own final rounding.
+#include <algorithm>
+
+#include "sgemm_tile16.hpp"
+
+namespace sgemm_mi355x {
+
+namespace {
+
+// In the workspace, per call.  `rows`: rows that are not ignored.
+struct XentHead {
+    int rows;
+    float gmax;        // max |dloss| over them; 1 where that is 0 or infinite
+};
+
+struct XentArgs {
+    const char *X, *W;                  // W: padded copy if one is needed
+    long ldx, ldw;
+    int M, N, K;
+    float alpha;
+    const long long *target;
+    long long ignore;
+    XentHead *head;
+    int *map;                           // row of X of each listed row
+    int *label;                         // its target, -1 outside 0 .. N-1
+    char *Xc;                           // the listed rows side by side, K rounded up to whole chunks
+    long ldxc;
+    bool take_x;                        // X can be used in place if no row is ignored
+    float *loss, *lse;
+    // forward
+    float *tlogit;                      // logit of the target, per listed row
+    float2 *part;                       // [tile column][listed row]: maximum, sum
+    // backward
+    const float *lse_in, *dloss;
+    long dloss_stride;
+    float *g, *lsec;                    // dloss / gmax and lse of the listed rows
+    char *dX, *dW, *P;
+    long lddx, lddw, ldp;
+    float *sum;                         // FP32 sum of dX over the pieces
+    int n_first, n_count;               // piece of the vocabulary
+};
+
+__device__ __forceinline__ float max_abs(float a, float b) { return fmaxf(a, fabsf(b)); }
+
+constexpr int kCompactRows = 32;
+
+// Block b lists the rows b * kCompactRows ...: it counts the rows before
+// them itself (a pass over the targets, which stay in L2), so one launch
+// does.  GRAD: also max|dloss|, each listed row's dloss and lse, and zeros
+// in dX for ignored rows; else zeros in loss and lse.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
+    __shared__ int before[4], all[4];
+    __shared__ float big[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int r0 = blockIdx.x * kCompactRows;
+    int nb = 0, na = 0;
+    float gm = 0.f;
+    for (int i = tid; i < p.M; i += 256) {
+        if (p.target[i] == p.ignore) continue;
+        ++na;
+        nb += i < r0;
+        if (GRAD) gm = max_abs(gm, p.dloss[i * p.dloss_stride]);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        nb += __shfl_xor(nb, d);
+        na += __shfl_xor(na, d);
+        gm = fmaxf(gm, __shfl_xor(gm, d));
+    }
+    if (lane == 0) {
+        before[wave] = nb;
+        all[wave] = na;
+        big[wave] = gm;
+    }
+    __syncthreads();
+    nb = before[0] + before[1] + before[2] + before[3];
+    na = all[0] + all[1] + all[2] + all[3];
+    gm = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+    if (!(gm > 0.f && gm < __builtin_inff())) gm = 1.f;
+    if (blockIdx.x == 0 && tid == 0) *p.head = {na, gm};
+    const bool copy = !(p.take_x && na == p.M);
+    // each wave: 8 rows in turn
+    const int mine = r0 + (lane & 31);
+    const long long t = mine < p.M ? p.target[mine] : p.ignore;
+    const unsigned listed = (unsigned)__ballot(t != p.ignore);        // bit r: row r0 + r (lanes 0-31)
+    for (int r = wave; r < kCompactRows && r0 + r < p.M; r += 4) {
+        const int row = r0 + r;
+        if (!(listed >> r & 1)) {
+            if (GRAD) {
+                if (p.dX != nullptr)
+                    for (int k = lane; k < p.K; k += 64)
+                        reinterpret_cast<unsigned short *>(p.dX)[row * p.lddx + k] = 0;
+            } else if (lane == 0) {
+                p.loss[row] = 0.f;
+                p.lse[row] = 0.f;
+            }
+            continue;
+        }
+        const int at = nb + __builtin_popcount(listed & ((1u << r) - 1));
+        if (lane == 0) {
+            const long long v = p.target[row];
+            p.map[at] = row;
+            p.label[at] = v >= 0 && v < p.N ? (int)v : -1;
+            if (GRAD) {
+                const float d = p.dloss[row * p.dloss_stride];
+                // a target outside the vocabulary: NaN, as its loss is
+                p.g[at] = v >= 0 && v < p.N ? d / gm : __builtin_nanf("");
+                p.lsec[at] = p.lse_in[row];
+            } else {
+                p.tlogit[at] = __builtin_nanf("");          // replaced by the tile that holds the target
+            }
+        }
+        if (copy) {
+            const unsigned short *src = reinterpret_cast<const unsigned short *>(p.X) + row * p.ldx;
+            unsigned short *dst = reinterpret_cast<unsigned short *>(p.Xc) + at * p.ldxc;
+            if (p.take_x) {
+                for (int k = 8 * lane; k < p.K; k += 512)
+                    *reinterpret_cast<i32x4 *>(dst + k) = *reinterpret_cast<const i32x4 *>(src + k);
+            } else {
+                for (int k = lane; k < p.ldxc; k += 64) dst[k] = k < p.K ? src[k] : (unsigned short)0;
+            }
+        }
+    }
+}
+
+// The listed rows as an operand: X itself if every row is listed.
+__device__ __forceinline__ void listed_rows(const XentArgs &p, int rows, const char *&X, long &ldx) {
+    const bool in_place = p.take_x && rows == p.M;
+    X = in_place ? p.X : p.Xc;
+    ldx = in_place ? p.ldx : p.ldxc;
+}
+
+// This workgroup's tile of the listed rows x n grid and the logits there
+// (before alpha); false past the last tile.
+template <class T, bool F16>
+__device__ __forceinline__ bool logits_tile(const XentArgs &p, int rows, char *lds, int &m0, int &n0,
+                                            f32x4 (&acc)[T::MI][T::NB]) {
+    const int tiles_m = (rows + T::BM - 1) / T::BM, tiles_n = (p.n_count + T::BN - 1) / T::BN;
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return false;
+    int tm, tn;
+    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    m0 = tm * T::BM;
+    n0 = tn * T::BN;
+    Operands16 q = {nullptr, p.W + 2L * p.n_first * p.ldw, 0, p.ldw, rows, p.n_count, p.K};
+    listed_rows(p, rows, q.A, q.lda);
+    accumulate16<T, F16, false, true>(q, m0, n0, lds, acc);
+    return true;
+}
+
+template <class T, bool F16>
+__global__ void __launch_bounds__(T::NT) xent_stats_kernel(XentArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
+    int m0, n0;
+    f32x4 acc[T::MI][T::NB];
+    if (!logits_tile<T, F16>(p, rows, lds, m0, n0, acc)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+    const int col0 = n0 + wn * T::WN + 4 * (lane >> 4);
+    float2 *red = reinterpret_cast<float2 *>(lds);                  // [WAVES_N][BM]
+    __syncthreads();                                                // the K loop's last LDS reads
+#pragma unroll
+    for (int mi = 0; mi < T::MI; ++mi) {
+        const int r = wm * T::WM + mi * 16 + (lane & 15), row = m0 + r;
+        const int label = row < rows ? p.label[row] : -1;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = col0 + nb * 16 + e;
+                const float l = acc[mi][nb][e] * p.alpha;
+                if (col == label) p.tlogit[row] = l;
+                acc[mi][nb][e] = col < p.N ? l : -__builtin_inff();
+                top = fmaxf(top, acc[mi][nb][e]);
+            }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // (a row of nothing but -inf sums to 0, one with a NaN to NaN)
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += __expf(acc[mi][nb][e] - base);
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (lane < 16) red[wn * T::BM + r] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < T::BM && m0 + r < rows; r += T::NT) {
+        float2 a = red[r];
+#pragma unroll
+        for (int w = 1; w < T::WAVES_N; ++w) {
+            const float2 b = red[w * T::BM + r];
+            const float top = fmaxf(a.x, b.x), base = top == -__builtin_inff() ? 0.f : top;
+            a = make_float2(top, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+        }
+        p.part[(long)(n0 / T::BN) * p.M + m0 + r] = a;
+    }
+}
+
+// Joins the tile columns of 64 rows per block: 16 threads a row take every
+// 16th tile, then a tree of 16.
+__global__ void __launch_bounds__(1024) xent_join_kernel(XentArgs p, int tiles_n) {
+    __shared__ float2 red[16][64];
+    const int r = threadIdx.x & 63, slice = threadIdx.x >> 6, row = blockIdx.x * 64 + r;
+    const bool live = row < p.head->rows;
+    auto join = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x), base = top == -__builtin_inff() ? 0.f : top;
+        return make_float2(top, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+    };
+    float2 a = make_float2(-__builtin_inff(), 0.f);
+    if (live)
+        for (int t = slice; t < tiles_n; t += 16) a = join(a, p.part[(long)t * p.M + row]);
+    red[slice][r] = a;
+    __syncthreads();
+    if (slice != 0 || !live) return;
+    for (int s = 1; s < 16; ++s) a = join(a, red[s][r]);
+    const float lse = a.x + logf(a.y);
+    const int to = p.map[row];
+    p.lse[to] = lse;
+    p.loss[to] = lse - p.tlogit[row];
+}
+
+// P [listed rows][piece of the vocabulary] in 16 bits, zeros behind the
+// vocabulary's end up to whole tiles.
+template <class T, bool F16>
+__global__ void __launch_bounds__(T::NT) xent_dlogits_kernel(XentArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
+    int m0, n0;
+    f32x4 acc[T::MI][T::NB];
+    if (!logits_tile<T, F16>(p, rows, lds, m0, n0, acc)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col0 = n0 + wave % T::WAVES_N * T::WN + 4 * (lane >> 4);
+#pragma unroll
+    for (int mi = 0; mi < T::MI; ++mi) {
+        const int row = m0 + wave / T::WAVES_N * T::WM + mi * 16 + (lane & 15);
+        if (row >= rows) continue;
+        const int label = p.label[row] - p.n_first;
+        const float g = p.g[row], lse = p.lsec[row];
+        char *dst = p.P + 2 * row * p.ldp;
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) {
+            const int col = col0 + nb * 16;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float s = __expf(acc[mi][nb][e] * p.alpha - lse) - (col + e == label ? 1.f : 0.f);
+                // (dloss 0 takes a row out whatever its logits are)
+                v[e] = col + e < p.n_count && g != 0.f ? s * g : 0.f;
+            }
+            *reinterpret_cast<i32x2 *>(dst + 2 * col) = round16<F16>(v);
+        }
+    }
+}
+
+// dX: sum += P * piece of W; the last piece scales, rounds and puts each row
+// in its place.
+template <class T, bool F16>
+__global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, int last) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
+    const int tiles_m = (rows + T::BM - 1) / T::BM, tiles_n = (p.K + T::BN - 1) / T::BN;
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+    int tm, tn;
+    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    const Operands16 q = {p.P, p.W + 2L * p.n_first * p.ldw, p.ldp, p.ldw, rows, p.K, p.n_count};
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, false, false>(q, m0, n0, lds, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const float scale = p.alpha * p.head->gmax;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0;
+#pragma unroll
+    for (int mi = 0; mi < T::MI; ++mi) {
+        const int row = m0 + wave / T::WAVES_N * T::WM + mi * 16 + (lane & 15);
+        if (row >= rows) continue;
+        float *sum = p.sum + row * p.ldxc;                    // whole chunks of columns
+        char *out = p.dX + 2 * p.map[row] * p.lddx;
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) {
+            const int col = n0 + wave % T::WAVES_N * T::WN + nb * 16 + 4 * (lane >> 4);
+            if (col >= p.K) continue;
+            f32x4 v = acc[mi][nb];
+            if (!first) v += *reinterpret_cast<const f32x4 *>(sum + col);
+            if (last) store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
+            else *reinterpret_cast<f32x4 *>(sum + col) = v;
+        }
+    }
+}
+
+// The piece of dW: P^T * X over the listed rows.
+template <class T, bool F16>
+__global__ void __launch_bounds__(T::NT) xent_dw_kernel(XentArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
+    const int tiles_m = (p.n_count + T::BM - 1) / T::BM, tiles_n = (p.K + T::BN - 1) / T::BN;
+    int tm, tn;
+    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    Operands16 q = {p.P, nullptr, p.ldp, 0, p.n_count, p.K, rows};
+    listed_rows(p, rows, q.B, q.ldb);
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, true, false>(q, tm * T::BM, tn * T::BN, lds, acc);
+    store_tile<T, F16, true>(acc, tm * T::BM, tn * T::BN, p.n_count, p.K, p.dW + 2L * p.n_first * p.lddw, p.lddw,
+                             p.alpha * p.head->gmax, 0.f);
+}
+
+// Bytes of P at most, so that it stays in the Infinity Cache between the
+// kernel that writes it and the two that read it.
+constexpr long kPieceBytes = 256L << 20;
+
+long piece_columns(int M, int N) {
+    const long most = std::max(kPieceBytes / 2 / std::max(M, 1) / 256 * 256, 1024L);
+    const long pieces = (N + most - 1) / most;
+    return ceil_to((N + pieces - 1) / pieces, 256);
+}
+
+// The workspace, laid out from `base` (null: only its size is wanted).
+struct Layout {
+    char *base;
+    long at = 0;
+    char *take(long bytes) {
+        char *here = base == nullptr ? nullptr : base + at;
+        at += ceil_to(bytes, 256);
+        return here;
+    }
+};
+
+long xent_layout(XentArgs &p, void *workspace, bool grad, char *&Wc) {
+    Layout l = {static_cast<char *>(workspace)};
+    p.ldxc = ceil_to(p.K, 8);
+    p.take_x = chunk_rows(p.X, p.ldx, p.K);
+    p.head = reinterpret_cast<XentHead *>(l.take(sizeof(XentHead)));
+    p.map = reinterpret_cast<int *>(l.take(4L * p.M));
+    p.label = reinterpret_cast<int *>(l.take(4L * p.M));
+    p.Xc = l.take(2L * p.M * p.ldxc);
+    Wc = chunk_rows(p.W, p.ldw, p.K) ? nullptr : l.take(2L * p.N * p.ldxc);
+    if (!grad) {
+        p.tlogit = reinterpret_cast<float *>(l.take(4L * p.M));
+        p.part = reinterpret_cast<float2 *>(l.take(8L * p.M * ((p.N + 127L) / 128)));
+    } else {
+        p.g = reinterpret_cast<float *>(l.take(4L * p.M));
+        p.lsec = reinterpret_cast<float *>(l.take(4L * p.M));
+        p.ldp = piece_columns(p.M, p.N);
+        p.P = l.take(2L * p.M * p.ldp);
+        p.sum = p.ldp < p.N ? reinterpret_cast<float *>(l.take(4L * p.M * p.ldxc)) : nullptr;
+    }
+    return l.at;
+}
+
+int check(int dtype, int M, int N, int K, int ldx, int ldw) {
+    if (dtype != SGEMM_DTYPE_BF16 && dtype != SGEMM_DTYPE_F16) return SGEMM_STATUS_INVALID_DTYPE;
+    // (the vocabulary must hold a column for the sums to have a term)
+    if (M < 0 || N < 1 || K < 0 || ldx < std::max(K, 1) || ldw < std::max(K, 1) || K > kMaxLd16 ||
+        M > (1 << 30) || N > (1 << 30) || (M + 31L) / 32 * ((N + 127L) / 128) > 0x7fffffffL)
+        return SGEMM_STATUS_INVALID_DIM;
+    return SGEMM_STATUS_OK;
+}
+
+bool scratch_ok(long need, const void *workspace, long long bytes) {
+    return workspace != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(workspace) & 15) == 0;
+}
+
+unsigned tiles(long m, long n, int bm, int bn) { return (unsigned)((m + bm - 1) / bm * ((n + bn - 1) / bn)); }
+
+// The tile of a product of at most m rows: few rows take the tile that
+// wastes least, many the one that reads least.
+int tile_of(long m, long n) { return m <= 32 ? 0 : tiles(m, n, 256, 256) >= 256 ? 2 : 1; }
+
+#define XENT_LAUNCH(KERNEL, T, GRID, ...) \
+    (f16 ? launch_k(KERNEL<T, true>, dim3(GRID), dim3(T::NT), s, __VA_ARGS__) \
+         : launch_k(KERNEL<T, false>, dim3(GRID), dim3(T::NT), s, __VA_ARGS__))
+
+}  // namespace
+}  // namespace sgemm_mi355x
+
+using namespace sgemm_mi355x;
+
+extern "C" {
+
+long long sgemm_lowp_xent_workspace(int M, int N, int K, const void *X, int ldx, const void *W, int ldw, int grad) {
+    const int st = check(SGEMM_DTYPE_BF16, M, N, K, ldx, ldw);
+    if (st != SGEMM_STATUS_OK) return st;
+    XentArgs p = {};
+    p.X = static_cast<const char *>(X);
+    p.W = static_cast<const char *>(W);
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    char *Wc;
+    return M == 0 && !grad ? 0 : xent_layout(p, nullptr, grad != 0, Wc);
+}
+
+int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha, const void *X, int ldx, const void *W, int ldw,
+                    const long long *target, long long ignore_index, float *loss, float *lse, void *workspace,
+                    long long workspace_bytes, void *stream) {
+    const int st = check(dtype, M, N, K, ldx, ldw);
+    if (st != SGEMM_STATUS_OK) return st;
+    if (M == 0) return SGEMM_STATUS_OK;
+    if (target == nullptr || loss == nullptr || lse == nullptr || (K > 0 && (X == nullptr || W == nullptr)))
+        return SGEMM_STATUS_NULL_POINTER;
+    XentArgs p = {};
+    p.X = static_cast<const char *>(X);
+    p.W = static_cast<const char *>(W);
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.M = M;
+    p.N = p.n_count = N;
+    p.K = K;
+    p.alpha = alpha;
+    p.target = target;
+    p.ignore = ignore_index;
+    p.loss = loss;
+    p.lse = lse;
+    char *Wc;
+    if (!scratch_ok(xent_layout(p, nullptr, false, Wc), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
+    xent_layout(p, workspace, false, Wc);
+    const bool f16 = dtype == SGEMM_DTYPE_F16;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = launch_k(xent_compact_kernel<false>, dim3((M + kCompactRows - 1) / kCompactRows), dim3(256), s, p);
+    if (e == hipSuccess && Wc != nullptr) {
+        e = pad_rows(W, ldw, 0, 1, N, K, Wc, N, s);
+        p.W = Wc;
+        p.ldw = p.ldxc;
+    }
+    const int tile = tile_of(M, N);
+    if (e == hipSuccess)
+        e = tile == 0   ? XENT_LAUNCH(xent_stats_kernel, Tile32, tiles(M, N, 32, 128), p)
+            : tile == 1 ? XENT_LAUNCH(xent_stats_kernel, Tile128, tiles(M, N, 128, 128), p)
+                        : XENT_LAUNCH(xent_stats_kernel, Tile256, tiles(M, N, 256, 256), p);
+    if (e == hipSuccess)
+        e = launch_k(xent_join_kernel, dim3((M + 63) / 64), dim3(1024), s, p, (N + (tile == 2 ? 255 : 127)) / (tile == 2 ? 256 : 128));
+    return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
+}
+
+int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void *X, int ldx, const void *W, int ldw,
+                         const long long *target, long long ignore_index, const float *lse, const float *dloss,
+                         int dloss_stride, void *dX, int lddx, void *dW, int lddw, void *workspace,
+                         long long workspace_bytes, void *stream) {
+    const int st = check(dtype, M, N, K, ldx, ldw);
+    if (st != SGEMM_STATUS_OK) return st;
+    if (dloss_stride < 0 || (dX != nullptr && lddx < std::max(K, 1)) || (dW != nullptr && lddw < std::max(K, 1)))
+        return SGEMM_STATUS_INVALID_DIM;
+    if (K == 0 || (dX == nullptr && dW == nullptr) || (M == 0 && dW == nullptr)) return SGEMM_STATUS_OK;
+    if (W == nullptr || (M > 0 && (X == nullptr || target == nullptr || lse == nullptr || dloss == nullptr)))
+        return SGEMM_STATUS_NULL_POINTER;
+    XentArgs p = {};
+    p.X = static_cast<const char *>(X);
+    p.W = static_cast<const char *>(W);
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.alpha = alpha;
+    p.target = target;
+    p.ignore = ignore_index;
+    p.lse_in = lse;
+    p.dloss = dloss;
+    p.dloss_stride = dloss_stride;
+    p.dX = static_cast<char *>(dX);
+    p.dW = static_cast<char *>(dW);
+    p.lddx = lddx;
+    p.lddw = lddw;
+    char *Wc;
+    if (!scratch_ok(xent_layout(p, nullptr, true, Wc), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
+    xent_layout(p, workspace, true, Wc);
+    const bool f16 = dtype == SGEMM_DTYPE_F16;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    // (M == 0: one block, which finds no row; dW is then zeros)
+    hipError_t e = launch_k(xent_compact_kernel<true>, dim3(std::max((M + kCompactRows - 1) / kCompactRows, 1)), dim3(256), s, p);
+    if (e == hipSuccess && Wc != nullptr) {
+        e = pad_rows(W, ldw, 0, 1, N, K, Wc, N, s);
+        p.W = Wc;
+        p.ldw = p.ldxc;
+    }
+    for (p.n_first = 0; p.n_first < N && e == hipSuccess; p.n_first += (int)p.ldp) {
+        p.n_count = (int)std::min((long)N - p.n_first, p.ldp);
+        const int first = p.n_first == 0, last = p.n_first + p.n_count == N;
+        if (M > 0) {
+            const int tile = tile_of(M, p.n_count);
+            e = tile == 0   ? XENT_LAUNCH(xent_dlogits_kernel, Tile32, tiles(M, p.n_count, 32, 128), p)
+                : tile == 1 ? XENT_LAUNCH(xent_dlogits_kernel, Tile128, tiles(M, p.n_count, 128, 128), p)
+                            : XENT_LAUNCH(xent_dlogits_kernel, Tile256, tiles(M, p.n_count, 256, 256), p);
+        }
+        if (e == hipSuccess && M > 0 && dX != nullptr) {
+            const int tile = tile_of(M, K);
+            e = tile == 0   ? XENT_LAUNCH(xent_dx_kernel, Tile32, tiles(M, K, 32, 128), p, first, last)
+                : tile == 1 ? XENT_LAUNCH(xent_dx_kernel, Tile128, tiles(M, K, 128, 128), p, first, last)
+                            : XENT_LAUNCH(xent_dx_kernel, Tile256, tiles(M, K, 256, 256), p, first, last);
+        }
+        if (e == hipSuccess && dW != nullptr)
+            e = tile_of(p.n_count, K) == 2 ? XENT_LAUNCH(xent_dw_kernel, Tile256, tiles(p.n_count, K, 256, 256), p)
+                                           : XENT_LAUNCH(xent_dw_kernel, Tile128, tiles(p.n_count, K, 128, 128), p);
+    }
+    return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
+}
+
+}  // extern "C"

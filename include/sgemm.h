@@ -80,11 +80,11 @@ extern "C" {
 #define SGEMM_STATUS_NULL_POINTER (-2)      /* NULL A, B or C with a non-empty extent */
 #define SGEMM_STATUS_HIP_ERROR (-3)         /* the HIP runtime reported an error; see sgemm_last_hip_error() */
 #define SGEMM_STATUS_INVALID_VARIANT (-4)   /* sgemm_ex: no such variant */
-#define SGEMM_STATUS_UNSUPPORTED (-5)       /* sgemm_ex: variant needs 16-byte alignment the arguments lack */
+#define SGEMM_STATUS_UNSUPPORTED (-5)       /* a forced variant, or a packed weight, needs 16-byte alignment */
 #define SGEMM_STATUS_INVALID_OP (-6)        /* an operation code other than SGEMM_OP_N / SGEMM_OP_T */
 
-#define SGEMM_STATUS_INVALID_DTYPE (-7)     /* sgemm_lowp: an input type other than SGEMM_DTYPE_BF16 / _F16 */
-#define SGEMM_STATUS_SCRATCH_TOO_SMALL (-8) /* sgemm_noalloc: the split of K needs more than its scratch */
+#define SGEMM_STATUS_INVALID_DTYPE (-7)     /* an element type the call does not take */
+#define SGEMM_STATUS_SCRATCH_TOO_SMALL (-8) /* the call needs more scratch or workspace than it has */
 
 /* Device memory the library keeps between calls (see "Workspace" above). */
 #define SGEMM_WORKSPACE_BYTES (64ll * 1024 * 1024 + 16 * 1024)  /* one split-K workspace */
@@ -93,9 +93,10 @@ extern "C" {
 #define SGEMM_MAX_COPY_BUFFER_BYTES (4ll << 30)  /* largest copy buffer; larger copies are not made */
 #define SGEMM_NOALLOC_SCRATCH_BYTES (64ll * 1024 * 1024 + 16 * 1024)  /* sgemm_noalloc's static scratch, per device */
 
-/* Input element types of sgemm_lowp. */
+/* Element types of sgemm_lowp and the calls below it. */
 #define SGEMM_DTYPE_BF16 1                  /* bfloat16: 1 sign, 8 exponent, 7 fraction bits */
 #define SGEMM_DTYPE_F16 2                   /* IEEE binary16 */
+#define SGEMM_DTYPE_F32 3                   /* IEEE binary32: result type of the grouped and 4-bit products */
 
 /* Operation codes of the sgemm_op family. */
 #define SGEMM_OP_N 0                        /* use the stored matrix as is */
@@ -369,6 +370,132 @@ int sgemm_lowp_strided_batched(int dtype, int op_a, int op_b, int M, int N, int 
                                const void *B, int ldb, long long stride_b,
                                float beta, float *C, int ldc, long long stride_c,
                                int batch, void *stream);
+
+/*
+ * Products of a language model's weights that a plain product cannot express.
+ * All take BF16 or FP16 operands (`dtype`) with FP32 accumulation, run on
+ * `stream` without synchronising, keep nothing between calls and allocate
+ * nothing: where a call needs device memory of its own the caller passes a
+ * 16-byte aligned `workspace` of at least the bytes that the matching
+ * *_workspace() function returns for the same arguments (it looks at pointers
+ * for their alignment only; 0: pass NULL).  A workspace is free again when
+ * the call's work on the stream is done; two calls that may run at the same
+ * time, or two captured graphs that may, need one each.  So every call can be
+ * captured into a graph.  Results are deterministic.  C must not overlap an
+ * operand or the workspace.  Leading dimensions and strides count elements.
+ * SGEMM_STATUS_SCRATCH_TOO_SMALL: the workspace is missing, unaligned or too
+ * small.
+ *
+ * sgemm_lowp_grouped: rows offsets[g] .. offsets[g+1] - 1 of A [M,K] and of
+ * C [M,N] belong to group g, whose matrix is op(B) with B at
+ * B + g*stride_b, op as in sgemm_lowp_op():
+ *   C[rows of g] = alpha * A[rows of g] * op(B[g]) + beta * C[rows of g].
+ * `offsets` is a device array of groups + 1 row numbers that do not decrease,
+ * within 0 .. M (others are clamped to that range, and rows that two groups
+ * then claim hold either's result).  Groups may be empty; rows of no group
+ * are left as they were.  dtype_c: `dtype` or SGEMM_DTYPE_F32.  The gradient
+ * with respect to A is the same call with op_b turned round, the one with
+ * respect to B sgemm_lowp_grouped_wgrad.  K and N below 2^22 - 64, groups up
+ * to 65535.  Operands whose rows are not whole aligned 16-byte chunks
+ * (pointer, leading dimension, row length and stride_b multiples of 8
+ * elements) are first copied into zero-padded rows in the workspace.
+ */
+int sgemm_lowp_grouped(int dtype, int op_b, int groups, int M, int N, int K, float alpha,
+                       const void *A, int lda,
+                       const void *B, int ldb, long long stride_b,
+                       const int *offsets, float beta, void *C, int ldc, int dtype_c,
+                       void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_lowp_grouped_workspace(int op_b, int groups, int M, int N, int K,
+                                       const void *A, int lda,
+                                       const void *B, int ldb, long long stride_b);
+
+/*
+ * sgemm_lowp_grouped_wgrad: one product per group over the group's rows,
+ *   C[g] = alpha * A[rows of g]^T * D[rows of g] + beta * C[g],
+ * A [M,K], D [M,N], C[g] K x N at C + g*stride_c (stride_c >=
+ * (K-1)*ldc + N when groups > 1).  An empty group gives beta * C[g]
+ * (zeros when beta is 0).  Otherwise as sgemm_lowp_grouped().
+ */
+int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float alpha,
+                             const void *A, int lda, const void *D, int ldd,
+                             const int *offsets, float beta, void *C, int ldc,
+                             long long stride_c, int dtype_c,
+                             void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_lowp_grouped_wgrad_workspace(int M, int N, int K, const void *A, int lda,
+                                             const void *D, int ldd);
+
+/*
+ * sgemm_lowp_xent: the softmax cross entropy of the logits
+ * l = alpha * X * W^T, X [M,K] rows, W [N,K] a vocabulary of N >= 1:
+ *   lse[i] = log(sum_v exp(l[i][v])),  loss[i] = lse[i] - l[i][target[i]],
+ * both FP32, without the M x N logits being in memory.  Rows with
+ * target[i] == ignore_index give 0 in both, whatever X holds there; any other
+ * target outside 0 .. N-1 gives a NaN loss.  K below 2^22 - 64, M and N up to
+ * 2^30.
+ */
+int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha,
+                    const void *X, int ldx, const void *W, int ldw,
+                    const long long *target, long long ignore_index,
+                    float *loss, float *lse,
+                    void *workspace, long long workspace_bytes, void *stream);
+
+/*
+ * sgemm_lowp_xent_grad: the gradients of sum_i dloss[i] * loss[i],
+ *   dX = alpha * diag(dloss) * P * W,  dW = alpha * P^T * diag(dloss) * X,
+ *   P[i][v] = exp(l[i][v] - lse[i]) - [v == target[i]],
+ * with lse from sgemm_lowp_xent() on the same arguments; dX [M,K] and dW
+ * [N,K] are of `dtype`, and either may be NULL if it is not wanted.  dloss[i]
+ * is at dloss + i*dloss_stride (0: one value for all rows).  Ignored rows
+ * give zeros in dX and nothing to dW; rows with a target outside 0 .. N-1
+ * (and not ignored) give NaN.  The logits are formed again, a piece of the
+ * vocabulary at a time, with P * dloss / max|dloss| of that piece in 16 bits
+ * in the workspace.
+ */
+int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha,
+                         const void *X, int ldx, const void *W, int ldw,
+                         const long long *target, long long ignore_index,
+                         const float *lse, const float *dloss, int dloss_stride,
+                         void *dX, int lddx, void *dW, int lddw,
+                         void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_lowp_xent_workspace(int M, int N, int K, const void *X, int ldx,
+                                    const void *W, int ldw, int grad);
+
+/*
+ * sgemm_w4: C = alpha * X * Wq^T + beta * C, X [M,K] of `dtype`, C [M,N] of
+ * `dtype` or SGEMM_DTYPE_F32 (dtype_c), and a weight of 4-bit values,
+ *   Wq[n][k] = (q[n][k] - z[n][k / group]) * s[n][k / group],
+ * group 32, 64 or 128, the products and sums of unrounded weights in FP32.
+ * With Kp = K rounded up to a multiple of 128:
+ *   packed  N rows of Kp / 2 bytes, 16-byte aligned, 64 bytes per 128 k: the
+ *           32-bit word 4*j + s of a chunk (j, s = 0 .. 3) holds
+ *           k = 32*s + 8*j .. + 7 of it, element 2i in bits 4i .. 4i+3 and
+ *           element 2i+1 in bits 16+4i .. 16+4i+3; what it holds for k >= K
+ *           is not used
+ *   scales  N rows of Kp / group values of `dtype`, 2-byte aligned
+ *   zeros   N rows of Kp / group bytes 0 .. 15, or NULL (every z is 8)
+ * No workspace.
+ */
+int sgemm_w4(int dtype, int M, int N, int K, float alpha,
+             const void *X, int ldx,
+             const void *packed, const void *scales, const void *zeros, int group,
+             float beta, void *C, int ldc, int dtype_c, void *stream);
+
+/*
+ * sgemm_w4_quantize: W [N,K] of `dtype` into the form above (zeros NULL:
+ * without zero points).  s is rounded to `dtype` first and q chosen for the
+ * rounded s, halves to even:
+ *   without  s = max|w| / 7,                       q = round(w / s) + 8
+ *   with     s = (max(w, 0) - min(w, 0)) / 15,     z = round(-min(w, 0) / s),
+ *            q = round(w / s) + z
+ * over the group's k < K, z and q clamped to 0 .. 15; where s is 0, z is 0
+ * (with) and q = z.  A group holding a NaN or an infinity gets s NaN.
+ * sgemm_w4_dequantize: W = (q - z) * s, rounded to `dtype`.
+ */
+int sgemm_w4_quantize(int dtype, int N, int K, const void *W, int ldw, int group,
+                      void *packed, void *scales, void *zeros, void *stream);
+int sgemm_w4_dequantize(int dtype, int N, int K,
+                        const void *packed, const void *scales, const void *zeros, int group,
+                        void *W, int ldw, void *stream);
 
 /* The variant sgemm_lowp() would run for these arguments (no launch; the
  * pointers are only inspected for alignment), or SGEMM_STATUS_INVALID_DIM.
