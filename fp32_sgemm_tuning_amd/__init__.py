@@ -443,8 +443,9 @@ class W4Weight(NamedTuple):
     With Kp = K rounded up to 128: packed uint8 [N, Kp/2] (16-byte aligned;
     64 bytes hold 128 k as 32-bit words, word 4j + s of them k = 32s + 8j..+7,
     element 2i in bits 4i..4i+3, element 2i+1 in bits 16+4i..16+4i+3), scales
-    [N, Kp/group] of the inputs' type, zeros uint8 [N, Kp/group] with values
-    0..15, or None (every z is 8); all contiguous."""
+    [N, Kp/group] of the inputs' type (8-byte aligned), zeros uint8
+    [N, Kp/group] with values 0..15 (4-byte aligned), or None (every z is 8);
+    all contiguous."""
     packed: "torch.Tensor"              # noqa: F821
     scales: "torch.Tensor"              # noqa: F821
     zeros: "Optional[torch.Tensor]"     # noqa: F821
@@ -495,9 +496,10 @@ def sgemm_w4(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     with _on(device, stream) as h:
         C = _result(C, (M, N), out_dtype, torch.float32, (torch.float32, X.dtype), beta, device)
         ldc = _ld(C, "C", (C.dtype,))
+        keep, ws, size = _workspace(capi.sgemm_w4_workspace(M, K, X.data_ptr(), ldx), device)
         _check(capi.sgemm_w4(_codes()[X.dtype], M, N, K, float(alpha), X.data_ptr(), ldx, W.packed.data_ptr(),
                              W.scales.data_ptr(), _address(W.zeros), W.group, float(beta), C.data_ptr(), ldc,
-                             _codes()[C.dtype], h))
+                             _codes()[C.dtype], ws, size, h))
     return C
 
 

@@ -48,12 +48,15 @@ __device__ __forceinline__ int q_pair(unsigned w) {
     return (int)((v & (F16 ? 0x03C003C0u : 0x00780078u)) | (F16 ? 0x4C004C00u : 0x41804180u));
 }
 
-// MB blocks of 16 rows of X by 16 rows of W per workgroup; its NW waves
-// share the chunks and add up through LDS.  GROUP: k per scale.  XVEC: rows
-// of X are whole aligned 16-byte chunks.
-template <int MB, int NW, int GROUP, bool ZEROS, bool F16, bool OUT16, bool XVEC>
-__global__ void __launch_bounds__(64 * NW) w4_kernel(W4Args p) {
+// Few rows of X: MB blocks of 16 of them by 16 rows of W per workgroup, whose
+// NW waves take consecutive runs of chunks and add up through LDS.  Bound by
+// the weights' bytes if enough of them are in flight, so a wave starts the
+// loads of U chunks (weights, scales, zero points, X) before it uses the
+// first.  GROUP: k per scale.
+template <int MB, int NW, int GROUP, bool ZEROS, bool F16, bool OUT16>
+__global__ void __launch_bounds__(64 * NW) w4_rows_kernel(W4Args p) {
     constexpr int GPC = kChunk / GROUP, SPG = 4 / GPC;      // groups per chunk, k steps per group
+    constexpr int U = MB == 1 ? 4 : MB == 2 ? 2 : 1;
     __shared__ f32x4 part[NW][MB][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, lg = lane >> 4;
@@ -65,38 +68,57 @@ __global__ void __launch_bounds__(64 * NW) w4_kernel(W4Args p) {
     const unsigned short *xrow[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
-        xrow[b] = reinterpret_cast<const unsigned short *>(p.X) + (long)min(m0 + 16 * b + lr, p.M - 1) * p.ldx;
+        xrow[b] = reinterpret_cast<const unsigned short *>(p.X) + (long)min(m0 + 16 * b + lr, p.M - 1) * p.ldx + 8 * lg;
     const int one = F16 ? 0x3C003C00 : 0x3F803F80;
     const i32x4 ones = {one, one, one, one};
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     f32x4 total[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) total[b] = zero;
-    for (int c = wave; c < p.chunks; c += NW) {
-        const i32x4 w = *reinterpret_cast<const i32x4 *>(wrow + (long)c * 64);
-        f32x4 sum[MB], sx[MB];
+    const int last = (int)((long)p.chunks * (wave + 1) / NW);
+    for (int c0 = (int)((long)p.chunks * wave / NW); c0 < last; c0 += U) {
+        i32x4 w[U], x[U][4][MB];
+        unsigned long sc[U];
+        unsigned zp[U];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = c * kChunk + 32 * s + 8 * lg;
-            const i32x4 wf = {q_pair<F16, 0>(w[s]), q_pair<F16, 1>(w[s]), q_pair<F16, 2>(w[s]), q_pair<F16, 3>(w[s])};
+        for (int t = 0; t < U; ++t) {
+            const int c = min(c0 + t, last - 1);
+            w[t] = *reinterpret_cast<const i32x4 *>(wrow + (long)c * 64);
+            if constexpr (GPC == 4) sc[t] = *reinterpret_cast<const unsigned long *>(srow + (long)c * GPC);
+            else if constexpr (GPC == 2) sc[t] = *reinterpret_cast<const unsigned *>(srow + (long)c * GPC);
+            else sc[t] = srow[c];
+            if constexpr (ZEROS && GPC == 4) zp[t] = *reinterpret_cast<const unsigned *>(zrow + (long)c * GPC);
+            else if constexpr (ZEROS && GPC == 2) zp[t] = *reinterpret_cast<const unsigned short *>(zrow + (long)c * GPC);
+            else zp[t] = ZEROS ? zrow[c] : 0x08080808u;
 #pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                i32x4 xf = {0, 0, 0, 0};
-                if constexpr (XVEC) {
-                    if (k < p.K) xf = *reinterpret_cast<const i32x4 *>(xrow[b] + k);
-                } else {
+            for (int s = 0; s < 4; ++s) {
+                const int k = c * kChunk + 32 * s;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (k + e < p.K) xf[e >> 1] |= (int)xrow[b][k + e] << (16 * (e & 1));
+                for (int b = 0; b < MB; ++b) {
+                    // (chunks of X behind K are zeros: K is a multiple of 8 here)
+                    x[t][s][b] = i32x4{0, 0, 0, 0};
+                    if (k + 8 * lg < p.K && c0 + t < last) x[t][s][b] = *reinterpret_cast<const i32x4 *>(xrow[b] + k);
                 }
-                sum[b] = mfma_16x16x32<F16>(xf, wf, s % SPG == 0 ? zero : sum[b]);
-                sx[b] = mfma_16x16x32<F16>(xf, ones, s % SPG == 0 ? zero : sx[b]);
             }
-            if (s % SPG == SPG - 1) {
-                const int g = c * GPC + s / SPG;
-                const float scale = widen16<F16>(srow[g]), z = ZEROS ? 16.f + (float)zrow[g] : 24.f;
+        }
 #pragma unroll
-                for (int b = 0; b < MB; ++b) total[b] += (sum[b] - sx[b] * z) * scale;
+        for (int t = 0; t < U; ++t) {
+            f32x4 sum[MB], sx[MB];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const unsigned v = w[t][s];
+                const i32x4 wf = {q_pair<F16, 0>(v), q_pair<F16, 1>(v), q_pair<F16, 2>(v), q_pair<F16, 3>(v)};
+#pragma unroll
+                for (int b = 0; b < MB; ++b) {
+                    sum[b] = mfma_16x16x32<F16>(x[t][s][b], wf, s % SPG == 0 ? zero : sum[b]);
+                    sx[b] = mfma_16x16x32<F16>(x[t][s][b], ones, s % SPG == 0 ? zero : sx[b]);
+                }
+                if (s % SPG == SPG - 1) {
+                    const float scale = widen16<F16>((unsigned short)(sc[t] >> (16 * (s / SPG))));
+                    const float z = 16.f + (float)(zp[t] >> (8 * (s / SPG)) & 255);
+#pragma unroll
+                    for (int b = 0; b < MB; ++b) total[b] += (sum[b] - sx[b] * z) * scale;
+                }
             }
         }
     }
@@ -126,6 +148,172 @@ __global__ void __launch_bounds__(64 * NW) w4_kernel(W4Args p) {
                 *dst = p.beta != 0.f ? o + p.beta * *dst : o;
             }
         }
+    }
+}
+
+// The eight values q - z of a word, exactly, as four registers of pairs;
+// zs: 16 + z (fp16: twice in 16 bits; bf16: z in FP32).
+template <bool F16>
+__device__ __forceinline__ i32x4 centred(unsigned w, unsigned zs) {
+    if constexpr (F16) {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        const h2 z = __builtin_bit_cast(h2, zs);
+        return i32x4{__builtin_bit_cast(int, __builtin_bit_cast(h2, q_pair<true, 0>(w)) - z),
+                     __builtin_bit_cast(int, __builtin_bit_cast(h2, q_pair<true, 1>(w)) - z),
+                     __builtin_bit_cast(int, __builtin_bit_cast(h2, q_pair<true, 2>(w)) - z),
+                     __builtin_bit_cast(int, __builtin_bit_cast(h2, q_pair<true, 3>(w)) - z)};
+    } else {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const float z = __uint_as_float(zs);
+        // bytes 0..3 of `even` are nibbles 0, 2, 4, 6, of `odd` 1, 3, 5, 7
+        const unsigned even = w & 0x0F0F0F0Fu, odd = w >> 4 & 0x0F0F0F0Fu;
+        auto pair = [&](unsigned v, int lo) {
+            const f2 f = {(float)(v >> (8 * lo) & 255) - z, (float)(v >> (8 * lo + 16) & 255) - z};
+            return __builtin_bit_cast(int, __builtin_convertvector(f, b2));
+        };
+        return i32x4{pair(even, 0), pair(odd, 0), pair(even, 1), pair(odd, 1)};
+    }
+}
+
+// Many rows of X: a workgroup of WM x WN waves takes 16*MI*WM rows of X by
+// 16*NB*WN rows of W.  X comes through LDS (direct loads of one 128-k chunk,
+// two stages, rows of 256 bytes in the layout ALayout<64>); the weights go
+// from memory straight into the registers of the one wave column that needs
+// them, which takes half of the LDS traffic of a plain product away.  q - z is
+// exact in 16 bits; two k steps of a group are summed by the matrix
+// instructions and then added to the FP32 total with the group's scale, one
+// multiply-add per output and 64 k (32 for groups of 32): what bounds it next
+// to the matrix instructions.  The product is formed transposed, as in
+// sgemm_lowp.hpp: lane l holds row l%16 and columns 4*(l/16) .. +3.
+template <int MI, int NB, int WM, int WN, int GROUP, bool ZEROS, bool F16, bool OUT16>
+__global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
+    constexpr int GPC = kChunk / GROUP, SPG = GROUP == 32 ? 1 : 2, PARTS = 4 / SPG;
+    constexpr int NWAVES = WM * WN, BM = 16 * MI * WM, BN = 16 * NB * WN;
+    constexpr int STAGE = BM * 256, L = STAGE / 16 / (64 * NWAVES);
+    using AL = ALayout<64>;
+    __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int wm = wave / WN, wn = wave % WN;
+    int tm, tn;
+    const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    // direct loads: load i of a wave fills four rows of a stage, 16-byte chunk
+    // c8 / 8 of them in this lane (the layout's swizzle, the same for every i)
+    const int row0 = 4 * wave + lg, c8 = 8 * (lr ^ (row0 & 15)), rows = min(BM, p.M - m0);
+    const unsigned off0 = 2u * (unsigned)(row0 * (int)p.ldx + c8), step = 2u * 4 * NWAVES * (unsigned)p.ldx;
+    static_assert(4 * NWAVES % 16 == 0, "one swizzle for all loads");
+    const int range = (int)(2 * ((rows - 1) * p.ldx + kChunk));
+    const char *corner = p.X + 2L * m0 * p.ldx;
+    const unsigned lds0 = (unsigned)reinterpret_cast<uintptr_t>((lds_addr_t)lds);
+    auto load_x = [&](int c, int st) {
+        const bool inside = c * kChunk + c8 < p.K;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            dma16_lowp(corner + 2L * c * kChunk, range, lds0 + st * STAGE + (i * NWAVES + wave) * 1024,
+                       (int)(inside && row0 + 4 * NWAVES * i < rows ? off0 + i * step : kOutOfRange));
+    };
+    // lane (lr, lg) loads for its row of W; the scale of the four columns that
+    // a lane's results stand in comes from the lanes that hold them
+    const unsigned char *wtile = p.packed + (long)n0 * p.chunks * 64, *ztile = ZEROS ? p.zeros + (long)n0 * p.chunks * GPC : nullptr;
+    const unsigned short *stile = p.scales + (long)n0 * p.chunks * GPC;
+    unsigned first[NB];                                     // first chunk of the lane's rows, from n0 on
+#pragma unroll
+    for (int b = 0; b < NB; ++b) first[b] = (unsigned)(min(16 * (wn * NB + b) + lr, p.N - 1 - n0) * p.chunks);
+    using Scales = typename std::conditional<GPC == 4, unsigned long, unsigned>::type;
+    i32x4 w[NB];
+    Scales sc[NB];
+    unsigned zp[NB];
+    auto load_w = [&](int c) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const unsigned at = first[b] + c;
+            w[b] = *reinterpret_cast<const i32x4 *>(wtile + (at * 64 + 16 * lg));
+            if constexpr (GPC > 1) sc[b] = *reinterpret_cast<const Scales *>(stile + at * GPC);
+            else sc[b] = stile[at];
+            if constexpr (ZEROS && GPC == 4) zp[b] = *reinterpret_cast<const unsigned *>(ztile + at * GPC);
+            else if constexpr (ZEROS && GPC == 2) zp[b] = *reinterpret_cast<const unsigned short *>(ztile + at * GPC);
+            else zp[b] = ZEROS ? ztile[at] : 0x08080808u;
+        }
+    };
+    f32x4 total[MI][NB];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) total[mi][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (p.chunks > 0) {
+        load_x(0, 0);
+        load_w(0);
+    }
+    for (int c = 0; c < p.chunks; ++c) {
+        // this wave's loads of chunk c have landed, then everyone's; and
+        // everyone has read the other stage
+        wait_vm_lgkm0<0>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        i32x4 cw[NB];
+        Scales cs[NB];
+        unsigned cz[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            cw[b] = w[b];
+            cs[b] = sc[b];
+            cz[b] = zp[b];
+        }
+        if (c + 1 < p.chunks) {
+            load_x(c + 1, (c + 1) & 1);
+            load_w(c + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const char *stage = lds + (c & 1) * STAGE;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+            const int g = h * GPC / PARTS;                  // group of these k steps
+            i32x4 wf[SPG][NB];
+            f32x4 scale[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const unsigned z = cz[b] >> (8 * g) & 255;
+                unsigned zs;
+                if constexpr (F16) {
+                    zs = (0x4C00u + (z << 6)) * 0x10001u;   // 16 + z twice
+                } else {
+                    zs = __float_as_uint((float)z);
+                }
+#pragma unroll
+                for (int s = 0; s < SPG; ++s) wf[s][b] = centred<F16>(cw[b][h * SPG + s], zs);
+                const float mine = widen16<F16>((unsigned short)(cs[b] >> (16 * g)));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) scale[b][r] = __shfl(mine, 4 * lg + r);
+            }
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+                f32x4 sum[NB];
+#pragma unroll
+                for (int s = 0; s < SPG; ++s) {
+                    const int m = (wm * MI + mi) * 16 + lr;
+                    const i32x4 x = *reinterpret_cast<const i32x4 *>(stage + 4 * AL::offset(m, 4 * (h * SPG + s) + lg));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        sum[b] = mfma_16x16x32<F16>(wf[s][b], x, s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[b]);
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) total[mi][b] += sum[b] * scale[b];
+            }
+        }
+    }
+    constexpr int E = OUT16 ? 2 : 4;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.C) & (4 * E - 1)) == 0 && (p.ldc & 3) == 0;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+        const int row = m0 + (wm * MI + mi) * 16 + lr;
+        if (row >= p.M) continue;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            store4<F16, OUT16>(p.C + (long)row * p.ldc * E, n0 + (wn * NB + b) * 16 + 4 * lg, p.N, vec, p.beta,
+                               total[mi][b] * p.alpha);
     }
 }
 
@@ -260,22 +448,40 @@ hipError_t with_form(int group, bool zeros, bool f16, F &&f) {
 }
 
 template <int MB, int NW>
-hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, bool xvec, hipStream_t s) {
+hipError_t launch_rows(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
     const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.M + 16 * MB - 1) / (16 * MB))), block(64 * NW);
     return with_form(group, p.zeros != nullptr, f16, [&](auto g, auto z, auto f) {
         constexpr int G = decltype(g)::value;
         constexpr bool Z = decltype(z)::value, F = decltype(f)::value;
-        if (out16) return xvec ? launch_k(w4_kernel<MB, NW, G, Z, F, true, true>, grid, block, s, p)
-                               : launch_k(w4_kernel<MB, NW, G, Z, F, true, false>, grid, block, s, p);
-        return xvec ? launch_k(w4_kernel<MB, NW, G, Z, F, false, true>, grid, block, s, p)
-                    : launch_k(w4_kernel<MB, NW, G, Z, F, false, false>, grid, block, s, p);
+        return out16 ? launch_k(w4_rows_kernel<MB, NW, G, Z, F, true>, grid, block, s, p)
+                     : launch_k(w4_rows_kernel<MB, NW, G, Z, F, false>, grid, block, s, p);
+    });
+}
+
+template <int MI, int NB, int WM, int WN>
+hipError_t launch_tile(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
+    constexpr int BM = 16 * MI * WM, BN = 16 * NB * WN;
+    const dim3 grid((unsigned)(((p.M + BM - 1L) / BM) * ((p.N + BN - 1) / BN))), block(64 * WM * WN);
+    return with_form(group, p.zeros != nullptr, f16, [&](auto g, auto z, auto f) {
+        constexpr int G = decltype(g)::value;
+        constexpr bool Z = decltype(z)::value, F = decltype(f)::value;
+        return out16 ? launch_k(w4_tile_kernel<MI, NB, WM, WN, G, Z, F, true>, grid, block, s, p)
+                     : launch_k(w4_tile_kernel<MI, NB, WM, WN, G, Z, F, false>, grid, block, s, p);
     });
 }
 
 int check(int dtype, int N, int K, int group) {
     if (dtype != SGEMM_DTYPE_BF16 && dtype != SGEMM_DTYPE_F16) return SGEMM_STATUS_INVALID_DTYPE;
     if (N < 0 || K < 0 || (group != 32 && group != 64 && group != 128)) return SGEMM_STATUS_INVALID_DIM;
-    return K > (1 << 30) ? SGEMM_STATUS_INVALID_DIM : SGEMM_STATUS_OK;
+    return K > kMaxLd16 || N > (1 << 30) ? SGEMM_STATUS_INVALID_DIM : SGEMM_STATUS_OK;
+}
+
+constexpr int kMaxRows = 1 << 24;       // launch grid extents
+
+// The packed form's alignment: a chunk of weights, scales and zero points each in one load.
+bool packed_ok(const void *packed, const void *scales, const void *zeros) {
+    return !(reinterpret_cast<uintptr_t>(packed) & 15) && !(reinterpret_cast<uintptr_t>(scales) & 7) &&
+           !(reinterpret_cast<uintptr_t>(zeros) & 3);
 }
 
 int chunks_of(int K) { return (K + kChunk - 1) / kChunk; }
@@ -289,26 +495,41 @@ using namespace sgemm_mi355x;
 
 extern "C" {
 
+long long sgemm_w4_workspace(int M, int K, const void *X, int ldx) {
+    if (M < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    return M == 0 || K == 0 || chunk_rows(X, ldx, K) ? 0 : 2L * M * ceil_to(K, 8);
+}
+
 int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx, const void *packed,
              const void *scales, const void *zeros, int group, float beta, void *C, int ldc, int dtype_c,
-             void *stream) {
+             void *workspace, long long workspace_bytes, void *stream) {
     const int st = check(dtype, N, K, group);
     if (st != SGEMM_STATUS_OK) return st;
     if (dtype_c != dtype && dtype_c != SGEMM_DTYPE_F32) return SGEMM_STATUS_INVALID_DTYPE;
-    if (M < 0 || ldx < std::max(K, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if (M < 0 || M > kMaxRows || ldx < std::max(K, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
     if (M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || (K > 0 && (X == nullptr || packed == nullptr || scales == nullptr)))
         return SGEMM_STATUS_NULL_POINTER;
-    if (reinterpret_cast<uintptr_t>(packed) & 15) return SGEMM_STATUS_UNSUPPORTED;
-    if ((M + 15) / 16 > 65535) return SGEMM_STATUS_INVALID_DIM;
-    const W4Args p = {static_cast<const char *>(X), static_cast<const unsigned char *>(packed),
-                      static_cast<const unsigned char *>(zeros), static_cast<const unsigned short *>(scales),
-                      static_cast<char *>(C), ldx, ldc, M, N, K, chunks_of(K), alpha, beta};
+    if (!packed_ok(packed, scales, zeros)) return SGEMM_STATUS_UNSUPPORTED;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    W4Args p = {static_cast<const char *>(X), static_cast<const unsigned char *>(packed),
+                static_cast<const unsigned char *>(zeros), static_cast<const unsigned short *>(scales),
+                static_cast<char *>(C), ldx, ldc, M, N, K, chunks_of(K), alpha, beta};
     const bool f16 = dtype == SGEMM_DTYPE_F16, out16 = dtype_c != SGEMM_DTYPE_F32;
-    const bool xvec = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0 && K % 8 == 0;
-    const hipError_t e = M <= 16 ? launch_w4<1, 8>(p, group, f16, out16, xvec, s)
-                                 : launch_w4<4, 4>(p, group, f16, out16, xvec, s);
+    const long long copy = sgemm_w4_workspace(M, K, X, ldx);
+    if (copy > 0) {
+        if (workspace == nullptr || workspace_bytes < copy || (reinterpret_cast<uintptr_t>(workspace) & 15))
+            return SGEMM_STATUS_SCRATCH_TOO_SMALL;
+        const hipError_t e = pad_rows(X, ldx, 0, 1, M, K, workspace, M, s);
+        if (e != hipSuccess) return hip_status(e, "kernel launch");
+        p.X = static_cast<const char *>(workspace);
+        p.ldx = ceil_to(K, 8);
+        p.K = (int)p.ldx;                   // the copy's columns behind K are zeros
+    }
+    const hipError_t e = M <= 16   ? launch_rows<1, 8>(p, group, f16, out16, s)
+                         : M <= 32 ? launch_rows<2, 8>(p, group, f16, out16, s)
+                         : M <= 64 ? launch_rows<4, 4>(p, group, f16, out16, s)
+                                   : launch_tile<8, 4, 2, 4>(p, group, f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
@@ -319,7 +540,7 @@ int sgemm_w4_quantize(int dtype, int N, int K, const void *W, int ldw, int group
     if (ldw < std::max(K, 1)) return SGEMM_STATUS_INVALID_DIM;
     if (N == 0 || K == 0) return SGEMM_STATUS_OK;
     if (W == nullptr || packed == nullptr || scales == nullptr) return SGEMM_STATUS_NULL_POINTER;
-    if (reinterpret_cast<uintptr_t>(packed) & 15) return SGEMM_STATUS_UNSUPPORTED;
+    if (!packed_ok(packed, scales, zeros)) return SGEMM_STATUS_UNSUPPORTED;
     const PackArgs p = {static_cast<const unsigned short *>(W), nullptr, static_cast<unsigned char *>(packed),
                         static_cast<unsigned char *>(zeros), static_cast<unsigned short *>(scales), ldw, N, K,
                         chunks_of(K), (reinterpret_cast<uintptr_t>(W) & 15) == 0 && ldw % 8 == 0 && K % 8 == 0};
@@ -338,7 +559,7 @@ int sgemm_w4_dequantize(int dtype, int N, int K, const void *packed, const void 
     if (ldw < std::max(K, 1)) return SGEMM_STATUS_INVALID_DIM;
     if (N == 0 || K == 0) return SGEMM_STATUS_OK;
     if (W == nullptr || packed == nullptr || scales == nullptr) return SGEMM_STATUS_NULL_POINTER;
-    if (reinterpret_cast<uintptr_t>(packed) & 15) return SGEMM_STATUS_UNSUPPORTED;
+    if (!packed_ok(packed, scales, zeros)) return SGEMM_STATUS_UNSUPPORTED;
     const PackArgs p = {nullptr, static_cast<unsigned short *>(W),
                         const_cast<unsigned char *>(static_cast<const unsigned char *>(packed)),
                         const_cast<unsigned char *>(static_cast<const unsigned char *>(zeros)),

@@ -471,14 +471,19 @@ long long sgemm_lowp_xent_workspace(int M, int N, int K, const void *X, int ldx,
  *           k = 32*s + 8*j .. + 7 of it, element 2i in bits 4i .. 4i+3 and
  *           element 2i+1 in bits 16+4i .. 16+4i+3; what it holds for k >= K
  *           is not used
- *   scales  N rows of Kp / group values of `dtype`, 2-byte aligned
- *   zeros   N rows of Kp / group bytes 0 .. 15, or NULL (every z is 8)
- * No workspace.
+ *   scales  N rows of Kp / group values of `dtype`, 8-byte aligned
+ *   zeros   N rows of Kp / group bytes 0 .. 15, 4-byte aligned, or NULL
+ *           (every z is 8)
+ * SGEMM_STATUS_UNSUPPORTED: one of them is not aligned so.  X whose rows are
+ * not whole aligned 16-byte chunks is first copied into the workspace.  M up
+ * to 2^24, K below 2^22 - 64.
  */
 int sgemm_w4(int dtype, int M, int N, int K, float alpha,
              const void *X, int ldx,
              const void *packed, const void *scales, const void *zeros, int group,
-             float beta, void *C, int ldc, int dtype_c, void *stream);
+             float beta, void *C, int ldc, int dtype_c,
+             void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_w4_workspace(int M, int K, const void *X, int ldx);
 
 /*
  * sgemm_w4_quantize: W [N,K] of `dtype` into the form above (zeros NULL:

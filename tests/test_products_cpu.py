@@ -16,7 +16,7 @@ GRAD = dict(dtype=1, M=8, N=100, K=16, alpha=1.0, X=AL, ldx=16, W=AL, ldw=16, ta
             dloss=AL, dloss_stride=1, dX=AL, lddx=16, dW=AL, lddw=16, workspace=AL, workspace_bytes=1 << 40,
             stream=None)
 W4 = dict(dtype=1, M=3, N=32, K=128, alpha=1.0, X=AL, ldx=128, packed=AL, scales=AL, zeros=None, group=128, beta=0.0,
-          C=AL, ldc=32, dtype_c=1, stream=None)
+          C=AL, ldc=32, dtype_c=1, workspace=None, workspace_bytes=0, stream=None)
 PACK = dict(dtype=1, N=32, K=128, W=AL, ldw=128, group=64, packed=AL, scales=AL, zeros=None, stream=None)
 UNPACK = dict(dtype=1, N=32, K=128, packed=AL, scales=AL, zeros=None, group=64, W=AL, ldw=128, stream=None)
 
@@ -55,7 +55,9 @@ REFUSED = [
         (TYPE, dict(dtype=3)), (TYPE, dict(dtype_c=2)), (DIM, dict(M=-1)), (DIM, dict(N=-1)), (DIM, dict(K=-1)),
         (DIM, dict(group=16)), (DIM, dict(group=256)), (DIM, dict(ldx=127)), (DIM, dict(ldc=31)),
         (NULL, dict(X=None)), (NULL, dict(packed=None)), (NULL, dict(scales=None)), (NULL, dict(C=None)),
-        (UNSUP, dict(packed=0x10008))]),
+        (UNSUP, dict(packed=0x10008)), (UNSUP, dict(scales=0x10004)), (UNSUP, dict(zeros=0x10002)),
+        (DIM, dict(M=(1 << 24) + 1)), (DIM, dict(K=1 << 23, ldx=1 << 23)), (SMALL, dict(X=MIS)),
+        (SMALL, dict(ldx=129, workspace=AL, workspace_bytes=3 * 256 - 1))]),
     (capi.sgemm_w4_quantize, PACK, [
         (TYPE, dict(dtype=3)), (DIM, dict(N=-1)), (DIM, dict(group=48)), (DIM, dict(ldw=127)), (NULL, dict(W=None)),
         (NULL, dict(packed=None)), (NULL, dict(scales=None)), (UNSUP, dict(packed=0x10004))]),
@@ -97,6 +99,10 @@ def test_workspaces():
     M, N, K = 8192, 128000, 4096
     assert capi.sgemm_lowp_xent_workspace(M, N, K, AL, K, AL, K, 1) < M * N * 2 // 4
     assert capi.sgemm_lowp_xent_workspace(M, N, K, AL, K, AL, K, 0) < M * N * 2 // 8
+
+
+    assert capi.sgemm_w4_workspace(3, 128, AL, 128) == 0
+    assert capi.sgemm_w4_workspace(3, 125, AL, 128) == 3 * 128 * 2
 
 
 def test_python_refusals_without_a_device():
