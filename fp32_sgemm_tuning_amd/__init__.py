@@ -221,10 +221,15 @@ def sgemm_lowp(A, B, C=None, alpha=1.0, beta=0.0, variant=None, stream=None, tra
 # ---------------------------------------------------------------------------
 # Products grouped by rows, the output layer with its loss, 4-bit weights.
 # ---------------------------------------------------------------------------
+_CODES = {}     # torch type -> element type code
+
+
 def _codes():
-    import torch
-    return {torch.bfloat16: capi.SGEMM_DTYPE_BF16, torch.float16: capi.SGEMM_DTYPE_F16,
-            torch.float32: capi.SGEMM_DTYPE_F32}
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: capi.SGEMM_DTYPE_BF16, torch.float16: capi.SGEMM_DTYPE_F16,
+                       torch.float32: capi.SGEMM_DTYPE_F32})
+    return _CODES
 
 
 def _inputs16():
@@ -232,13 +237,13 @@ def _inputs16():
     return torch.bfloat16, torch.float16
 
 
-def _one_device(**tensors):
-    """The device of the tensors (None ones left out); an error if they are on several."""
-    seen = {name: t.device for name, t in tensors.items() if t is not None}
-    devices = set(seen.values())
-    if len(devices) != 1:
-        raise ValueError("operands must be on one device, got " + ", ".join(f"{n} on {d}" for n, d in seen.items()))
-    device = devices.pop()
+def _one_device(*named):
+    """The device of the (name, tensor) pairs (None tensors left out); an error if they are on several."""
+    device = named[0][1].device
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError("operands must be on one device, got " +
+                             ", ".join(f"{n} on {x.device}" for n, x in named if x is not None))
     if device.type != "cuda":
         raise ValueError("operands must be device tensors")
     return device
@@ -253,13 +258,28 @@ def _vector(t, name, dtype, size):
         raise ValueError(f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _On:
     """`device` current, and `stream` (if given) current on it, so that what
-    is allocated for a call belongs to the stream the call runs on."""
-    import torch
-    with _device_ctx(device), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
-        yield _stream_handle(device, stream)
+    is allocated for a call belongs to the stream the call runs on; gives the
+    stream's handle."""
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        import torch
+        inner = _device_ctx(self.device)
+        if self.stream is not None or not isinstance(inner, contextlib.nullcontext):
+            self.stack = contextlib.ExitStack()
+            self.stack.enter_context(inner)
+            if self.stream is not None:
+                self.stack.enter_context(torch.cuda.stream(self.stream))
+        return _stream_handle(self.device, self.stream)
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
 
 
 def _check(status):
@@ -268,12 +288,16 @@ def _check(status):
     return status
 
 
-def _workspace(size, device):
-    """(tensor, address, bytes); the tensor is kept by the caller over the call."""
-    import torch
-    _check(size)
-    w = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-    return w, (w.data_ptr() if size else None), size
+def _with_workspace(call, size, device):
+    """call(workspace address, bytes), with a workspace of size() bytes if it
+    asks for one (it has then enqueued nothing)."""
+    status = call(None, 0)
+    if status == capi.SGEMM_STATUS_SCRATCH_TOO_SMALL:
+        import torch
+        n = _check(size())
+        keep = torch.empty(n, dtype=torch.uint8, device=device)
+        status = call(keep.data_ptr(), n)
+    _check(status)
 
 
 def _result(C, shape, out_dtype, default, allowed, beta, device):
@@ -326,16 +350,16 @@ def sgemm_grouped(A, B, offsets, C=None, alpha=1.0, beta=0.0, trans_b=False, out
         raise ValueError(f"inner dimensions differ: A is {M}x{K}, op(B[g]) is {K2}x{N}")
     if B.shape[0] != groups:
         raise ValueError(f"B holds {B.shape[0]} matrices, offsets bound {groups} groups")
-    device = _one_device(A=A, B=B, offsets=offsets, C=C)
-    with _on(device, stream) as h:
+    device = _one_device(("A", A), ("B", B), ("offsets", offsets), ("C", C))
+    with _On(device, stream) as h:
         C = _result(C, (M, N), out_dtype, torch.float32, (torch.float32, A.dtype), beta, device)
         ldc = _ld(C, "C", (C.dtype,))
         op = capi.SGEMM_OP_T if trans_b else capi.SGEMM_OP_N
         b_args = (A.data_ptr(), lda, B.data_ptr(), ldb, sb)
-        keep, ws, size = _workspace(capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *b_args), device)
-        _check(capi.sgemm_lowp_grouped(_codes()[A.dtype], op, groups, M, N, K, float(alpha), *b_args,
-                                       offsets.data_ptr(), float(beta), C.data_ptr(), ldc, _codes()[C.dtype], ws,
-                                       size, h))
+        args = (_codes()[A.dtype], op, groups, M, N, K, float(alpha), *b_args, offsets.data_ptr(), float(beta),
+                C.data_ptr(), ldc, _codes()[C.dtype])
+        _with_workspace(lambda ws, size: capi.sgemm_lowp_grouped(*args, ws, size, h),
+                        lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *b_args), device)
     return C
 
 
@@ -357,15 +381,15 @@ def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=No
         raise TypeError(f"A is {A.dtype} but D is {D.dtype}")
     if M2 != M:
         raise ValueError(f"A has {M} rows, D has {M2}")
-    device = _one_device(A=A, D=D, offsets=offsets, C=C)
-    with _on(device, stream) as h:
+    device = _one_device(("A", A), ("D", D), ("offsets", offsets), ("C", C))
+    with _On(device, stream) as h:
         C = _result(C, (groups, K, N), out_dtype, torch.float32, (torch.float32, A.dtype), beta, device)
         _, _, ldc, sc = _mat(C, "C", (C.dtype,))
         a_args = (A.data_ptr(), lda, D.data_ptr(), ldd)
-        keep, ws, size = _workspace(capi.sgemm_lowp_grouped_wgrad_workspace(M, N, K, *a_args), device)
-        _check(capi.sgemm_lowp_grouped_wgrad(_codes()[A.dtype], groups, M, N, K, float(alpha), *a_args,
-                                             offsets.data_ptr(), float(beta), C.data_ptr(), ldc, sc,
-                                             _codes()[C.dtype], ws, size, h))
+        args = (_codes()[A.dtype], groups, M, N, K, float(alpha), *a_args, offsets.data_ptr(), float(beta),
+                C.data_ptr(), ldc, sc, _codes()[C.dtype])
+        _with_workspace(lambda ws, size: capi.sgemm_lowp_grouped_wgrad(*args, ws, size, h),
+                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(M, N, K, *a_args), device)
     return C
 
 
@@ -395,14 +419,15 @@ def sgemm_xent(X, W, target, alpha=1.0, ignore_index=-100, stream=None):
     gives a NaN loss."""
     import torch
     M, N, K, ldx, ldw = _xent_args(X, W, target)
-    device = _one_device(X=X, W=W, target=target)
-    with _on(device, stream) as h:
+    device = _one_device(("X", X), ("W", W), ("target", target))
+    with _On(device, stream) as h:
         loss = torch.empty(M, dtype=torch.float32, device=device)
         lse = torch.empty(M, dtype=torch.float32, device=device)
         args = (X.data_ptr(), ldx, W.data_ptr(), ldw)
-        keep, ws, size = _workspace(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 0), device)
+        size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 0))
+        keep = torch.empty(size, dtype=torch.uint8, device=device)
         _check(capi.sgemm_lowp_xent(_codes()[X.dtype], M, N, K, float(alpha), *args, target.data_ptr(),
-                                    int(ignore_index), loss.data_ptr(), lse.data_ptr(), ws, size, h))
+                                    int(ignore_index), loss.data_ptr(), lse.data_ptr(), keep.data_ptr(), size, h))
     return loss, lse
 
 
@@ -423,16 +448,17 @@ def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need
         step = dloss.stride(0)
     else:
         raise ValueError(f"dloss has shape {tuple(dloss.shape)}, expected {(M,)} or one value")
-    device = _one_device(X=X, W=W, target=target, lse=lse, dloss=dloss)
-    with _on(device, stream) as h:
+    device = _one_device(("X", X), ("W", W), ("target", target), ("lse", lse), ("dloss", dloss))
+    with _On(device, stream) as h:
         dX = torch.empty((M, K), dtype=X.dtype, device=device) if need_dx else None
         dW = torch.empty((N, K), dtype=X.dtype, device=device) if need_dw else None
         args = (X.data_ptr(), ldx, W.data_ptr(), ldw)
-        keep, ws, size = _workspace(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 1), device)
+        size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 1))
+        keep = torch.empty(size, dtype=torch.uint8, device=device)
         _check(capi.sgemm_lowp_xent_grad(_codes()[X.dtype], M, N, K, float(alpha), *args, target.data_ptr(),
                                          int(ignore_index), lse.data_ptr(), dloss.data_ptr(), step,
                                          dX.data_ptr() if need_dx else None, max(K, 1),
-                                         dW.data_ptr() if need_dw else None, max(K, 1), ws, size, h))
+                                         dW.data_ptr() if need_dw else None, max(K, 1), keep.data_ptr(), size, h))
     return dX, dW
 
 
@@ -492,14 +518,15 @@ def sgemm_w4(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
         raise TypeError(f"X is {X.dtype} but the scales are {W.scales.dtype}")
     if K != W.K:
         raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {N}x{W.K}")
-    device = _one_device(X=X, packed=W.packed, scales=W.scales, zeros=W.zeros, C=C)
-    with _on(device, stream) as h:
+    device = _one_device(("X", X), ("packed", W.packed), ("scales", W.scales), ("zeros", W.zeros), ("C", C))
+    with _On(device, stream) as h:
         C = _result(C, (M, N), out_dtype, torch.float32, (torch.float32, X.dtype), beta, device)
         ldc = _ld(C, "C", (C.dtype,))
-        keep, ws, size = _workspace(capi.sgemm_w4_workspace(M, K, X.data_ptr(), ldx), device)
-        _check(capi.sgemm_w4(_codes()[X.dtype], M, N, K, float(alpha), X.data_ptr(), ldx, W.packed.data_ptr(),
-                             W.scales.data_ptr(), _address(W.zeros), W.group, float(beta), C.data_ptr(), ldc,
-                             _codes()[C.dtype], ws, size, h))
+        x, codes = X.data_ptr(), _codes()
+        args = (codes[X.dtype], M, N, K, float(alpha), x, ldx, W.packed.data_ptr(), W.scales.data_ptr(),
+                _address(W.zeros), W.group, float(beta), C.data_ptr(), ldc, codes[C.dtype])
+        _with_workspace(lambda ws, size: capi.sgemm_w4(*args, ws, size, h),
+                        lambda: capi.sgemm_w4_workspace(M, K, x, ldx), device)
     return C
 
 
@@ -514,8 +541,8 @@ def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
     if group not in (32, 64, 128):
         raise ValueError(f"group is {group}, expected 32, 64 or 128")
     Kp = (K + 127) // 128 * 128
-    device = _one_device(W=W)
-    with _on(device, stream) as h:
+    device = _one_device(("W", W))
+    with _On(device, stream) as h:
         out = W4Weight(torch.empty((N, Kp // 2), dtype=torch.uint8, device=device),
                        torch.empty((N, Kp // group), dtype=W.dtype, device=device),
                        torch.empty((N, Kp // group), dtype=torch.uint8, device=device) if zeros else None, K, group)
@@ -528,8 +555,8 @@ def sgemm_w4_dequantize(W, stream=None):
     """The values [N,K] a W4Weight stands for, rounded to its scales' type."""
     import torch
     N = _w4(W)
-    device = _one_device(packed=W.packed, scales=W.scales, zeros=W.zeros)
-    with _on(device, stream) as h:
+    device = _one_device(("packed", W.packed), ("scales", W.scales), ("zeros", W.zeros))
+    with _On(device, stream) as h:
         out = torch.empty((N, W.K), dtype=W.scales.dtype, device=device)
         _check(capi.sgemm_w4_dequantize(_codes()[out.dtype], N, W.K, W.packed.data_ptr(), W.scales.data_ptr(),
                                         _address(W.zeros), W.group, out.data_ptr(), max(W.K, 1), h))

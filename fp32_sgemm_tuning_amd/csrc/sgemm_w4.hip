@@ -48,94 +48,140 @@ __device__ __forceinline__ int q_pair(unsigned w) {
     return (int)((v & (F16 ? 0x03C003C0u : 0x00780078u)) | (F16 ? 0x4C004C00u : 0x41804180u));
 }
 
-// Few rows of X: MB blocks of 16 of them by 16 rows of W per workgroup, whose
-// NW waves take consecutive runs of chunks and add up through LDS.  Bound by
-// the weights' bytes if enough of them are in flight, so a wave starts the
-// loads of U chunks (weights, scales, zero points, X) before it uses the
-// first.  GROUP: k per scale.
-template <int MB, int NW, int GROUP, bool ZEROS, bool F16, bool OUT16>
+// Few rows of X: MB blocks of 16 of them by NB blocks of 16 rows of W per
+// workgroup, whose NW waves take consecutive runs of chunks and add up
+// through LDS.  The weights' bytes bound it as far as the vector memory path
+// of a compute unit keeps up (64 bytes a clock, and a cycle for each 128-byte
+// line that a load touches), so that path is spared: a wave loads four chunks
+// of weights at once, one load brings the scales of four chunks (lane
+// (n, j) has row n's of chunk j; they are handed round in registers), and
+// lanes of rows past M load nothing.  GROUP: k per scale.
+template <int MB, int NB, int NW, int GROUP, bool ZEROS, bool F16, bool OUT16>
 __global__ void __launch_bounds__(64 * NW) w4_rows_kernel(W4Args p) {
     constexpr int GPC = kChunk / GROUP, SPG = 4 / GPC;      // groups per chunk, k steps per group
-    constexpr int U = MB == 1 ? 4 : MB == 2 ? 2 : 1;
-    __shared__ f32x4 part[NW][MB][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using Scales = typename std::conditional<GPC == 4, unsigned long, unsigned>::type;
+    __shared__ f32x4 part[NW][MB * NB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MB;
-    const long n = min(n0 + lr, p.N - 1);
-    const unsigned char *wrow = p.packed + n * p.chunks * 64 + 16 * lg;
-    const unsigned short *srow = p.scales + n * p.chunks * GPC;
-    const unsigned char *zrow = ZEROS ? p.zeros + n * p.chunks * GPC : nullptr;
-    const unsigned short *xrow[MB];
+    const int n0 = blockIdx.x * 16 * NB, m0 = blockIdx.y * 16 * MB;
+    const unsigned char *wtile = p.packed + (long)n0 * p.chunks * 64;
+    const unsigned char *ztile = ZEROS ? p.zeros + (long)n0 * p.chunks * GPC : nullptr;
+    const unsigned short *stile = p.scales + (long)n0 * p.chunks * GPC;
+    const unsigned short *xtile = reinterpret_cast<const unsigned short *>(p.X) + (long)m0 * p.ldx;
+    unsigned first[NB], xrow[MB];                           // first chunk of this lane's rows of W; its rows of X
+    bool live[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
-        xrow[b] = reinterpret_cast<const unsigned short *>(p.X) + (long)min(m0 + 16 * b + lr, p.M - 1) * p.ldx + 8 * lg;
+    for (int b = 0; b < NB; ++b) first[b] = (unsigned)(min(16 * b + lr, p.N - 1 - n0) * p.chunks);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        live[m] = 16 * m + lr < p.M - m0;
+        xrow[m] = (unsigned)(16 * m + lr) * (unsigned)p.ldx + 8 * lg;
+    }
     const int one = F16 ? 0x3C003C00 : 0x3F803F80;
     const i32x4 ones = {one, one, one, one};
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 total[MB];
+    f32x4 total[MB][NB];
+    i32x4 x[2][4][MB];                                      // two chunks of X in turn
 #pragma unroll
-    for (int b = 0; b < MB; ++b) total[b] = zero;
-    const int last = (int)((long)p.chunks * (wave + 1) / NW);
-    for (int c0 = (int)((long)p.chunks * wave / NW); c0 < last; c0 += U) {
-        i32x4 w[U], x[U][4][MB];
-        unsigned long sc[U];
-        unsigned zp[U];
+    for (int m = 0; m < MB; ++m) {
 #pragma unroll
-        for (int t = 0; t < U; ++t) {
-            const int c = min(c0 + t, last - 1);
-            w[t] = *reinterpret_cast<const i32x4 *>(wrow + (long)c * 64);
-            if constexpr (GPC == 4) sc[t] = *reinterpret_cast<const unsigned long *>(srow + (long)c * GPC);
-            else if constexpr (GPC == 2) sc[t] = *reinterpret_cast<const unsigned *>(srow + (long)c * GPC);
-            else sc[t] = srow[c];
-            if constexpr (ZEROS && GPC == 4) zp[t] = *reinterpret_cast<const unsigned *>(zrow + (long)c * GPC);
-            else if constexpr (ZEROS && GPC == 2) zp[t] = *reinterpret_cast<const unsigned short *>(zrow + (long)c * GPC);
-            else zp[t] = ZEROS ? zrow[c] : 0x08080808u;
+        for (int b = 0; b < NB; ++b) total[m][b] = zero;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = c * kChunk + 32 * s;
+        for (int s = 0; s < 4; ++s) x[0][s][m] = x[1][s][m] = i32x4{0, 0, 0, 0};
+    }
+    // (what a lane of a row past M holds only reaches results of such rows)
+    auto load_x = [&](int c, i32x4 (&to)[4][MB]) {
+        const unsigned short *xc = xtile + (long)c * kChunk;
+        const bool whole = (c + 1) * kChunk <= p.K;
 #pragma unroll
-                for (int b = 0; b < MB; ++b) {
-                    // (chunks of X behind K are zeros: K is a multiple of 8 here)
-                    x[t][s][b] = i32x4{0, 0, 0, 0};
-                    if (k + 8 * lg < p.K && c0 + t < last) x[t][s][b] = *reinterpret_cast<const i32x4 *>(xrow[b] + k);
+        for (int m = 0; m < MB; ++m) {
+            if (whole) {
+                if (live[m]) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) to[s][m] = *reinterpret_cast<const i32x4 *>(xc + (xrow[m] + 32 * s));
+                }
+            } else {                                        // (K is a multiple of 8 here)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    to[s][m] = i32x4{0, 0, 0, 0};
+                    if (live[m] && c * kChunk + 32 * s + 8 * lg < p.K)
+                        to[s][m] = *reinterpret_cast<const i32x4 *>(xc + (xrow[m] + 32 * s));
                 }
             }
         }
+    };
+    const int last = (int)((long)p.chunks * (wave + 1) / NW);
+    for (int c0 = (int)((long)p.chunks * wave / NW); c0 < last; c0 += 4) {
+        i32x4 w[4][NB];
+        Scales four_s[NB];
+        unsigned four_z[NB];
 #pragma unroll
-        for (int t = 0; t < U; ++t) {
-            f32x4 sum[MB], sx[MB];
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t == 0 || c0 + t < last)
+                    w[t][b] = *reinterpret_cast<const i32x4 *>(wtile + ((first[b] + c0 + t) * 64 + 16 * lg));
+            const unsigned at = first[b] + min(c0 + lg, last - 1);
+            if constexpr (GPC > 1) four_s[b] = *reinterpret_cast<const Scales *>(stile + at * GPC);
+            else four_s[b] = stile[at];
+            if constexpr (ZEROS && GPC == 4) four_z[b] = *reinterpret_cast<const unsigned *>(ztile + at * GPC);
+            else if constexpr (ZEROS && GPC == 2) four_z[b] = *reinterpret_cast<const unsigned short *>(ztile + at * GPC);
+            else four_z[b] = ZEROS ? ztile[at] : 0x08080808u;
+        }
+        load_x(c0, x[0]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (c0 + t >= last) break;
+            if (t < 3 && c0 + t + 1 < last) load_x(c0 + t + 1, x[(t + 1) & 1]);
+            f32x4 sum[MB][NB], sx[MB];
+            Scales sc[NB];
+            unsigned zp[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                sc[b] = __shfl(four_s[b], 16 * t + lr);
+                zp[b] = ZEROS ? __shfl(four_z[b], 16 * t + lr) : 0x08080808u;
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const unsigned v = w[t][s];
-                const i32x4 wf = {q_pair<F16, 0>(v), q_pair<F16, 1>(v), q_pair<F16, 2>(v), q_pair<F16, 3>(v)};
 #pragma unroll
-                for (int b = 0; b < MB; ++b) {
-                    sum[b] = mfma_16x16x32<F16>(x[t][s][b], wf, s % SPG == 0 ? zero : sum[b]);
-                    sx[b] = mfma_16x16x32<F16>(x[t][s][b], ones, s % SPG == 0 ? zero : sx[b]);
+                for (int m = 0; m < MB; ++m)
+                    sx[m] = mfma_16x16x32<F16>(x[t & 1][s][m], ones, s % SPG == 0 ? zero : sx[m]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const unsigned v = w[t][b][s];
+                    const i32x4 wf = {q_pair<F16, 0>(v), q_pair<F16, 1>(v), q_pair<F16, 2>(v), q_pair<F16, 3>(v)};
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        sum[m][b] = mfma_16x16x32<F16>(x[t & 1][s][m], wf, s % SPG == 0 ? zero : sum[m][b]);
                 }
                 if (s % SPG == SPG - 1) {
-                    const float scale = widen16<F16>((unsigned short)(sc[t] >> (16 * (s / SPG))));
-                    const float z = 16.f + (float)(zp[t] >> (8 * (s / SPG)) & 255);
 #pragma unroll
-                    for (int b = 0; b < MB; ++b) total[b] += (sum[b] - sx[b] * z) * scale;
+                    for (int b = 0; b < NB; ++b) {
+                        const float scale = widen16<F16>((unsigned short)(sc[b] >> (16 * (s / SPG))));
+                        const float z = 16.f + (float)(zp[b] >> (8 * (s / SPG)) & 255);
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) total[m][b] += (sum[m][b] - sx[m] * z) * scale;
+                    }
                 }
             }
         }
     }
 #pragma unroll
-    for (int b = 0; b < MB; ++b) part[wave][b][lane] = total[b];
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) part[wave][m * NB + b][lane] = total[m][b];
     __syncthreads();
-    // block b's lane l holds rows 4*(l/16) .. +3 of column l%16
-    for (int t = threadIdx.x; t < MB * 64; t += 64 * NW) {
+    // block (m, b)'s lane l holds rows 4*(l/16) .. +3 of column l%16
+    for (int t = threadIdx.x; t < MB * NB * 64; t += 64 * NW) {
         const int b = t >> 6, l = t & 63;
         f32x4 v = part[0][b][l];
 #pragma unroll
         for (int w = 1; w < NW; ++w) v += part[w][b][l];
-        const int col = n0 + (l & 15);
+        const int col = n0 + 16 * (b % NB) + (l & 15);
         if (col >= p.N) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = m0 + 16 * b + 4 * (l >> 4) + r;
+            const int row = m0 + 16 * (b / NB) + 4 * (l >> 4) + r;
             if (row >= p.M) continue;
             float o = p.alpha * v[r];
             if constexpr (OUT16) {
@@ -178,20 +224,24 @@ __device__ __forceinline__ i32x4 centred(unsigned w, unsigned zs) {
 
 // Many rows of X: a workgroup of WM x WN waves takes 16*MI*WM rows of X by
 // 16*NB*WN rows of W.  X comes through LDS (direct loads of one 128-k chunk,
-// two stages, rows of 256 bytes in the layout ALayout<64>); the weights go
-// from memory straight into the registers of the one wave column that needs
-// them, which takes half of the LDS traffic of a plain product away.  q - z is
-// exact in 16 bits; two k steps of a group are summed by the matrix
-// instructions and then added to the FP32 total with the group's scale, one
-// multiply-add per output and 64 k (32 for groups of 32): what bounds it next
-// to the matrix instructions.  The product is formed transposed, as in
+// two stages, rows of 256 bytes, 16-byte chunk c of row m at c ^ (m % 16): free
+// of bank conflicts); the weights go from memory straight into the registers
+// of the one wave that multiplies them, so each is unpacked once per tile and
+// only X loads the LDS.  q - z is exact in 16 bits; two k steps of a group
+// (one for groups of 32) are summed by the matrix instructions and then added
+// to the FP32 total with the group's scale.  Those multiply-adds and the
+// unpacking take about as many cycles as the matrix instructions, so every
+// matrix instruction is followed by its share of them: left to itself the
+// compiler gathers each kind, and the same tile runs 169 us instead of 152
+// (2048 x 8192 x 4096, groups of 64 with zero points, FP16: 903 TFLOP/s).  Two
+// workgroups of four waves share a compute unit; one of eight, in step at
+// every barrier, takes 167 us.  The product is formed transposed, as in
 // sgemm_lowp.hpp: lane l holds row l%16 and columns 4*(l/16) .. +3.
 template <int MI, int NB, int WM, int WN, int GROUP, bool ZEROS, bool F16, bool OUT16>
 __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
     constexpr int GPC = kChunk / GROUP, SPG = GROUP == 32 ? 1 : 2, PARTS = 4 / SPG;
     constexpr int NWAVES = WM * WN, BM = 16 * MI * WM, BN = 16 * NB * WN;
     constexpr int STAGE = BM * 256, L = STAGE / 16 / (64 * NWAVES);
-    using AL = ALayout<64>;
     __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
@@ -243,9 +293,32 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int b = 0; b < NB; ++b) total[mi][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // the values and scales of k steps h*SPG .. of a chunk, from its registers
+    i32x4 wf[2][SPG][NB];
+    f32x4 scale[2][NB];
+    // word (b, s) of part h, and the scales of part h for block b
+    auto unpack_word = [&](auto hc, auto bc, auto sc_, const i32x4 (&cw)[NB], const unsigned (&cz)[NB]) {
+        constexpr int h = decltype(hc)::value, b = decltype(bc)::value, s = decltype(sc_)::value;
+        const unsigned z = cz[b] >> (8 * (h * GPC / PARTS)) & 255;
+        wf[h & 1][s][b] = centred<F16>(cw[b][h * SPG + s], F16 ? (0x4C00u + (z << 6)) * 0x10001u : __float_as_uint((float)z));
+    };
+    auto unpack_scale = [&](auto hc, auto bc, const Scales (&cs)[NB]) {
+        constexpr int h = decltype(hc)::value, b = decltype(bc)::value;
+        const float mine = widen16<F16>((unsigned short)(cs[b] >> (16 * (h * GPC / PARTS))));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) scale[h & 1][b][r] = __shfl(mine, 4 * lg + r);
+    };
+    const int frag = (wm * MI * 16 + lr) * 256;             // this lane's row in a stage
+    auto read_x = [&](const char *stage, int mi, int step) {
+        return *reinterpret_cast<const i32x4 *>(stage + frag + mi * 16 * 256 + 16 * ((4 * step + lg) ^ lr));
+    };
     if (p.chunks > 0) {
         load_x(0, 0);
         load_w(0);
+        static_for<0, NB>([&](auto bc) {
+            unpack_scale(IntC<0>{}, bc, sc);
+            static_for<0, SPG>([&](auto s) { unpack_word(IntC<0>{}, bc, s, w, zp); });
+        });
     }
     for (int c = 0; c < p.chunks; ++c) {
         // this wave's loads of chunk c have landed, then everyone's; and
@@ -262,47 +335,51 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
             cs[b] = sc[b];
             cz[b] = zp[b];
         }
-        if (c + 1 < p.chunks) {
-            load_x(c + 1, (c + 1) & 1);
-            load_w(c + 1);
-        }
+        const int next = min(c + 1, p.chunks - 1);          // (the last chunk's weights once more, unused)
+        if (c + 1 < p.chunks) load_x(c + 1, (c + 1) & 1);
+        load_w(next);
         __builtin_amdgcn_sched_barrier(0);
         const char *stage = lds + (c & 1) * STAGE;
+        // Step j = (part h, 16 rows mi): its matrix instructions; in between,
+        // the sums of the step before are scaled, X for step j + AHEAD is
+        // read and, spread over the part, the values of the next part (or
+        // of the next chunk's first) are unpacked.
+        constexpr int STEPS = PARTS * MI, AHEAD = 3;
+        f32x4 sum[2][NB];
+        i32x4 x[AHEAD + 1][SPG];
+        auto read_step = [&](auto jc) {
+            constexpr int j = decltype(jc)::value;
 #pragma unroll
-        for (int h = 0; h < PARTS; ++h) {
-            const int g = h * GPC / PARTS;                  // group of these k steps
-            i32x4 wf[SPG][NB];
-            f32x4 scale[NB];
+            for (int s = 0; s < SPG; ++s) x[j % (AHEAD + 1)][s] = read_x(stage, j % MI, j / MI * SPG + s);
+        };
+        // results of a step, in as many pieces as it has matrix instructions
+        constexpr int Q = SPG * NB;
+        auto finish = [&](auto jc, auto qc) {
+            constexpr int j = decltype(jc)::value, q = decltype(qc)::value;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const unsigned z = cz[b] >> (8 * g) & 255;
-                unsigned zs;
-                if constexpr (F16) {
-                    zs = (0x4C00u + (z << 6)) * 0x10001u;   // 16 + z twice
-                } else {
-                    zs = __float_as_uint((float)z);
-                }
-#pragma unroll
-                for (int s = 0; s < SPG; ++s) wf[s][b] = centred<F16>(cw[b][h * SPG + s], zs);
-                const float mine = widen16<F16>((unsigned short)(cs[b] >> (16 * g)));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) scale[b][r] = __shfl(mine, 4 * lg + r);
-            }
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) {
-                f32x4 sum[NB];
-#pragma unroll
-                for (int s = 0; s < SPG; ++s) {
-                    const int m = (wm * MI + mi) * 16 + lr;
-                    const i32x4 x = *reinterpret_cast<const i32x4 *>(stage + 4 * AL::offset(m, 4 * (h * SPG + s) + lg));
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        sum[b] = mfma_16x16x32<F16>(wf[s][b], x, s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[b]);
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) total[mi][b] += sum[b] * scale[b];
-            }
-        }
+            for (int e = 4 * NB * q / Q; e < 4 * NB * (q + 1) / Q; ++e)
+                total[j % MI][e / 4][e % 4] += sum[j & 1][e / 4][e % 4] * scale[j / MI & 1][e / 4][e % 4];
+        };
+        static_for<0, AHEAD>(read_step);
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<0, STEPS>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, h = j / MI, mi = j % MI, next_h = (h + 1) % PARTS;
+            static_for<0, Q>([&](auto qc) {
+                constexpr int q = decltype(qc)::value, s = q / NB, b = q % NB;
+                sum[j & 1][b] = mfma_16x16x32<F16>(wf[h & 1][s][b], x[j % (AHEAD + 1)][s],
+                                                   s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j & 1][b]);
+                if constexpr (q == 0 && j + AHEAD < STEPS) read_step(IntC<j + AHEAD>{});
+                if constexpr (j > 0) finish(IntC<(j > 0 ? j - 1 : 0)>{}, qc);
+                // Q words of the next part over the steps mi of this one
+                static_for<Q * (mi * Q + q) / (MI * Q), Q * (mi * Q + q + 1) / (MI * Q)>([&](auto uc) {
+                    constexpr int u = decltype(uc)::value;
+                    if constexpr (u / SPG * SPG == u) unpack_scale(IntC<next_h>{}, IntC<u / SPG>{}, next_h ? cs : sc);
+                    unpack_word(IntC<next_h>{}, IntC<u / SPG>{}, IntC<u % SPG>{}, next_h ? cw : w, next_h ? cz : zp);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+        static_for<0, Q>([&](auto qc) { finish(IntC<STEPS - 1>{}, qc); });
     }
     constexpr int E = OUT16 ? 2 : 4;
     const bool vec = (reinterpret_cast<uintptr_t>(p.C) & (4 * E - 1)) == 0 && (p.ldc & 3) == 0;
@@ -447,14 +524,14 @@ hipError_t with_form(int group, bool zeros, bool f16, F &&f) {
     return group == 32 ? by_zero(IntC<32>{}) : group == 64 ? by_zero(IntC<64>{}) : by_zero(IntC<128>{});
 }
 
-template <int MB, int NW>
+template <int MB, int NB, int NW>
 hipError_t launch_rows(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
-    const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.M + 16 * MB - 1) / (16 * MB))), block(64 * NW);
+    const dim3 grid((unsigned)((p.N + 16 * NB - 1) / (16 * NB)), (unsigned)((p.M + 16 * MB - 1) / (16 * MB))), block(64 * NW);
     return with_form(group, p.zeros != nullptr, f16, [&](auto g, auto z, auto f) {
         constexpr int G = decltype(g)::value;
         constexpr bool Z = decltype(z)::value, F = decltype(f)::value;
-        return out16 ? launch_k(w4_rows_kernel<MB, NW, G, Z, F, true>, grid, block, s, p)
-                     : launch_k(w4_rows_kernel<MB, NW, G, Z, F, false>, grid, block, s, p);
+        return out16 ? launch_k(w4_rows_kernel<MB, NB, NW, G, Z, F, true>, grid, block, s, p)
+                     : launch_k(w4_rows_kernel<MB, NB, NW, G, Z, F, false>, grid, block, s, p);
     });
 }
 
@@ -468,6 +545,30 @@ hipError_t launch_tile(const W4Args &p, int group, bool f16, bool out16, hipStre
         return out16 ? launch_k(w4_tile_kernel<MI, NB, WM, WN, G, Z, F, true>, grid, block, s, p)
                      : launch_k(w4_tile_kernel<MI, NB, WM, WN, G, Z, F, false>, grid, block, s, p);
     });
+}
+
+// Up to 64 rows: the widest block of W that still leaves 200 workgroups (more
+// columns share the loads of X, fewer workgroups leave compute units idle:
+// 8 x 14336 x 4096 17.9 / 16.4 / 14.1 us on 16, 32 and 64 columns, 1 x 4096 x
+// 4096 5.3 / 6.6 / 10.1 us).  More rows: the shortest of three predicted times,
+// all for K = 4096, per 256 workgroups of a kernel once a compute unit's share
+// is full: 32 x 64 blocks of the first kernel 19.6 us, 64 x 128 tiles 27 us
+// (41 at least), 128 x 128 tiles 38 us (51 at least); measured on N = 8192 for
+// 128 rows 37.7 / 42.6 / 51.4 us, for 256 rows 73.9 / 42.0 / 57, for 2048 rows
+// 590 / 216 / 152.
+hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
+    auto blocks = [&](int bm, int bn) { return (p.M + bm - 1L) / bm * ((p.N + bn - 1L) / bn); };
+    if (p.M <= 16)
+        return blocks(16, 64) >= 200   ? launch_rows<1, 4, 8>(p, group, f16, out16, s)
+               : blocks(16, 32) >= 200 ? launch_rows<1, 2, 8>(p, group, f16, out16, s)
+                                       : launch_rows<1, 1, 8>(p, group, f16, out16, s);
+    const double rows = std::max(19.6, 19.6 * blocks(32, 64) / 256), t64 = std::max(41.0, 27.0 * blocks(64, 128) / 256),
+                 t128 = std::max(51.0, 38.0 * blocks(128, 128) / 256);
+    if (p.M <= 64 || (rows <= t64 && rows <= t128))
+        return blocks(32, 64) >= 200   ? launch_rows<2, 4, 4>(p, group, f16, out16, s)
+               : blocks(32, 32) >= 200 ? launch_rows<2, 2, 8>(p, group, f16, out16, s)
+                                       : launch_rows<2, 1, 8>(p, group, f16, out16, s);
+    return t64 <= t128 ? launch_tile<4, 2, 1, 4>(p, group, f16, out16, s) : launch_tile<8, 2, 1, 4>(p, group, f16, out16, s);
 }
 
 int check(int dtype, int N, int K, int group) {
@@ -526,10 +627,7 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx
         p.ldx = ceil_to(K, 8);
         p.K = (int)p.ldx;                   // the copy's columns behind K are zeros
     }
-    const hipError_t e = M <= 16   ? launch_rows<1, 8>(p, group, f16, out16, s)
-                         : M <= 32 ? launch_rows<2, 8>(p, group, f16, out16, s)
-                         : M <= 64 ? launch_rows<4, 4>(p, group, f16, out16, s)
-                                   : launch_tile<8, 4, 2, 4>(p, group, f16, out16, s);
+    const hipError_t e = launch_w4(p, group, f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
