@@ -232,20 +232,34 @@ def _codes():
     return _CODES
 
 
-def _inputs16():
-    import torch
-    return torch.bfloat16, torch.float16
+def _rows16(t, name):
+    """(type code, rows, columns, leading dimension) of a 16-bit row-major matrix view."""
+    code = _codes().get(t.dtype, 0)
+    if code not in (capi.SGEMM_DTYPE_BF16, capi.SGEMM_DTYPE_F16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    step, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    # (a single row, or none, has no meaningful row stride)
+    return code, rows, cols, step if rows > 1 or step >= cols > 0 else max(cols, 1)
 
 
-def _one_device(*named):
-    """The device of the (name, tensor) pairs (None tensors left out); an error if they are on several."""
-    device = named[0][1].device
-    for name, t in named:
-        if t is not None and t.device != device:
-            raise ValueError("operands must be on one device, got " +
-                             ", ".join(f"{n} on {x.device}" for n, x in named if x is not None))
+def _same_type(a, a_name, b, b_name):
+    if a.dtype != b.dtype:
+        raise TypeError(f"{a_name} is {a.dtype} but {b_name} is {b.dtype}")
+
+
+def _one_device(first, *named):
+    """The device of `first` and of the (name, tensor) pairs (None tensors left out)."""
+    device = first.device
     if device.type != "cuda":
         raise ValueError("operands must be device tensors")
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"operands must be on one device: {name} is on {t.device}, not on {device}")
     return device
 
 
@@ -258,28 +272,14 @@ def _vector(t, name, dtype, size):
         raise ValueError(f"{name} must be contiguous")
 
 
-class _On:
-    """`device` current, and `stream` (if given) current on it, so that what
-    is allocated for a call belongs to the stream the call runs on; gives the
-    stream's handle."""
-    __slots__ = ("device", "stream", "stack")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.stack = device, stream, None
-
-    def __enter__(self):
-        import torch
-        inner = _device_ctx(self.device)
-        if self.stream is not None or not isinstance(inner, contextlib.nullcontext):
-            self.stack = contextlib.ExitStack()
-            self.stack.enter_context(inner)
-            if self.stream is not None:
-                self.stack.enter_context(torch.cuda.stream(self.stream))
-        return _stream_handle(self.device, self.stream)
-
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
+def _run(device, stream, call):
+    """call(stream handle), with `device` current and `stream` (if given)
+    current on it, so that what it allocates belongs to the stream it runs on."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(_stream_handle(device, None))
+    with _device_ctx(device), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
+        return call(_stream_handle(device, stream))
 
 
 def _check(status):
@@ -288,7 +288,7 @@ def _check(status):
     return status
 
 
-def _with_workspace(call, size, device):
+def _with_workspace(device, call, size):
     """call(workspace address, bytes), with a workspace of size() bytes if it
     asks for one (it has then enqueued nothing)."""
     status = call(None, 0)
@@ -300,20 +300,34 @@ def _with_workspace(call, size, device):
     _check(status)
 
 
-def _result(C, shape, out_dtype, default, allowed, beta, device):
-    """The result tensor of a call, checked or allocated."""
+def _check_result(C, shape, out_dtype, operand, beta):
+    """Before anything is allocated: beta, a given C's shape and type, the wanted type."""
     import torch
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty(shape, dtype=out_dtype or default, device=device)
-    elif out_dtype is not None and C.dtype != out_dtype:
+        if out_dtype is not None and out_dtype not in (torch.float32, operand.dtype):
+            raise TypeError(f"out_dtype is {out_dtype}, expected float32 or {operand.dtype}")
+        return
+    if out_dtype is not None and C.dtype != out_dtype:
         raise TypeError(f"C is {C.dtype} but out_dtype is {out_dtype}")
-    if C.dtype not in allowed:
-        raise TypeError(f"C has type {C.dtype}")
-    if tuple(C.shape) != tuple(shape):
-        raise ValueError(f"C has shape {tuple(C.shape)}, expected {tuple(shape)}")
-    return C
+    if C.dtype not in (torch.float32, operand.dtype):
+        raise TypeError(f"C has type {C.dtype}, expected float32 or {operand.dtype}")
+    if tuple(C.shape) != shape:
+        raise ValueError(f"C has shape {tuple(C.shape)}, expected {shape}")
+    if shape[-1] > 1 and C.stride(-1) != 1:
+        raise ValueError("C must have unit column stride (row-major)")
+
+
+def _result(C, shape, out_dtype, device):
+    """(C, its type's code, leading dimension), allocated here where it is None."""
+    import torch
+    rows, cols = shape[-2:]
+    if C is None:
+        dtype = out_dtype or torch.float32
+        return torch.empty(shape, dtype=dtype, device=device), _CODES[dtype], max(cols, 1)
+    step = C.stride(-2)
+    return C, _CODES[C.dtype], step if rows > 1 or step >= cols > 0 else max(cols, 1)
 
 
 def _offsets(offsets):
@@ -337,30 +351,33 @@ def sgemm_grouped(A, B, offsets, C=None, alpha=1.0, beta=0.0, trans_b=False, out
     be empty; rows of no group are left as they were (uninitialised in a C
     allocated here).  The gradient with respect to A is this call on dC with
     trans_b turned round; with respect to B see sgemm_grouped_wgrad."""
-    import torch
     groups = _offsets(offsets)
-    if A.dim() != 2 or B.dim() != 3:
-        raise ValueError("A must be 2-D and B 3-D")
-    M, K, lda, _ = _mat(A, "A", _inputs16())
-    rb, cb, ldb, sb = _mat(B, "B", _inputs16())
-    if B.dtype != A.dtype:
-        raise TypeError(f"A is {A.dtype} but B is {B.dtype}")
+    code, M, K, lda = _rows16(A, "A")
+    if B.dim() != 3:
+        raise ValueError("B must be 3-D")
+    _same_type(A, "A", B, "B")
+    held, rb, cb = B.shape
+    sb, ldb, unit = B.stride()
+    if unit != 1 and cb > 1:
+        raise ValueError("B must have unit column stride (row-major)")
+    ldb = ldb if rb > 1 or ldb >= cb > 0 else max(cb, 1)
     K2, N = (cb, rb) if trans_b else (rb, cb)
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A is {M}x{K}, op(B[g]) is {K2}x{N}")
-    if B.shape[0] != groups:
-        raise ValueError(f"B holds {B.shape[0]} matrices, offsets bound {groups} groups")
-    device = _one_device(("A", A), ("B", B), ("offsets", offsets), ("C", C))
-    with _On(device, stream) as h:
-        C = _result(C, (M, N), out_dtype, torch.float32, (torch.float32, A.dtype), beta, device)
-        ldc = _ld(C, "C", (C.dtype,))
-        op = capi.SGEMM_OP_T if trans_b else capi.SGEMM_OP_N
-        b_args = (A.data_ptr(), lda, B.data_ptr(), ldb, sb)
-        args = (_codes()[A.dtype], op, groups, M, N, K, float(alpha), *b_args, offsets.data_ptr(), float(beta),
-                C.data_ptr(), ldc, _codes()[C.dtype])
-        _with_workspace(lambda ws, size: capi.sgemm_lowp_grouped(*args, ws, size, h),
-                        lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *b_args), device)
-    return C
+    if held != groups:
+        raise ValueError(f"B holds {held} matrices, offsets bound {groups} groups")
+    device = _one_device(A, ("B", B), ("offsets", offsets), ("C", C))
+    _check_result(C, (M, N), out_dtype, A, beta)
+    op = capi.SGEMM_OP_T if trans_b else capi.SGEMM_OP_N
+    operands = (A.data_ptr(), lda, B.data_ptr(), ldb, sb if held > 1 else 0)
+
+    def call(h):
+        out, code_c, ldc = _result(C, (M, N), out_dtype, device)
+        args = (code, op, groups, M, N, K, alpha, *operands, offsets.data_ptr(), beta, out.data_ptr(), ldc, code_c)
+        _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped(*args, ws, size, h),
+                        lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *operands))
+        return out
+    return _run(device, stream, call)
 
 
 def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
@@ -371,42 +388,37 @@ def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=No
     A's type.  An empty group gives beta * C[g].  With C = A @ B[g] per group,
     dB = sgemm_grouped_wgrad(A, dC, offsets); for weights stored [G,N,K]
     (trans_b) the operands change places."""
-    import torch
     groups = _offsets(offsets)
-    M, K, lda, _ = _mat(A, "A", _inputs16())
-    M2, N, ldd, _ = _mat(D, "D", _inputs16())
-    if A.dim() != 2 or D.dim() != 2:
-        raise ValueError("A and D must be 2-D")
-    if D.dtype != A.dtype:
-        raise TypeError(f"A is {A.dtype} but D is {D.dtype}")
+    code, M, K, lda = _rows16(A, "A")
+    _, M2, N, ldd = _rows16(D, "D")
+    _same_type(A, "A", D, "D")
     if M2 != M:
         raise ValueError(f"A has {M} rows, D has {M2}")
-    device = _one_device(("A", A), ("D", D), ("offsets", offsets), ("C", C))
-    with _On(device, stream) as h:
-        C = _result(C, (groups, K, N), out_dtype, torch.float32, (torch.float32, A.dtype), beta, device)
-        _, _, ldc, sc = _mat(C, "C", (C.dtype,))
-        a_args = (A.data_ptr(), lda, D.data_ptr(), ldd)
-        args = (_codes()[A.dtype], groups, M, N, K, float(alpha), *a_args, offsets.data_ptr(), float(beta),
-                C.data_ptr(), ldc, sc, _codes()[C.dtype])
-        _with_workspace(lambda ws, size: capi.sgemm_lowp_grouped_wgrad(*args, ws, size, h),
-                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(M, N, K, *a_args), device)
-    return C
+    device = _one_device(A, ("D", D), ("offsets", offsets), ("C", C))
+    _check_result(C, (groups, K, N), out_dtype, A, beta)
+    operands = (A.data_ptr(), lda, D.data_ptr(), ldd)
+
+    def call(h):
+        out, code_c, ldc = _result(C, (groups, K, N), out_dtype, device)
+        args = (code, groups, M, N, K, alpha, *operands, offsets.data_ptr(), beta, out.data_ptr(), ldc,
+                out.stride(0) if groups > 1 else 0, code_c)
+        _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped_wgrad(*args, ws, size, h),
+                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(M, N, K, *operands))
+        return out
+    return _run(device, stream, call)
 
 
 def _xent_args(X, W, target):
     import torch
-    if X.dim() != 2 or W.dim() != 2:
-        raise ValueError("X and W must be 2-D")
-    M, K, ldx, _ = _mat(X, "X", _inputs16())
-    N, K2, ldw, _ = _mat(W, "W", _inputs16())
-    if W.dtype != X.dtype:
-        raise TypeError(f"X is {X.dtype} but W is {W.dtype}")
+    code, M, K, ldx = _rows16(X, "X")
+    _, N, K2, ldw = _rows16(W, "W")
+    _same_type(X, "X", W, "W")
     if K2 != K:
         raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {N}x{K2}")
     if N < 1:
         raise ValueError("W holds no rows")
     _vector(target, "target", torch.int64, M)
-    return M, N, K, ldx, ldw
+    return code, M, N, K, (X.data_ptr(), ldx, W.data_ptr(), ldw)
 
 
 def sgemm_xent(X, W, target, alpha=1.0, ignore_index=-100, stream=None):
@@ -418,17 +430,18 @@ def sgemm_xent(X, W, target, alpha=1.0, ignore_index=-100, stream=None):
     target is ignore_index give 0 in both; any other target outside 0..V-1
     gives a NaN loss."""
     import torch
-    M, N, K, ldx, ldw = _xent_args(X, W, target)
-    device = _one_device(("X", X), ("W", W), ("target", target))
-    with _On(device, stream) as h:
-        loss = torch.empty(M, dtype=torch.float32, device=device)
-        lse = torch.empty(M, dtype=torch.float32, device=device)
-        args = (X.data_ptr(), ldx, W.data_ptr(), ldw)
-        size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 0))
-        keep = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(capi.sgemm_lowp_xent(_codes()[X.dtype], M, N, K, float(alpha), *args, target.data_ptr(),
-                                    int(ignore_index), loss.data_ptr(), lse.data_ptr(), keep.data_ptr(), size, h))
-    return loss, lse
+    code, M, N, K, operands = _xent_args(X, W, target)
+    device = _one_device(X, ("W", W), ("target", target))
+    size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *operands, 0))
+
+    def call(h):
+        out = torch.empty((2, M), dtype=torch.float32, device=device)
+        loss, lse = out.unbind()
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(capi.sgemm_lowp_xent(code, M, N, K, alpha, *operands, target.data_ptr(), ignore_index, loss.data_ptr(),
+                                    lse.data_ptr(), ws.data_ptr(), size, h))
+        return loss, lse
+    return _run(device, stream, call)
 
 
 def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need_dx=True, need_dw=True, stream=None):
@@ -438,28 +451,28 @@ def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need
     dloss float32 [T], or one value ([] or [1]) for all rows.  need_dx /
     need_dw False: None in that place, and no work for it (a frozen W)."""
     import torch
-    M, N, K, ldx, ldw = _xent_args(X, W, target)
+    code, M, N, K, operands = _xent_args(X, W, target)
     _vector(lse, "lse", torch.float32, M)
     if dloss.dtype != torch.float32:
         raise TypeError("dloss must be float32")
-    if dloss.numel() == 1:
+    if dloss.numel() == 1 and dloss.dim() <= 1:
         step = 0
-    elif dloss.dim() == 1 and dloss.shape[0] == M and dloss.stride(0) >= 0:
+    elif dloss.dim() == 1 and dloss.shape[0] == M:
         step = dloss.stride(0)
     else:
         raise ValueError(f"dloss has shape {tuple(dloss.shape)}, expected {(M,)} or one value")
-    device = _one_device(("X", X), ("W", W), ("target", target), ("lse", lse), ("dloss", dloss))
-    with _On(device, stream) as h:
+    device = _one_device(X, ("W", W), ("target", target), ("lse", lse), ("dloss", dloss))
+    size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *operands, 1))
+
+    def call(h):
         dX = torch.empty((M, K), dtype=X.dtype, device=device) if need_dx else None
         dW = torch.empty((N, K), dtype=X.dtype, device=device) if need_dw else None
-        args = (X.data_ptr(), ldx, W.data_ptr(), ldw)
-        size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *args, 1))
-        keep = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(capi.sgemm_lowp_xent_grad(_codes()[X.dtype], M, N, K, float(alpha), *args, target.data_ptr(),
-                                         int(ignore_index), lse.data_ptr(), dloss.data_ptr(), step,
-                                         dX.data_ptr() if need_dx else None, max(K, 1),
-                                         dW.data_ptr() if need_dw else None, max(K, 1), keep.data_ptr(), size, h))
-    return dX, dW
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(capi.sgemm_lowp_xent_grad(code, M, N, K, alpha, *operands, target.data_ptr(), ignore_index,
+                                         lse.data_ptr(), dloss.data_ptr(), step, _address(dX), max(K, 1), _address(dW),
+                                         max(K, 1), ws.data_ptr(), size, h))
+        return dX, dW
+    return _run(device, stream, call)
 
 
 class W4Weight(NamedTuple):
@@ -480,21 +493,23 @@ class W4Weight(NamedTuple):
 
 
 def _w4(W):
-    """(N, checked) of a W4Weight."""
+    """The rows of a W4Weight, its parts checked."""
     import torch
-    if W.group not in (32, 64, 128):
-        raise ValueError(f"group is {W.group}, expected 32, 64 or 128")
-    if W.packed.dtype != torch.uint8 or W.packed.dim() != 2:
+    packed, scales, zeros, K, group = W
+    if group not in (32, 64, 128):
+        raise ValueError(f"group is {group}, expected 32, 64 or 128")
+    if packed.dtype != torch.uint8 or packed.dim() != 2:
         raise TypeError("packed must be a uint8 matrix")
-    if W.scales.dtype not in _inputs16():
-        raise TypeError(f"scales has type {W.scales.dtype}")
-    N, Kp = W.packed.shape[0], (W.K + 127) // 128 * 128
-    if W.zeros is not None and W.zeros.dtype != torch.uint8:
+    if scales.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"scales has type {scales.dtype}")
+    if zeros is not None and zeros.dtype != torch.uint8:
         raise TypeError("zeros must be uint8")
-    for t, name, cols in ((W.packed, "packed", Kp // 2), (W.scales, "scales", Kp // W.group),
-                          (W.zeros, "zeros", Kp // W.group)):
-        if t is not None and (tuple(t.shape) != (N, cols) or not t.is_contiguous()):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected contiguous {(N, cols)}")
+    N, Kp = packed.shape[0], (K + 127) // 128 * 128
+    if packed.shape[1] != Kp // 2 or not packed.is_contiguous():
+        raise ValueError(f"packed has shape {tuple(packed.shape)}, expected contiguous {(N, Kp // 2)}")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t is not None and (t.shape != (N, Kp // group) or not t.is_contiguous()):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected contiguous {(N, Kp // group)}")
     return N
 
 
@@ -509,25 +524,24 @@ def sgemm_w4(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     X [M,K] bfloat16 or float16, any M from a single token to a prompt; the
     scales are of X's type.  C [M,N] is float32 (the default) or of X's
     type."""
-    import torch
     N = _w4(W)
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
-    M, K, ldx, _ = _mat(X, "X", _inputs16())
-    if W.scales.dtype != X.dtype:
-        raise TypeError(f"X is {X.dtype} but the scales are {W.scales.dtype}")
-    if K != W.K:
-        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {N}x{W.K}")
-    device = _one_device(("X", X), ("packed", W.packed), ("scales", W.scales), ("zeros", W.zeros), ("C", C))
-    with _On(device, stream) as h:
-        C = _result(C, (M, N), out_dtype, torch.float32, (torch.float32, X.dtype), beta, device)
-        ldc = _ld(C, "C", (C.dtype,))
-        x, codes = X.data_ptr(), _codes()
-        args = (codes[X.dtype], M, N, K, float(alpha), x, ldx, W.packed.data_ptr(), W.scales.data_ptr(),
-                _address(W.zeros), W.group, float(beta), C.data_ptr(), ldc, codes[C.dtype])
-        _with_workspace(lambda ws, size: capi.sgemm_w4(*args, ws, size, h),
-                        lambda: capi.sgemm_w4_workspace(M, K, x, ldx), device)
-    return C
+    code, M, K, ldx = _rows16(X, "X")
+    packed, scales, zeros, WK, group = W
+    _same_type(X, "X", scales, "scales")
+    if K != WK:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {N}x{WK}")
+    device = _one_device(X, ("packed", packed), ("scales", scales), ("zeros", zeros), ("C", C))
+    _check_result(C, (M, N), out_dtype, X, beta)
+
+    def call(h):
+        out, code_c, ldc = _result(C, (M, N), out_dtype, device)
+        x = X.data_ptr()
+        args = (code, M, N, K, alpha, x, ldx, packed.data_ptr(), scales.data_ptr(), _address(zeros), group, beta,
+                out.data_ptr(), ldc, code_c)
+        _with_workspace(device, lambda ws, size: capi.sgemm_w4(*args, ws, size, h),
+                        lambda: capi.sgemm_w4_workspace(M, K, x, ldx))
+        return out
+    return _run(device, stream, call)
 
 
 def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
@@ -535,29 +549,32 @@ def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
     consecutive k, and with `zeros` a zero point (for groups that lie to one
     side of 0)."""
     import torch
-    if W.dim() != 2:
-        raise ValueError("W must be 2-D")
-    N, K, ldw, _ = _mat(W, "W", _inputs16())
+    code, N, K, ldw = _rows16(W, "W")
     if group not in (32, 64, 128):
         raise ValueError(f"group is {group}, expected 32, 64 or 128")
     Kp = (K + 127) // 128 * 128
-    device = _one_device(("W", W))
-    with _On(device, stream) as h:
+    device = _one_device(W)
+
+    def call(h):
         out = W4Weight(torch.empty((N, Kp // 2), dtype=torch.uint8, device=device),
                        torch.empty((N, Kp // group), dtype=W.dtype, device=device),
                        torch.empty((N, Kp // group), dtype=torch.uint8, device=device) if zeros else None, K, group)
-        _check(capi.sgemm_w4_quantize(_codes()[W.dtype], N, K, W.data_ptr(), ldw, group, out.packed.data_ptr(),
+        _check(capi.sgemm_w4_quantize(code, N, K, W.data_ptr(), ldw, group, out.packed.data_ptr(),
                                       out.scales.data_ptr(), _address(out.zeros), h))
-    return out
+        return out
+    return _run(device, stream, call)
 
 
 def sgemm_w4_dequantize(W, stream=None):
     """The values [N,K] a W4Weight stands for, rounded to its scales' type."""
     import torch
     N = _w4(W)
-    device = _one_device(("packed", W.packed), ("scales", W.scales), ("zeros", W.zeros))
-    with _On(device, stream) as h:
-        out = torch.empty((N, W.K), dtype=W.scales.dtype, device=device)
-        _check(capi.sgemm_w4_dequantize(_codes()[out.dtype], N, W.K, W.packed.data_ptr(), W.scales.data_ptr(),
-                                        _address(W.zeros), W.group, out.data_ptr(), max(W.K, 1), h))
-    return out
+    packed, scales, zeros, K, group = W
+    device = _one_device(packed, ("scales", scales), ("zeros", zeros))
+
+    def call(h):
+        out = torch.empty((N, K), dtype=scales.dtype, device=device)
+        _check(capi.sgemm_w4_dequantize(_codes()[out.dtype], N, K, packed.data_ptr(), scales.data_ptr(),
+                                        _address(zeros), group, out.data_ptr(), max(K, 1), h))
+        return out
+    return _run(device, stream, call)
