@@ -115,63 +115,77 @@ __global__ void __launch_bounds__(T::NT) group_k_kernel(GroupArgs p) {
                               p.alpha, p.beta);
 }
 
+// One 16-byte chunk of dst per thread and step, from rows of any alignment
+// (a 16-byte load needs none on this chip; the copy is bound by memory).
 __global__ void __launch_bounds__(256) pad_rows_kernel(const unsigned short *src, long ld, long stride, int rows,
-                                                       int cols, unsigned short *dst, int rows_out, int chunks) {
+                                                       int cols, unsigned short *dst, int chunks) {
     typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-    const long n = (long)rows_out * chunks;
-    src += blockIdx.y * stride;
-    dst += blockIdx.y * n * 8;
-    for (long q = blockIdx.x * 256L + threadIdx.x; q < n; q += gridDim.x * 256L) {
-        const long r = q / chunks;
-        const int c = (int)(q - r * chunks) * 8;
+    const int r = blockIdx.x;
+    src += blockIdx.y * stride + r * ld;
+    dst += ((long)blockIdx.y * gridDim.x + r) * chunks * 8;
+    for (int q = threadIdx.x; q < chunks; q += 256) {
+        const int c = 8 * q;
         u16x8 v;
+        if (c + 8 <= cols) {
+            __builtin_memcpy(&v, src + c, 16);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = r < rows && c + e < cols ? src[r * ld + c + e] : (unsigned short)0;
+            for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? src[c + e] : (unsigned short)0;
+        }
         reinterpret_cast<u16x8 *>(dst)[q] = v;
     }
 }
 
-hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, int rows_out,
-                    hipStream_t s) {
-    const int chunks = (cols + 7) / 8;
-    const long n = (long)rows_out * chunks;
-    const long blocks = std::min((n + 255) / 256, std::max(4096L / copies, 16L));
-    return launch_k(pad_rows_kernel, dim3((unsigned)blocks, (unsigned)copies), dim3(256), s,
+hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, hipStream_t s) {
+    return launch_k(pad_rows_kernel, dim3((unsigned)rows, (unsigned)copies), dim3(256), s,
                     static_cast<const unsigned short *>(src), ld, stride, rows, cols, static_cast<unsigned short *>(dst),
-                    rows_out, chunks);
+                    (cols + 7) / 8);
 }
 
 namespace {
 
 constexpr int kMaxGroups = 65535;   // launch grid extent of the padded copies
 
-template <class T, bool OUT16>
-hipError_t launch_rows(const GroupArgs &p, bool f16, bool tb, hipStream_t s) {
+#define GROUP_FORMS(KERNEL, ...)                                                                                     \
+    (f16 ? (out16 ? launch_k(KERNEL<T, true, __VA_ARGS__ true>, grid, dim3(T::NT), s, p)                             \
+                  : launch_k(KERNEL<T, true, __VA_ARGS__ false>, grid, dim3(T::NT), s, p))                           \
+         : (out16 ? launch_k(KERNEL<T, false, __VA_ARGS__ true>, grid, dim3(T::NT), s, p)                            \
+                  : launch_k(KERNEL<T, false, __VA_ARGS__ false>, grid, dim3(T::NT), s, p)))
+
+template <class T, bool TB>
+hipError_t launch_rows(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
     const long groups = std::min(p.groups, p.M);
-    const long grid = (p.M + groups * (T::BM - 1)) / T::BM * ((p.N + T::BN - 1) / T::BN);
-    const dim3 g((unsigned)grid), b(T::NT);
-    if (f16) return tb ? launch_k(group_rows_kernel<T, true, true, OUT16>, g, b, s, p)
-                       : launch_k(group_rows_kernel<T, true, false, OUT16>, g, b, s, p);
-    return tb ? launch_k(group_rows_kernel<T, false, true, OUT16>, g, b, s, p)
-              : launch_k(group_rows_kernel<T, false, false, OUT16>, g, b, s, p);
+    const dim3 grid((unsigned)((p.M + groups * (T::BM - 1)) / T::BM * ((p.N + T::BN - 1) / T::BN)));
+    return GROUP_FORMS(group_rows_kernel, TB, );
 }
 
-template <class T, bool OUT16>
-hipError_t launch_k_groups(const GroupArgs &p, bool f16, hipStream_t s) {
+template <class T>
+hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
     const long tiles = (long)((p.K + T::BM - 1) / T::BM) * ((p.N + T::BN - 1) / T::BN);
-    const dim3 g((unsigned)(ceil_to(tiles, 8) * p.groups)), b(T::NT);
-    return f16 ? launch_k(group_k_kernel<T, true, OUT16>, g, b, s, p)
-               : launch_k(group_k_kernel<T, false, OUT16>, g, b, s, p);
+    const dim3 grid((unsigned)(ceil_to(tiles, 8) * p.groups));
+    return GROUP_FORMS(group_k_kernel, );
 }
 
-template <class T>
-hipError_t launch_rows(const GroupArgs &p, bool f16, bool tb, bool out16, hipStream_t s) {
-    return out16 ? launch_rows<T, true>(p, f16, tb, s) : launch_rows<T, false>(p, f16, tb, s);
+// Up to 32 rows per group on average go to the tile of 32 rows, bound by the
+// weights' bytes; else by rounds, with half a tile more per group.
+hipError_t launch_rows(const GroupArgs &p, bool tb, bool f16, bool out16, hipStream_t s) {
+    const double used = std::min(p.groups, p.M), rows = p.M;
+    if (rows / used <= 32) return tb ? launch_rows<Tile32, true>(p, f16, out16, s) : launch_rows<Tile32, false>(p, f16, out16, s);
+    switch (pick_shape(rows / 256 + used / 2, rows / 128 + used / 2, p.N, tb)) {
+        case Shape::k256: return tb ? launch_rows<Tile256, true>(p, f16, out16, s) : launch_rows<Tile256, false>(p, f16, out16, s);
+        case Shape::kTall: return launch_rows<TileTall, true>(p, f16, out16, s);
+        case Shape::kWide: return launch_rows<TileWide, false>(p, f16, out16, s);
+        default: return tb ? launch_rows<Tile128, true>(p, f16, out16, s) : launch_rows<Tile128, false>(p, f16, out16, s);
+    }
 }
 
-template <class T>
-hipError_t launch_k_groups(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
-    return out16 ? launch_k_groups<T, true>(p, f16, s) : launch_k_groups<T, false>(p, f16, s);
+hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
+    const double m256 = (p.K + 255) / 256, m128 = (p.K + 127) / 128;
+    switch (pick_shape(m256 * p.groups, m128 * p.groups, p.N, false)) {
+        case Shape::k256: return launch_wgrad<Tile256>(p, f16, out16, s);
+        case Shape::kWide: return launch_wgrad<TileWide>(p, f16, out16, s);
+        default: return launch_wgrad<Tile128>(p, f16, out16, s);
+    }
 }
 
 bool in_dtype(int d) { return d == SGEMM_DTYPE_BF16 || d == SGEMM_DTYPE_F16; }
@@ -237,23 +251,20 @@ int sgemm_lowp_grouped(int dtype, int op_b, int groups, int M, int N, int K, flo
         char *w = static_cast<char *>(workspace);
         hipError_t e = hipSuccess;
         if (c.a) {
-            e = pad_rows(A, lda, 0, 1, M, K, w, M, s);
+            e = pad_rows(A, lda, 0, 1, M, K, w, s);
             p.A = w;
             p.lda = ceil_to(K, 8);
         }
         if (e == hipSuccess && c.b) {
             const int rows = tb ? N : K, cols = tb ? K : N;
-            e = pad_rows(B, ldb, stride_b, groups, rows, cols, w + c.a, rows, s);
+            e = pad_rows(B, ldb, stride_b, groups, rows, cols, w + c.a, s);
             p.B = w + c.a;
             p.ldb = ceil_to(cols, 8);
             p.strideB = rows * p.ldb;
         }
         if (e != hipSuccess) return hip_status(e, "kernel launch");
     }
-    const long rows = M / groups;           // rows of an average group
-    const hipError_t e = rows <= 32 ? launch_rows<Tile32>(p, f16, tb, out16, s)
-                         : rows <= 512 ? launch_rows<Tile128>(p, f16, tb, out16, s)
-                                       : launch_rows<Tile256>(p, f16, tb, out16, s);
+    const hipError_t e = launch_rows(p, tb, f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
@@ -286,20 +297,18 @@ int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float a
         char *w = static_cast<char *>(workspace);
         hipError_t e = hipSuccess;
         if (c.a) {
-            e = pad_rows(A, lda, 0, 1, M, K, w, M, s);
+            e = pad_rows(A, lda, 0, 1, M, K, w, s);
             p.A = w;
             p.lda = ceil_to(K, 8);
         }
         if (e == hipSuccess && c.b) {
-            e = pad_rows(D, ldd, 0, 1, M, N, w + c.a, M, s);
+            e = pad_rows(D, ldd, 0, 1, M, N, w + c.a, s);
             p.B = w + c.a;
             p.ldb = ceil_to(N, 8);
         }
         if (e != hipSuccess) return hip_status(e, "kernel launch");
     }
-    const long tiles256 = (K + 255L) / 256 * ((N + 255) / 256) * groups;
-    const hipError_t e = tiles256 >= 256 ? launch_k_groups<Tile256>(p, f16, out16, s)
-                                         : launch_k_groups<Tile128>(p, f16, out16, s);
+    const hipError_t e = launch_wgrad(p, f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 

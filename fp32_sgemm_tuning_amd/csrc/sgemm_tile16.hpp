@@ -24,8 +24,32 @@ struct TileShape {
     static constexpr int LDS = NS_ * (BM_ + BN_) * BK_ * 2;
 };
 using Tile32 = TileShape<32, 128, 64, 1, 4, 4, false>;
-using Tile128 = TileShape<128, 128, 64, 2, 4, 4, true>;
+using Tile128 = TileShape<128, 128, 64, 2, 2, 2, false>;     // two workgroups to a compute unit
+using TileWide = TileShape<128, 256, 32, 2, 4, 3, true>;
+using TileTall = TileShape<256, 128, 64, 2, 4, 3, false>;
 using Tile256 = TileShape<256, 256, 32, 2, 4, 4, true>;
+
+// Which of them a product runs on.  Large tiles do more per byte they load,
+// but the last round of tiles over the 256 compute units (512 places for
+// Tile128) is rarely full, so the time goes by rounds: at least one, and on
+// average half a round more than tiles / places.  Microseconds per round and
+// 2048 k, measured on grouped products of 3001 to 16384 rows by 2048 to 5000
+// columns: Tile256 44 (B as stored) or 46 (B transposed), TileWide 27, TileTall
+// 26, Tile128 30 or 31.  (16384 x 4096 x 2048 in 16 groups: Tile256 251 us,
+// TileWide 273, Tile128 300; 3001 x 5000 x 2048 in 5 groups: 79, 56, 61; with
+// B transposed, 16384 x 2048 x 4096: Tile256 277, TileTall 261, Tile128 308.)
+// m256, m128: rows of tiles of either height; tb: B transposed, where
+// TileTall is built, else TileWide is.
+enum class Shape { k32, k128, kWide, kTall, k256 };
+
+inline Shape pick_shape(double m256, double m128, long n, bool tb) {
+    auto rounds = [](double tiles, double places) { return tiles / places + 0.5 > 1 ? tiles / places + 0.5 : 1.0; };
+    const double n256 = (n + 255) / 256, n128 = (n + 127) / 128;
+    const double t256 = rounds(m256 * n256, 256) * (tb ? 46 : 44), t128 = rounds(m128 * n128, 512) * (tb ? 31 : 30),
+                 mixed = tb ? rounds(m256 * n128, 256) * 26 : rounds(m128 * n256, 256) * 27;
+    if (mixed <= t256 && mixed <= t128) return tb ? Shape::kTall : Shape::kWide;
+    return t256 <= t128 ? Shape::k256 : Shape::k128;
+}
 
 // The operands of one tile's product as lowp_accumulate takes them.
 struct Operands16 {
@@ -141,9 +165,8 @@ inline bool chunk_rows(const void *p, long ld, long cols) {     // rows of whole
 }
 
 // dst [copies][rows][cols8] = src [copies][rows][cols] (row length cols8:
-// cols rounded up to whole 16-byte chunks, zeros behind cols); rows from
-// `rows` to `rows_out` are zero.
-hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, int rows_out,
-                    hipStream_t s);
+// cols rounded up to whole 16-byte chunks, zeros behind cols); up to 65535
+// copies.
+hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, hipStream_t s);
 
 }  // namespace sgemm_mi355x

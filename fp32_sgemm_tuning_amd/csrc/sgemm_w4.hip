@@ -621,7 +621,7 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx
     if (copy > 0) {
         if (workspace == nullptr || workspace_bytes < copy || (reinterpret_cast<uintptr_t>(workspace) & 15))
             return SGEMM_STATUS_SCRATCH_TOO_SMALL;
-        const hipError_t e = pad_rows(X, ldx, 0, 1, M, K, workspace, M, s);
+        const hipError_t e = pad_rows(X, ldx, 0, 1, M, K, workspace, s);
         if (e != hipSuccess) return hip_status(e, "kernel launch");
         p.X = static_cast<const char *>(workspace);
         p.ldx = ceil_to(K, 8);

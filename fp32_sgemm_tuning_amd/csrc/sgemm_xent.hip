@@ -227,23 +227,31 @@ __global__ void __launch_bounds__(T::NT) xent_stats_kernel(XentArgs p) {
     }
 }
 
-// Joins the tile columns of 64 rows per block: 16 threads a row take every
-// 16th tile, then a tree of 16.
+// Joins the tile columns of 16 rows per block: 64 threads a row take every
+// 64th tile, four loads at a time, then a tree.
 __global__ void __launch_bounds__(1024) xent_join_kernel(XentArgs p, int tiles_n) {
-    __shared__ float2 red[16][64];
-    const int r = threadIdx.x & 63, slice = threadIdx.x >> 6, row = blockIdx.x * 64 + r;
+    __shared__ float2 red[64][16];
+    const int r = threadIdx.x & 15, slice = threadIdx.x >> 4, row = blockIdx.x * 16 + r;
     const bool live = row < p.head->rows;
     auto join = [](float2 a, float2 b) {
         const float top = fmaxf(a.x, b.x), base = top == -__builtin_inff() ? 0.f : top;
         return make_float2(top, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
     };
-    float2 a = make_float2(-__builtin_inff(), 0.f);
+    const float2 none = make_float2(-__builtin_inff(), 0.f);
+    float2 a = none;
     if (live)
-        for (int t = slice; t < tiles_n; t += 16) a = join(a, p.part[(long)t * p.M + row]);
+        for (int t = slice; t < tiles_n; t += 256) {
+            float2 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = t + 64 * i < tiles_n ? p.part[(long)(t + 64 * i) * p.M + row] : none;
+            a = join(a, join(join(b[0], b[1]), join(b[2], b[3])));
+        }
     red[slice][r] = a;
-    __syncthreads();
+    for (int half = 32; half; half >>= 1) {
+        __syncthreads();
+        if (slice < half) red[slice][r] = a = join(a, red[slice + half][r]);
+    }
     if (slice != 0 || !live) return;
-    for (int s = 1; s < 16; ++s) a = join(a, red[s][r]);
     const float lse = a.x + logf(a.y);
     const int to = p.map[row];
     p.lse[to] = lse;
@@ -283,8 +291,9 @@ __global__ void __launch_bounds__(T::NT) xent_dlogits_kernel(XentArgs p) {
     }
 }
 
-// dX: sum += P * piece of W; the last piece scales, rounds and puts each row
-// in its place.
+// dX: sum += P * piece of W, block y of gridDim.y over its share of the piece
+// into a sum of its own.  With one share the last piece scales, rounds and
+// puts each row in its place; else xent_dx_join_kernel does.
 template <class T, bool F16>
 __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, int last) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
@@ -294,17 +303,20 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
     int tm, tn;
     raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
     const int m0 = tm * T::BM, n0 = tn * T::BN;
-    const Operands16 q = {p.P, p.W + 2L * p.n_first * p.ldw, p.ldp, p.ldw, rows, p.K, p.n_count};
+    const int part = (p.n_count + 64 * (int)gridDim.y - 1) / (64 * (int)gridDim.y) * 64;       // whole K tiles
+    const int v0 = min(part * (int)blockIdx.y, p.n_count), v1 = min(v0 + part, p.n_count);
+    const Operands16 q = {p.P + 2L * v0, p.W + 2L * (p.n_first + v0) * p.ldw, p.ldp, p.ldw, rows, p.K, v1 - v0};
     f32x4 acc[T::MI][T::NB];
     accumulate16<T, F16, false, false>(q, m0, n0, lds, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float scale = p.alpha * p.head->gmax;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0, place = last && gridDim.y == 1;
+    float *sums = p.sum + (long)blockIdx.y * p.M * p.ldxc;
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
         const int row = m0 + wave / T::WAVES_N * T::WM + mi * 16 + (lane & 15);
         if (row >= rows) continue;
-        float *sum = p.sum + row * p.ldxc;                    // whole chunks of columns
+        float *sum = sums + row * p.ldxc;                     // whole chunks of columns
         char *out = p.dX + 2 * p.map[row] * p.lddx;
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) {
@@ -312,9 +324,26 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
             if (col >= p.K) continue;
             f32x4 v = acc[mi][nb];
             if (!first) v += *reinterpret_cast<const f32x4 *>(sum + col);
-            if (last) store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
+            if (place) store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
             else *reinterpret_cast<f32x4 *>(sum + col) = v;
         }
+    }
+}
+
+// The shares' sums, in order, scaled, rounded and put in place: one block per
+// listed row.
+template <bool F16>
+__global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int shares) {
+    const int row = blockIdx.x;
+    if (row >= p.head->rows) return;
+    const float scale = p.alpha * p.head->gmax;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0;
+    char *out = p.dX + 2 * p.map[row] * p.lddx;
+    for (int col = 4 * threadIdx.x; col < p.K; col += 1024) {
+        const float *sum = p.sum + row * p.ldxc + col;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(sum);
+        for (int y = 1; y < shares; ++y) v += *reinterpret_cast<const f32x4 *>(sum + (long)y * p.M * p.ldxc);
+        store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
     }
 }
 
@@ -342,6 +371,23 @@ long piece_columns(int M, int N) {
     const long most = std::max(kPieceBytes / 2 / std::max(M, 1) / 256 * 256, 1024L);
     const long pieces = (N + most - 1) / most;
     return ceil_to((N + pieces - 1) / pieces, 256);
+}
+
+// The tile of dX and into how many shares the vocabulary (of a piece of
+// `count` columns) is cut: the grid of M x K outputs rarely fills the chip and
+// its products are long, so as many shares as fill it, of 512 columns at
+// least (1331 rows of 2048 by 50021 columns: 444 us on 128 x 128 tiles
+// unshared, 290 on 256 x 256 in four shares).
+struct DxPlan {
+    Shape shape;
+    int shares;
+};
+
+DxPlan dx_plan(int M, int K, int count) {
+    const Shape shape = M <= 32 ? Shape::k32 : M <= 128 ? Shape::k128 : Shape::k256;
+    const int bm = M <= 32 ? 32 : M <= 128 ? 128 : 256, bn = M <= 128 ? 128 : 256;
+    const long tiles = (M + bm - 1L) / bm * ((K + bn - 1L) / bn), places = M <= 128 ? 512 : 256;
+    return {shape, (int)std::max(1L, std::min(places / std::max(tiles, 1L), count / 512L))};
 }
 
 // The workspace, laid out from `base` (null: only its size is wanted).
@@ -372,7 +418,8 @@ long xent_layout(XentArgs &p, void *workspace, bool grad, char *&Wc) {
         p.lsec = reinterpret_cast<float *>(l.take(4L * p.M));
         p.ldp = piece_columns(p.M, p.N);
         p.P = l.take(2L * p.M * p.ldp);
-        p.sum = p.ldp < p.N ? reinterpret_cast<float *>(l.take(4L * p.M * p.ldxc)) : nullptr;
+        const int shares = dx_plan(p.M, p.K, (int)std::min((long)p.N, p.ldp)).shares;
+        p.sum = p.ldp < p.N || shares > 1 ? reinterpret_cast<float *>(l.take(4L * shares * p.M * p.ldxc)) : nullptr;
     }
     return l.at;
 }
@@ -392,13 +439,14 @@ bool scratch_ok(long need, const void *workspace, long long bytes) {
 
 unsigned tiles(long m, long n, int bm, int bn) { return (unsigned)((m + bm - 1) / bm * ((n + bn - 1) / bn)); }
 
-// The tile of a product of at most m rows: few rows take the tile that
-// wastes least, many the one that reads least.
-int tile_of(long m, long n) { return m <= 32 ? 0 : tiles(m, n, 256, 256) >= 256 ? 2 : 1; }
+Shape logits_shape(int M, int N) {
+    return M <= 32 ? Shape::k32 : pick_shape((M + 255) / 256, (M + 127) / 128, N, true);
+}
 
-#define XENT_LAUNCH(KERNEL, T, GRID, ...) \
-    (f16 ? launch_k(KERNEL<T, true>, dim3(GRID), dim3(T::NT), s, __VA_ARGS__) \
-         : launch_k(KERNEL<T, false>, dim3(GRID), dim3(T::NT), s, __VA_ARGS__))
+// A kernel of tile T over at most m x n outputs, `shares` blocks each.
+#define XENT_LAUNCH(KERNEL, T, m, n, shares, ...)                                                                  \
+    (f16 ? launch_k(KERNEL<T, true>, dim3(tiles(m, n, T::BM, T::BN), shares), dim3(T::NT), s, __VA_ARGS__)         \
+         : launch_k(KERNEL<T, false>, dim3(tiles(m, n, T::BM, T::BN), shares), dim3(T::NT), s, __VA_ARGS__))
 
 }  // namespace
 }  // namespace sgemm_mi355x
@@ -450,17 +498,18 @@ int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha, const void *X, 
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = launch_k(xent_compact_kernel<false>, dim3((M + kCompactRows - 1) / kCompactRows), dim3(256), s, p);
     if (e == hipSuccess && Wc != nullptr) {
-        e = pad_rows(W, ldw, 0, 1, N, K, Wc, N, s);
+        e = pad_rows(W, ldw, 0, 1, N, K, Wc, s);
         p.W = Wc;
         p.ldw = p.ldxc;
     }
-    const int tile = tile_of(M, N);
+    const Shape shape = logits_shape(M, N);
     if (e == hipSuccess)
-        e = tile == 0   ? XENT_LAUNCH(xent_stats_kernel, Tile32, tiles(M, N, 32, 128), p)
-            : tile == 1 ? XENT_LAUNCH(xent_stats_kernel, Tile128, tiles(M, N, 128, 128), p)
-                        : XENT_LAUNCH(xent_stats_kernel, Tile256, tiles(M, N, 256, 256), p);
-    if (e == hipSuccess)
-        e = launch_k(xent_join_kernel, dim3((M + 63) / 64), dim3(1024), s, p, (N + (tile == 2 ? 255 : 127)) / (tile == 2 ? 256 : 128));
+        e = shape == Shape::k32     ? XENT_LAUNCH(xent_stats_kernel, Tile32, M, N, 1, p)
+            : shape == Shape::k128  ? XENT_LAUNCH(xent_stats_kernel, Tile128, M, N, 1, p)
+            : shape == Shape::kTall ? XENT_LAUNCH(xent_stats_kernel, TileTall, M, N, 1, p)
+                                    : XENT_LAUNCH(xent_stats_kernel, Tile256, M, N, 1, p);
+    const int bn = shape == Shape::k256 ? 256 : 128;
+    if (e == hipSuccess) e = launch_k(xent_join_kernel, dim3((M + 15) / 16), dim3(1024), s, p, (N + bn - 1) / bn);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
@@ -501,29 +550,36 @@ int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void
     // (M == 0: one block, which finds no row; dW is then zeros)
     hipError_t e = launch_k(xent_compact_kernel<true>, dim3(std::max((M + kCompactRows - 1) / kCompactRows, 1)), dim3(256), s, p);
     if (e == hipSuccess && Wc != nullptr) {
-        e = pad_rows(W, ldw, 0, 1, N, K, Wc, N, s);
+        e = pad_rows(W, ldw, 0, 1, N, K, Wc, s);
         p.W = Wc;
         p.ldw = p.ldxc;
     }
+    const DxPlan plan = dx_plan(M, K, (int)std::min((long)N, p.ldp));
     for (p.n_first = 0; p.n_first < N && e == hipSuccess; p.n_first += (int)p.ldp) {
         p.n_count = (int)std::min((long)N - p.n_first, p.ldp);
         const int first = p.n_first == 0, last = p.n_first + p.n_count == N;
         if (M > 0) {
-            const int tile = tile_of(M, p.n_count);
-            e = tile == 0   ? XENT_LAUNCH(xent_dlogits_kernel, Tile32, tiles(M, p.n_count, 32, 128), p)
-                : tile == 1 ? XENT_LAUNCH(xent_dlogits_kernel, Tile128, tiles(M, p.n_count, 128, 128), p)
-                            : XENT_LAUNCH(xent_dlogits_kernel, Tile256, tiles(M, p.n_count, 256, 256), p);
+            const Shape shape = logits_shape(M, p.n_count);
+            e = shape == Shape::k32     ? XENT_LAUNCH(xent_dlogits_kernel, Tile32, M, p.n_count, 1, p)
+                : shape == Shape::k128  ? XENT_LAUNCH(xent_dlogits_kernel, Tile128, M, p.n_count, 1, p)
+                : shape == Shape::kTall ? XENT_LAUNCH(xent_dlogits_kernel, TileTall, M, p.n_count, 1, p)
+                                        : XENT_LAUNCH(xent_dlogits_kernel, Tile256, M, p.n_count, 1, p);
         }
         if (e == hipSuccess && M > 0 && dX != nullptr) {
-            const int tile = tile_of(M, K);
-            e = tile == 0   ? XENT_LAUNCH(xent_dx_kernel, Tile32, tiles(M, K, 32, 128), p, first, last)
-                : tile == 1 ? XENT_LAUNCH(xent_dx_kernel, Tile128, tiles(M, K, 128, 128), p, first, last)
-                            : XENT_LAUNCH(xent_dx_kernel, Tile256, tiles(M, K, 256, 256), p, first, last);
+            e = plan.shape == Shape::k32    ? XENT_LAUNCH(xent_dx_kernel, Tile32, M, K, plan.shares, p, first, last)
+                : plan.shape == Shape::k128 ? XENT_LAUNCH(xent_dx_kernel, Tile128, M, K, plan.shares, p, first, last)
+                                            : XENT_LAUNCH(xent_dx_kernel, Tile256, M, K, plan.shares, p, first, last);
         }
-        if (e == hipSuccess && dW != nullptr)
-            e = tile_of(p.n_count, K) == 2 ? XENT_LAUNCH(xent_dw_kernel, Tile256, tiles(p.n_count, K, 256, 256), p)
-                                           : XENT_LAUNCH(xent_dw_kernel, Tile128, tiles(p.n_count, K, 128, 128), p);
+        if (e == hipSuccess && dW != nullptr) {
+            const Shape shape = pick_shape((p.n_count + 255) / 256, (p.n_count + 127) / 128, K, false);
+            e = shape == Shape::k128    ? XENT_LAUNCH(xent_dw_kernel, Tile128, p.n_count, K, 1, p)
+                : shape == Shape::kWide ? XENT_LAUNCH(xent_dw_kernel, TileWide, p.n_count, K, 1, p)
+                                        : XENT_LAUNCH(xent_dw_kernel, Tile256, p.n_count, K, 1, p);
+        }
     }
+    if (e == hipSuccess && M > 0 && dX != nullptr && plan.shares > 1)
+        e = f16 ? launch_k(xent_dx_join_kernel<true>, dim3(M), dim3(256), s, p, plan.shares)
+                : launch_k(xent_dx_join_kernel<false>, dim3(M), dim3(256), s, p, plan.shares);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
