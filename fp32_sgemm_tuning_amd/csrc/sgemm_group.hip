@@ -6,7 +6,7 @@
 //   group_k_kernel      C[g] = alpha * A[rows of g]^T * D[rows of g] + beta * C[g]
 //
 // Both run the K loop of sgemm_lowp.hpp on one block tile.  The host does
-// not know the groups' sizes, so the first kernel's grid covers the most
+// not know the groups' sizes, so the first kernels' grids cover the most
 // tiles that any split of the rows can have, floor((M + g*(BM-1)) / BM) tile
 // rows for g = min(groups, M) groups, and a workgroup finds its tile from
 // the offsets (one wave-wide scan of the groups' tile counts); workgroups
@@ -38,59 +38,89 @@ __device__ __forceinline__ int wave_sum(int v) {
     return v;
 }
 
-// The group and the tile of workgroup `bid`, the groups' tiles one after
-// another; false past the last.  Wave-uniform.
+// The groups' tiles of BM rows one after another: how many there are, and the
+// group and the tile of number `id`.  Wave-uniform.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const GroupArgs &p, int tiles_n, int bid, int &g, int &lo, int &rows, int &tm,
-                                          int &tn) {
-    const int lane = threadIdx.x & 63;
-    auto tiles = [&](int base) {
+struct TileList {
+    const GroupArgs &p;
+    int tiles_n, first, total;                  // first: tile rows of group `lane`
+    __device__ __forceinline__ int tile_rows(int g) const {
         int l = 0, r = 0;
-        if (base + lane < p.groups) group_rows(p.offsets, base + lane, p.M, l, r);
+        if (g < p.groups) group_rows(p.offsets, g, p.M, l, r);
         return (r + BM - 1) / BM;
-    };
-    const int first = tiles(0);
-    int total = wave_sum(first);
-    for (int base = 64; base < p.groups; base += 64) total += wave_sum(tiles(base));
-    total = __builtin_amdgcn_readfirstlane(total) * tiles_n;
-    if (bid >= total) return false;
-    int id = xcd_run(bid, total);
-    for (int base = 0;; base += 64) {
-        const int mine = base ? tiles(base) : first;
-        int upto = mine;                                    // tile rows up to this lane's group
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int below = __shfl_up(upto, d);
-            if (lane >= d) upto += below;
-        }
-        const unsigned long past = __ballot(id < upto * tiles_n);
-        if (past) {
-            const int at = __builtin_ctzl(past);
-            const int count = __builtin_amdgcn_readlane(mine, at);
-            id -= (__builtin_amdgcn_readlane(upto, at) - count) * tiles_n;
-            g = base + at;
-            group_rows(p.offsets, g, p.M, lo, rows);
-            g = __builtin_amdgcn_readfirstlane(g);
-            lo = __builtin_amdgcn_readfirstlane(lo);
-            rows = __builtin_amdgcn_readfirstlane(rows);
-            raster(id, count, tiles_n, tm, tn);
-            return true;
-        }
-        id -= __builtin_amdgcn_readlane(upto, 63) * tiles_n;
     }
+    __device__ __forceinline__ TileList(const GroupArgs &args, int bn) : p(args), tiles_n((args.N + bn - 1) / bn) {
+        const int lane = threadIdx.x & 63;
+        first = tile_rows(lane);
+        int sum = wave_sum(first);
+        for (int base = 64; base < p.groups; base += 64) sum += wave_sum(tile_rows(base + lane));
+        total = __builtin_amdgcn_readfirstlane(sum) * tiles_n;
+    }
+    // (id < total)
+    __device__ __forceinline__ void find(int id, int &g, int &lo, int &rows, int &tm, int &tn) const {
+        const int lane = threadIdx.x & 63;
+        for (int base = 0; base < p.groups; base += 64) {
+            const int mine = base ? tile_rows(base + lane) : first;
+            int upto = mine;                                    // tile rows up to this lane's group
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int below = __shfl_up(upto, d);
+                if (lane >= d) upto += below;
+            }
+            const unsigned long past = __ballot(id < upto * tiles_n);
+            if (past) {
+                const int at = __builtin_ctzl(past);
+                const int count = __builtin_amdgcn_readlane(mine, at);
+                id -= (__builtin_amdgcn_readlane(upto, at) - count) * tiles_n;
+                group_rows(p.offsets, base + at, p.M, lo, rows);
+                g = __builtin_amdgcn_readfirstlane(base + at);
+                lo = __builtin_amdgcn_readfirstlane(lo);
+                rows = __builtin_amdgcn_readfirstlane(rows);
+                raster(id, count, tiles_n, tm, tn);
+                return;
+            }
+            id -= __builtin_amdgcn_readlane(upto, 63) * tiles_n;
+        }
+    }
+};
+
+template <class T, bool F16, bool TB, bool OUT16>
+__device__ __forceinline__ void group_tile(const GroupArgs &p, char *lds, int g, int lo, int rows, int m0, int n0) {
+    const Operands16 q = {p.A + 2L * lo * p.lda, p.B + 2L * g * p.strideB, p.lda, p.ldb, rows, p.N, p.K};
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, false, TB>(q, m0, n0, lds, acc);
+    store_tile<T, F16, OUT16>(acc, m0, n0, rows, p.N, p.C + (OUT16 ? 2L : 4L) * lo * p.ldc, p.ldc, p.alpha, p.beta);
 }
 
+// One tile shape throughout.
 template <class T, bool F16, bool TB, bool OUT16>
 __global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const int tiles_n = (p.N + T::BN - 1) / T::BN;
-    int g, lo, rows, tm, tn;
-    if (!find_tile<T::BM>(p, tiles_n, blockIdx.x, g, lo, rows, tm, tn)) return;
-    const Operands16 q = {p.A + 2L * lo * p.lda, p.B + 2L * g * p.strideB, p.lda, p.ldb, rows, p.N, p.K};
-    f32x4 acc[T::MI][T::NB];
-    accumulate16<T, F16, false, TB>(q, tm * T::BM, tn * T::BN, lds, acc);
-    store_tile<T, F16, OUT16>(acc, tm * T::BM, tn * T::BN, rows, p.N, p.C + (OUT16 ? 2L : 4L) * lo * p.ldc, p.ldc, p.alpha,
-                              p.beta);
+    const TileList<T::BM> list(p, T::BN);
+    if ((int)blockIdx.x >= list.total) return;
+    int g = 0, lo = 0, rows = 0, tm = 0, tn = 0;
+    list.find(xcd_run(blockIdx.x, list.total), g, lo, rows, tm, tn);
+    group_tile<T, F16, TB, OUT16>(p, lds, g, lo, rows, tm * T::BM, tn * T::BN);
+}
+
+// Tiles of 256 x 256 with a finer last round.
+template <bool F16, bool TB, bool OUT16>
+struct GroupBody {
+    const TileList<256> list;
+    template <class T>
+    __device__ __forceinline__ void tile(char *lds, int id, int sub) const {
+        int g = 0, lo = 0, rows = 0, tm = 0, tn = 0, m0, n0;
+        list.find(id, g, lo, rows, tm, tn);
+        part_corner<T>(tm, tn, sub, m0, n0);
+        if (m0 < rows && n0 < list.p.N) group_tile<T, F16, TB, OUT16>(list.p, lds, g, lo, rows, m0, n0);
+    }
+};
+
+template <bool F16, bool TB, bool OUT16>
+__global__ void __launch_bounds__(512) group_mixed_kernel(GroupArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[Mixed<TB>::LDS];
+    const GroupBody<F16, TB, OUT16> body{TileList<256>(p, 256)};
+    Mixed<TB>::run(body, lds, body.list.total);
 }
 
 // A [M][K] and B [M][N] by rows; C[g] is K x N, the sum runs over the
@@ -146,46 +176,55 @@ namespace {
 
 constexpr int kMaxGroups = 65535;   // launch grid extent of the padded copies
 
-#define GROUP_FORMS(KERNEL, ...)                                                                                     \
-    (f16 ? (out16 ? launch_k(KERNEL<T, true, __VA_ARGS__ true>, grid, dim3(T::NT), s, p)                             \
-                  : launch_k(KERNEL<T, true, __VA_ARGS__ false>, grid, dim3(T::NT), s, p))                           \
-         : (out16 ? launch_k(KERNEL<T, false, __VA_ARGS__ true>, grid, dim3(T::NT), s, p)                            \
-                  : launch_k(KERNEL<T, false, __VA_ARGS__ false>, grid, dim3(T::NT), s, p)))
+// KERNEL<before..., F16, after..., OUT16>
+#define GROUP_FORMS(KERNEL, NT, BEFORE, AFTER)                                                  \
+    (f16 ? (out16 ? launch_k(KERNEL<BEFORE true, AFTER true>, grid, dim3(NT), s, p)             \
+                  : launch_k(KERNEL<BEFORE true, AFTER false>, grid, dim3(NT), s, p))           \
+         : (out16 ? launch_k(KERNEL<BEFORE false, AFTER true>, grid, dim3(NT), s, p)            \
+                  : launch_k(KERNEL<BEFORE false, AFTER false>, grid, dim3(NT), s, p)))
+#define COMMA ,
+
+// The most tiles of bm x bn that any split of the rows into groups can have.
+long most_tiles(const GroupArgs &p, int bm, int bn) {
+    const long groups = std::min(p.groups, p.M);
+    return (p.M + groups * (bm - 1)) / bm * ((p.N + bn - 1) / bn);
+}
 
 template <class T, bool TB>
 hipError_t launch_rows(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
-    const long groups = std::min(p.groups, p.M);
-    const dim3 grid((unsigned)((p.M + groups * (T::BM - 1)) / T::BM * ((p.N + T::BN - 1) / T::BN)));
-    return GROUP_FORMS(group_rows_kernel, TB, );
+    const dim3 grid((unsigned)most_tiles(p, T::BM, T::BN));
+    return GROUP_FORMS(group_rows_kernel, T::NT, T COMMA, TB COMMA);
+}
+
+template <bool TB>
+hipError_t launch_mixed(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
+    const dim3 grid((unsigned)mixed_grid(most_tiles(p, 256, 256)));
+    return GROUP_FORMS(group_mixed_kernel, 512, , TB COMMA);
 }
 
 template <class T>
 hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
     const long tiles = (long)((p.K + T::BM - 1) / T::BM) * ((p.N + T::BN - 1) / T::BN);
     const dim3 grid((unsigned)(ceil_to(tiles, 8) * p.groups));
-    return GROUP_FORMS(group_k_kernel, );
+    return GROUP_FORMS(group_k_kernel, T::NT, T COMMA, );
 }
 
-// Up to 32 rows per group on average go to the tile of 32 rows, bound by the
-// weights' bytes; else by rounds, with half a tile more per group.
+// By the rows of an average group: tiles of 32 rows are bound by the weights'
+// bytes, tiles of 128 leave less of a small group empty, tiles of 256 load
+// least.
 hipError_t launch_rows(const GroupArgs &p, bool tb, bool f16, bool out16, hipStream_t s) {
-    const double used = std::min(p.groups, p.M), rows = p.M;
-    if (rows / used <= 32) return tb ? launch_rows<Tile32, true>(p, f16, out16, s) : launch_rows<Tile32, false>(p, f16, out16, s);
-    switch (pick_shape(rows / 256 + used / 2, rows / 128 + used / 2, p.N, tb)) {
-        case Shape::k256: return tb ? launch_rows<Tile256, true>(p, f16, out16, s) : launch_rows<Tile256, false>(p, f16, out16, s);
-        case Shape::kTall: return launch_rows<TileTall, true>(p, f16, out16, s);
-        case Shape::kWide: return launch_rows<TileWide, false>(p, f16, out16, s);
-        default: return tb ? launch_rows<Tile128, true>(p, f16, out16, s) : launch_rows<Tile128, false>(p, f16, out16, s);
-    }
+    const int rows = p.M / std::min(p.groups, p.M);
+    if (rows <= 32) return tb ? launch_rows<Tile32, true>(p, f16, out16, s) : launch_rows<Tile32, false>(p, f16, out16, s);
+    if (rows <= 128) return tb ? launch_rows<Tile128, true>(p, f16, out16, s) : launch_rows<Tile128, false>(p, f16, out16, s);
+    return tb ? launch_mixed<true>(p, f16, out16, s) : launch_mixed<false>(p, f16, out16, s);
 }
 
+// Fewer than a round of the large tiles: the next smaller that fill it.
 hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
-    const double m256 = (p.K + 255) / 256, m128 = (p.K + 127) / 128;
-    switch (pick_shape(m256 * p.groups, m128 * p.groups, p.N, false)) {
-        case Shape::k256: return launch_wgrad<Tile256>(p, f16, out16, s);
-        case Shape::kWide: return launch_wgrad<TileWide>(p, f16, out16, s);
-        default: return launch_wgrad<Tile128>(p, f16, out16, s);
-    }
+    const long n256 = (p.N + 255) / 256, m128 = (p.K + 127) / 128;
+    if ((p.K + 255) / 256 * n256 * p.groups >= 256) return launch_wgrad<Tile256>(p, f16, out16, s);
+    if (m128 * n256 * p.groups >= 256) return launch_wgrad<TileWide>(p, f16, out16, s);
+    return launch_wgrad<Tile128>(p, f16, out16, s);
 }
 
 bool in_dtype(int d) { return d == SGEMM_DTYPE_BF16 || d == SGEMM_DTYPE_F16; }

@@ -27,29 +27,8 @@ using Tile32 = TileShape<32, 128, 64, 1, 4, 4, false>;
 using Tile128 = TileShape<128, 128, 64, 2, 2, 2, false>;     // two workgroups to a compute unit
 using TileWide = TileShape<128, 256, 32, 2, 4, 3, true>;
 using TileTall = TileShape<256, 128, 64, 2, 4, 3, false>;
+using TileQuarter = TileShape<128, 128, 64, 2, 4, 4, true>;
 using Tile256 = TileShape<256, 256, 32, 2, 4, 4, true>;
-
-// Which of them a product runs on.  Large tiles do more per byte they load,
-// but the last round of tiles over the 256 compute units (512 places for
-// Tile128) is rarely full, so the time goes by rounds: at least one, and on
-// average half a round more than tiles / places.  Microseconds per round and
-// 2048 k, measured on grouped products of 3001 to 16384 rows by 2048 to 5000
-// columns: Tile256 44 (B as stored) or 46 (B transposed), TileWide 27, TileTall
-// 26, Tile128 30 or 31.  (16384 x 4096 x 2048 in 16 groups: Tile256 251 us,
-// TileWide 273, Tile128 300; 3001 x 5000 x 2048 in 5 groups: 79, 56, 61; with
-// B transposed, 16384 x 2048 x 4096: Tile256 277, TileTall 261, Tile128 308.)
-// m256, m128: rows of tiles of either height; tb: B transposed, where
-// TileTall is built, else TileWide is.
-enum class Shape { k32, k128, kWide, kTall, k256 };
-
-inline Shape pick_shape(double m256, double m128, long n, bool tb) {
-    auto rounds = [](double tiles, double places) { return tiles / places + 0.5 > 1 ? tiles / places + 0.5 : 1.0; };
-    const double n256 = (n + 255) / 256, n128 = (n + 127) / 128;
-    const double t256 = rounds(m256 * n256, 256) * (tb ? 46 : 44), t128 = rounds(m128 * n128, 512) * (tb ? 31 : 30),
-                 mixed = tb ? rounds(m256 * n128, 256) * 26 : rounds(m128 * n256, 256) * 27;
-    if (mixed <= t256 && mixed <= t128) return tb ? Shape::kTall : Shape::kWide;
-    return t256 <= t128 ? Shape::k256 : Shape::k128;
-}
 
 // The operands of one tile's product as lowp_accumulate takes them.
 struct Operands16 {
@@ -81,6 +60,46 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int &tm
     const int rows = min(tiles_m - g * GM, GM);
     tm = g * GM + in % rows;
     tn = in / rows;
+}
+
+// A grid of `total` tiles of 256 x 256 over the 256 compute units, one
+// workgroup each: whole rounds run on Tile256, and a last round that fills at
+// most half of the chip is cut finer, in two (TileWide, or with B transposed
+// TileTall) or, below a quarter, in four, so that its tiles take 0.6 or 0.45
+// of a round instead of a whole one.  body.tile<T>(lds, id, sub) does part
+// `sub` of tile number `id`; the number of tiles need only be known here.
+// Launched with mixed_grid(largest total) workgroups of 512 threads.
+template <bool TB>
+struct Mixed {
+    using Half = typename std::conditional<TB, TileTall, TileWide>::type;
+    static constexpr int NT = 512;
+    static constexpr int LDS = Half::LDS > Tile256::LDS ? Half::LDS : Tile256::LDS;
+    static_assert(Tile256::NT == NT && Half::NT == NT && TileQuarter::NT == NT && TileQuarter::LDS <= LDS, "one launch");
+    template <class Body>
+    static __device__ __forceinline__ void run(const Body &body, char *lds, int total) {
+        const int bid = blockIdx.x, whole = total & ~255, rest = total - whole, k = bid - whole;
+        if (k < 0) body.template tile<Tile256>(lds, xcd_run(bid, whole), 0);
+        else if (rest > 128) {
+            if (k < rest) body.template tile<Tile256>(lds, whole + xcd_run(k, rest), 0);
+        } else if (rest > 64) {
+            if (k >= 2 * rest) return;
+            const int at = xcd_run(k, 2 * rest);
+            body.template tile<Half>(lds, whole + (at >> 1), at & 1);
+        } else if (k < 4 * rest) {
+            const int at = xcd_run(k, 4 * rest);
+            body.template tile<TileQuarter>(lds, whole + (at >> 2), at & 3);
+        }
+    }
+};
+
+inline long mixed_grid(long total) { return total + 256; }   // (whole rounds, and 256 at most behind them)
+
+// Corner of part `sub` of the 256 x 256 tile (tm, tn) for tile T.
+template <class T>
+__device__ __forceinline__ void part_corner(int tm, int tn, int sub, int &m0, int &n0) {
+    constexpr int PN = 256 / T::BN;
+    m0 = tm * 256 + sub / PN * T::BM;
+    n0 = tn * 256 + sub % PN * T::BN;
 }
 
 // Four FP32 values rounded to 16 bits (to nearest, ties to even).

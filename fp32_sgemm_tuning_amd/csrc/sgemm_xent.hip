@@ -12,14 +12,14 @@
 // on them and nothing they hold (NaN, Inf) reaches dW.
 //
 // Forward: each block tile of the logits stays in the accumulators;
-// xent_stats_kernel writes per row the tile's maximum and sum of
-// exp(l - maximum), and xent_join_kernel joins a row's tiles.
+// stats_tile writes per row and 128 columns the maximum and the sum of
+// exp(l - maximum), and xent_join_kernel joins a row's.
 //
 // Backward, for one piece of the vocabulary after the other:
-// xent_dlogits_kernel forms the piece of the logits again and stores
+// dlogits_tile forms the piece of the logits again and stores
 // P_iv * dloss_i / max|dloss| in 16 bits, then xent_dx_kernel adds its
-// product with the piece of W to an FP32 sum, and xent_dw_kernel writes the
-// piece of dW.  P lies in [-1, 1] and the scaled dloss too, so no 16-bit
+// product with the piece of W to an FP32 sum, and dw_tile writes the piece of
+// dW.  P lies in [-1, 1] and the scaled dloss too, so no 16-bit
 // range is left whatever the loss is scaled by; the factor max|dloss| is put
 // back in FP32.  Rounding this product to the inputs' 16 bits is what lets
 // the two gradient products run on the 16-bit matrix instructions; it is off
@@ -55,7 +55,7 @@ struct XentArgs {
     float *loss, *lse;
     // forward
     float *tlogit;                      // logit of the target, per listed row
-    float2 *part;                       // [tile column][listed row]: maximum, sum
+    float2 *part;                       // [128 columns][listed row]: maximum, sum
     // backward
     const float *lse_in, *dloss;
     long dloss_stride;
@@ -157,30 +157,22 @@ __device__ __forceinline__ void listed_rows(const XentArgs &p, int rows, const c
     ldx = in_place ? p.ldx : p.ldxc;
 }
 
-// This workgroup's tile of the listed rows x n grid and the logits there
-// (before alpha); false past the last tile.
+// The logits (before alpha) of the tile at (m0, n0) of the listed rows by the
+// piece of the vocabulary.
 template <class T, bool F16>
-__device__ __forceinline__ bool logits_tile(const XentArgs &p, int rows, char *lds, int &m0, int &n0,
+__device__ __forceinline__ void logits_tile(const XentArgs &p, int rows, char *lds, int m0, int n0,
                                             f32x4 (&acc)[T::MI][T::NB]) {
-    const int tiles_m = (rows + T::BM - 1) / T::BM, tiles_n = (p.n_count + T::BN - 1) / T::BN;
-    if ((int)blockIdx.x >= tiles_m * tiles_n) return false;
-    int tm, tn;
-    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
-    m0 = tm * T::BM;
-    n0 = tn * T::BN;
     Operands16 q = {nullptr, p.W + 2L * p.n_first * p.ldw, 0, p.ldw, rows, p.n_count, p.K};
     listed_rows(p, rows, q.A, q.lda);
     accumulate16<T, F16, false, true>(q, m0, n0, lds, acc);
-    return true;
 }
 
+// A row's maximum and sum over each 128 columns of the tile (one slot of
+// `part` each, whatever the tile), and the target's logit.
 template <class T, bool F16>
-__global__ void __launch_bounds__(T::NT) xent_stats_kernel(XentArgs p) {
-    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
-    int m0, n0;
+__device__ __forceinline__ void stats_tile(const XentArgs &p, int rows, char *lds, int m0, int n0) {
     f32x4 acc[T::MI][T::NB];
-    if (!logits_tile<T, F16>(p, rows, lds, m0, n0, acc)) return;
+    logits_tile<T, F16>(p, rows, lds, m0, n0, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
     const int col0 = n0 + wn * T::WN + 4 * (lane >> 4);
@@ -215,15 +207,18 @@ __global__ void __launch_bounds__(T::NT) xent_stats_kernel(XentArgs p) {
         if (lane < 16) red[wn * T::BM + r] = make_float2(top, sum);
     }
     __syncthreads();
-    for (int r = threadIdx.x; r < T::BM && m0 + r < rows; r += T::NT) {
-        float2 a = red[r];
+    constexpr int PER = 128 / T::WN;                                // waves per 128 columns
+    for (int t = threadIdx.x; t < T::BM * (T::BN / 128); t += T::NT) {
+        const int r = t % T::BM, slot = t / T::BM;
+        if (m0 + r >= rows || n0 + 128 * slot >= p.N) continue;
+        float2 a = red[slot * PER * T::BM + r];
 #pragma unroll
-        for (int w = 1; w < T::WAVES_N; ++w) {
-            const float2 b = red[w * T::BM + r];
+        for (int w = 1; w < PER; ++w) {
+            const float2 b = red[(slot * PER + w) * T::BM + r];
             const float top = fmaxf(a.x, b.x), base = top == -__builtin_inff() ? 0.f : top;
             a = make_float2(top, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
         }
-        p.part[(long)(n0 / T::BN) * p.M + m0 + r] = a;
+        p.part[(long)(n0 / 128 + slot) * p.M + m0 + r] = a;
     }
 }
 
@@ -259,14 +254,11 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(XentArgs p, int tiles_n
 }
 
 // P [listed rows][piece of the vocabulary] in 16 bits, zeros behind the
-// vocabulary's end up to whole tiles.
+// vocabulary's end up to the tile's.
 template <class T, bool F16>
-__global__ void __launch_bounds__(T::NT) xent_dlogits_kernel(XentArgs p) {
-    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
-    int m0, n0;
+__device__ __forceinline__ void dlogits_tile(const XentArgs &p, int rows, char *lds, int m0, int n0) {
     f32x4 acc[T::MI][T::NB];
-    if (!logits_tile<T, F16>(p, rows, lds, m0, n0, acc)) return;
+    logits_tile<T, F16>(p, rows, lds, m0, n0, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col0 = n0 + wave % T::WAVES_N * T::WN + 4 * (lane >> 4);
 #pragma unroll
@@ -289,6 +281,63 @@ __global__ void __launch_bounds__(T::NT) xent_dlogits_kernel(XentArgs p) {
             *reinterpret_cast<i32x2 *>(dst + 2 * col) = round16<F16>(v);
         }
     }
+}
+
+// The piece of dW: P^T * X over the listed rows.
+template <class T, bool F16>
+__device__ __forceinline__ void dw_tile(const XentArgs &p, int rows, char *lds, int m0, int n0) {
+    Operands16 q = {p.P, nullptr, p.ldp, 0, p.n_count, p.K, rows};
+    listed_rows(p, rows, q.B, q.ldb);
+    f32x4 acc[T::MI][T::NB];
+    accumulate16<T, F16, true, false>(q, m0, n0, lds, acc);
+    store_tile<T, F16, true>(acc, m0, n0, p.n_count, p.K, p.dW + 2L * p.n_first * p.lddw, p.lddw,
+                             p.alpha * p.head->gmax, 0.f);
+}
+
+// STEP 0: stats_tile, 1: dlogits_tile, over the listed rows by the piece; 2:
+// dw_tile, over the piece by K.  The number of listed rows is read here.
+template <int STEP, bool F16>
+struct XentBody {
+    const XentArgs &p;
+    int rows, m, n;                     // extents of the step's outputs
+    __device__ __forceinline__ explicit XentBody(const XentArgs &args) : p(args) {
+        rows = __builtin_amdgcn_readfirstlane(p.head->rows);
+        m = STEP == 2 ? p.n_count : rows;
+        n = STEP == 2 ? p.K : p.n_count;
+    }
+    __device__ __forceinline__ int total(int bm, int bn) const { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
+    template <class T>
+    __device__ __forceinline__ void at(char *lds, int m0, int n0) const {
+        if constexpr (STEP == 0) stats_tile<T, F16>(p, rows, lds, m0, n0);
+        else if constexpr (STEP == 1) dlogits_tile<T, F16>(p, rows, lds, m0, n0);
+        else dw_tile<T, F16>(p, rows, lds, m0, n0);
+    }
+    template <class T>
+    __device__ __forceinline__ void tile(char *lds, int id, int sub) const {
+        int tm, tn, m0, n0;
+        raster(id, (m + 255) / 256, (n + 255) / 256, tm, tn);
+        part_corner<T>(tm, tn, sub, m0, n0);
+        if (m0 < m && n0 < n) at<T>(lds, m0, n0);
+    }
+};
+
+template <int STEP, bool F16>
+__global__ void __launch_bounds__(512) xent_mixed_kernel(XentArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[Mixed<STEP != 2>::LDS];
+    const XentBody<STEP, F16> body(p);
+    Mixed<STEP != 2>::run(body, lds, body.total(256, 256));
+}
+
+// Few rows.
+template <int STEP, bool F16>
+__global__ void __launch_bounds__(Tile32::NT) xent_rows_kernel(XentArgs p) {
+    __shared__ __attribute__((aligned(16))) char lds[Tile32::LDS];
+    const XentBody<STEP, F16> body(p);
+    const int total = body.total(32, 128);
+    if ((int)blockIdx.x >= total) return;
+    int tm, tn;
+    raster(xcd_run(blockIdx.x, total), (body.m + 31) / 32, (body.n + 127) / 128, tm, tn);
+    body.template at<Tile32>(lds, 32 * tm, 128 * tn);
 }
 
 // dX: sum += P * piece of W, block y of gridDim.y over its share of the piece
@@ -347,22 +396,6 @@ __global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int share
     }
 }
 
-// The piece of dW: P^T * X over the listed rows.
-template <class T, bool F16>
-__global__ void __launch_bounds__(T::NT) xent_dw_kernel(XentArgs p) {
-    __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const int rows = __builtin_amdgcn_readfirstlane(p.head->rows);
-    const int tiles_m = (p.n_count + T::BM - 1) / T::BM, tiles_n = (p.K + T::BN - 1) / T::BN;
-    int tm, tn;
-    raster(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
-    Operands16 q = {p.P, nullptr, p.ldp, 0, p.n_count, p.K, rows};
-    listed_rows(p, rows, q.B, q.ldb);
-    f32x4 acc[T::MI][T::NB];
-    accumulate16<T, F16, true, false>(q, tm * T::BM, tn * T::BN, lds, acc);
-    store_tile<T, F16, true>(acc, tm * T::BM, tn * T::BN, p.n_count, p.K, p.dW + 2L * p.n_first * p.lddw, p.lddw,
-                             p.alpha * p.head->gmax, 0.f);
-}
-
 // Bytes of P at most, so that it stays in the Infinity Cache between the
 // kernel that writes it and the two that read it.
 constexpr long kPieceBytes = 256L << 20;
@@ -373,21 +406,15 @@ long piece_columns(int M, int N) {
     return ceil_to((N + pieces - 1) / pieces, 256);
 }
 
-// The tile of dX and into how many shares the vocabulary (of a piece of
-// `count` columns) is cut: the grid of M x K outputs rarely fills the chip and
-// its products are long, so as many shares as fill it, of 512 columns at
-// least (1331 rows of 2048 by 50021 columns: 444 us on 128 x 128 tiles
-// unshared, 290 on 256 x 256 in four shares).
-struct DxPlan {
-    Shape shape;
-    int shares;
-};
-
-DxPlan dx_plan(int M, int K, int count) {
-    const Shape shape = M <= 32 ? Shape::k32 : M <= 128 ? Shape::k128 : Shape::k256;
+// Into how many shares the vocabulary (of a piece of `count` columns) is cut
+// for dX: its grid of M x K outputs rarely fills the chip and its products are
+// long, so as many as fill it, of 512 columns at least (1331 rows of 2048 by
+// 50021 columns: 444 us on 128 x 128 tiles unshared, 286 and 15 for the join on
+// 256 x 256 in four shares).
+int dx_shares(int M, int K, int count) {
     const int bm = M <= 32 ? 32 : M <= 128 ? 128 : 256, bn = M <= 128 ? 128 : 256;
     const long tiles = (M + bm - 1L) / bm * ((K + bn - 1L) / bn), places = M <= 128 ? 512 : 256;
-    return {shape, (int)std::max(1L, std::min(places / std::max(tiles, 1L), count / 512L))};
+    return (int)std::max(1L, std::min(places / std::max(tiles, 1L), count / 512L));
 }
 
 // The workspace, laid out from `base` (null: only its size is wanted).
@@ -418,7 +445,7 @@ long xent_layout(XentArgs &p, void *workspace, bool grad, char *&Wc) {
         p.lsec = reinterpret_cast<float *>(l.take(4L * p.M));
         p.ldp = piece_columns(p.M, p.N);
         p.P = l.take(2L * p.M * p.ldp);
-        const int shares = dx_plan(p.M, p.K, (int)std::min((long)p.N, p.ldp)).shares;
+        const int shares = dx_shares(p.M, p.K, (int)std::min((long)p.N, p.ldp));
         p.sum = p.ldp < p.N || shares > 1 ? reinterpret_cast<float *>(l.take(4L * shares * p.M * p.ldxc)) : nullptr;
     }
     return l.at;
@@ -439,14 +466,28 @@ bool scratch_ok(long need, const void *workspace, long long bytes) {
 
 unsigned tiles(long m, long n, int bm, int bn) { return (unsigned)((m + bm - 1) / bm * ((n + bn - 1) / bn)); }
 
-Shape logits_shape(int M, int N) {
-    return M <= 32 ? Shape::k32 : pick_shape((M + 255) / 256, (M + 127) / 128, N, true);
+template <int STEP>
+hipError_t launch_mixed(const XentArgs &p, long m, long n, bool f16, hipStream_t s) {
+    const dim3 grid((unsigned)mixed_grid(tiles(m, n, 256, 256)));
+    return f16 ? launch_k(xent_mixed_kernel<STEP, true>, grid, dim3(512), s, p)
+               : launch_k(xent_mixed_kernel<STEP, false>, grid, dim3(512), s, p);
 }
 
-// A kernel of tile T over at most m x n outputs, `shares` blocks each.
-#define XENT_LAUNCH(KERNEL, T, m, n, shares, ...)                                                                  \
-    (f16 ? launch_k(KERNEL<T, true>, dim3(tiles(m, n, T::BM, T::BN), shares), dim3(T::NT), s, __VA_ARGS__)         \
-         : launch_k(KERNEL<T, false>, dim3(tiles(m, n, T::BM, T::BN), shares), dim3(T::NT), s, __VA_ARGS__))
+// Steps 0 and 1, on a tile of 32 rows (bound by the bytes of W) or large ones.
+template <int STEP>
+hipError_t launch_logits(const XentArgs &p, bool f16, hipStream_t s) {
+    if (p.M > 32) return launch_mixed<STEP>(p, p.M, p.n_count, f16, s);
+    const dim3 grid(tiles(p.M, p.n_count, 32, 128));
+    return f16 ? launch_k(xent_rows_kernel<STEP, true>, grid, dim3(Tile32::NT), s, p)
+               : launch_k(xent_rows_kernel<STEP, false>, grid, dim3(Tile32::NT), s, p);
+}
+
+template <class T>
+hipError_t launch_dx(const XentArgs &p, int shares, int first, int last, bool f16, hipStream_t s) {
+    const dim3 grid(tiles(p.M, p.K, T::BM, T::BN), shares);
+    return f16 ? launch_k(xent_dx_kernel<T, true>, grid, dim3(T::NT), s, p, first, last)
+               : launch_k(xent_dx_kernel<T, false>, grid, dim3(T::NT), s, p, first, last);
+}
 
 }  // namespace
 }  // namespace sgemm_mi355x
@@ -502,14 +543,8 @@ int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha, const void *X, 
         p.W = Wc;
         p.ldw = p.ldxc;
     }
-    const Shape shape = logits_shape(M, N);
-    if (e == hipSuccess)
-        e = shape == Shape::k32     ? XENT_LAUNCH(xent_stats_kernel, Tile32, M, N, 1, p)
-            : shape == Shape::k128  ? XENT_LAUNCH(xent_stats_kernel, Tile128, M, N, 1, p)
-            : shape == Shape::kTall ? XENT_LAUNCH(xent_stats_kernel, TileTall, M, N, 1, p)
-                                    : XENT_LAUNCH(xent_stats_kernel, Tile256, M, N, 1, p);
-    const int bn = shape == Shape::k256 ? 256 : 128;
-    if (e == hipSuccess) e = launch_k(xent_join_kernel, dim3((M + 15) / 16), dim3(1024), s, p, (N + bn - 1) / bn);
+    if (e == hipSuccess) e = launch_logits<0>(p, f16, s);
+    if (e == hipSuccess) e = launch_k(xent_join_kernel, dim3((M + 15) / 16), dim3(1024), s, p, (N + 127) / 128);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
@@ -554,32 +589,20 @@ int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void
         p.W = Wc;
         p.ldw = p.ldxc;
     }
-    const DxPlan plan = dx_plan(M, K, (int)std::min((long)N, p.ldp));
+    const int shares = dx_shares(M, K, (int)std::min((long)N, p.ldp));
     for (p.n_first = 0; p.n_first < N && e == hipSuccess; p.n_first += (int)p.ldp) {
         p.n_count = (int)std::min((long)N - p.n_first, p.ldp);
         const int first = p.n_first == 0, last = p.n_first + p.n_count == N;
-        if (M > 0) {
-            const Shape shape = logits_shape(M, p.n_count);
-            e = shape == Shape::k32     ? XENT_LAUNCH(xent_dlogits_kernel, Tile32, M, p.n_count, 1, p)
-                : shape == Shape::k128  ? XENT_LAUNCH(xent_dlogits_kernel, Tile128, M, p.n_count, 1, p)
-                : shape == Shape::kTall ? XENT_LAUNCH(xent_dlogits_kernel, TileTall, M, p.n_count, 1, p)
-                                        : XENT_LAUNCH(xent_dlogits_kernel, Tile256, M, p.n_count, 1, p);
-        }
-        if (e == hipSuccess && M > 0 && dX != nullptr) {
-            e = plan.shape == Shape::k32    ? XENT_LAUNCH(xent_dx_kernel, Tile32, M, K, plan.shares, p, first, last)
-                : plan.shape == Shape::k128 ? XENT_LAUNCH(xent_dx_kernel, Tile128, M, K, plan.shares, p, first, last)
-                                            : XENT_LAUNCH(xent_dx_kernel, Tile256, M, K, plan.shares, p, first, last);
-        }
-        if (e == hipSuccess && dW != nullptr) {
-            const Shape shape = pick_shape((p.n_count + 255) / 256, (p.n_count + 127) / 128, K, false);
-            e = shape == Shape::k128    ? XENT_LAUNCH(xent_dw_kernel, Tile128, p.n_count, K, 1, p)
-                : shape == Shape::kWide ? XENT_LAUNCH(xent_dw_kernel, TileWide, p.n_count, K, 1, p)
-                                        : XENT_LAUNCH(xent_dw_kernel, Tile256, p.n_count, K, 1, p);
-        }
+        if (M > 0) e = launch_logits<1>(p, f16, s);
+        if (e == hipSuccess && M > 0 && dX != nullptr)
+            e = M <= 32    ? launch_dx<Tile32>(p, shares, first, last, f16, s)
+                : M <= 128 ? launch_dx<Tile128>(p, shares, first, last, f16, s)
+                           : launch_dx<Tile256>(p, shares, first, last, f16, s);
+        if (e == hipSuccess && dW != nullptr) e = launch_mixed<2>(p, p.n_count, K, f16, s);
     }
-    if (e == hipSuccess && M > 0 && dX != nullptr && plan.shares > 1)
-        e = f16 ? launch_k(xent_dx_join_kernel<true>, dim3(M), dim3(256), s, p, plan.shares)
-                : launch_k(xent_dx_join_kernel<false>, dim3(M), dim3(256), s, p, plan.shares);
+    if (e == hipSuccess && M > 0 && dX != nullptr && shares > 1)
+        e = f16 ? launch_k(xent_dx_join_kernel<true>, dim3(M), dim3(256), s, p, shares)
+                : launch_k(xent_dx_join_kernel<false>, dim3(M), dim3(256), s, p, shares);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
