@@ -123,17 +123,31 @@ __global__ void __launch_bounds__(512) group_mixed_kernel(GroupArgs p) {
     Mixed<TB>::run(body, lds, body.list.total);
 }
 
+// The group of `turn` when up to 64 groups go by their rows, most first.
+__device__ __forceinline__ int longest_first(const GroupArgs &p, int turn) {
+    const int lane = threadIdx.x & 63;
+    int lo, mine = -1, rank = 0;
+    if (lane < p.groups) group_rows(p.offsets, lane, p.M, lo, mine);
+    for (int j = 0; j < p.groups; ++j) {
+        const int other = __builtin_amdgcn_readlane(mine, j);
+        rank += other > mine || (other == mine && j < lane);
+    }
+    return __builtin_ctzl(__ballot(lane < p.groups && rank == turn));
+}
+
 // A [M][K] and B [M][N] by rows; C[g] is K x N, the sum runs over the
 // group's rows.  A group's tiles go round the XCDs in runs of their own, so
-// that uneven groups still load the XCDs evenly.
+// that uneven groups still load the XCDs evenly, and the longest groups go
+// first, so that the last tiles to run are short ones.
 template <class T, bool F16, bool OUT16>
 __global__ void __launch_bounds__(T::NT) group_k_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
     const int tiles_m = (p.K + T::BM - 1) / T::BM, tiles_n = (p.N + T::BN - 1) / T::BN;
     const int tiles = tiles_m * tiles_n, per = (tiles + 7) >> 3;
-    const int g = blockIdx.x / (8 * per), id = (blockIdx.x & 7) * per + (blockIdx.x - g * 8 * per >> 3);
+    const int turn = blockIdx.x / (8 * per), id = (blockIdx.x & 7) * per + (blockIdx.x - turn * 8 * per >> 3);
     if (id >= tiles) return;
     int lo, rows, tm, tn;
+    const int g = p.groups <= 64 ? longest_first(p, turn) : turn;
     group_rows(p.offsets, g, p.M, lo, rows);
     lo = __builtin_amdgcn_readfirstlane(lo);
     rows = __builtin_amdgcn_readfirstlane(rows);

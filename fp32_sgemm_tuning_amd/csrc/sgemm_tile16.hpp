@@ -122,9 +122,10 @@ __device__ __forceinline__ float widen16(unsigned short bits) {
 
 // Columns col .. col+3 (those below N) of a row of C at `row`, C of FP32 or
 // (OUT16) 16-bit values: v, plus beta times what is there unless beta is 0
-// (then C is not read).  `vec`: 4-element accesses are aligned.
+// (then C is not read).  The four go in one access whatever the row's
+// alignment: this chip takes such accesses at any element.
 template <bool F16, bool OUT16>
-__device__ __forceinline__ void store4(char *row, int col, int N, bool vec, float beta, f32x4 v) {
+__device__ __forceinline__ void store4(char *row, int col, int N, float beta, f32x4 v) {
     if constexpr (OUT16) {
         unsigned short *dst = reinterpret_cast<unsigned short *>(row) + col;
         if (beta != 0.f) {
@@ -133,8 +134,8 @@ __device__ __forceinline__ void store4(char *row, int col, int N, bool vec, floa
                 if (col + r < N) v[r] += beta * widen16<F16>(dst[r]);
         }
         const i32x2 o = round16<F16>(v);
-        if (vec && col + 3 < N) {
-            *reinterpret_cast<i32x2 *>(dst) = o;
+        if (col + 3 < N) {
+            __builtin_memcpy(dst, &o, 8);
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -142,9 +143,13 @@ __device__ __forceinline__ void store4(char *row, int col, int N, bool vec, floa
         }
     } else {
         float *dst = reinterpret_cast<float *>(row) + col;
-        if (vec && col + 3 < N) {
-            if (beta != 0.f) v += *reinterpret_cast<const f32x4 *>(dst) * beta;
-            *reinterpret_cast<f32x4 *>(dst) = v;
+        if (col + 3 < N) {
+            if (beta != 0.f) {
+                f32x4 c;
+                __builtin_memcpy(&c, dst, 16);
+                v += c * beta;
+            }
+            __builtin_memcpy(dst, &v, 16);
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -160,7 +165,6 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[T::MI][T::NB], int
                                            long ldc, float alpha, float beta) {
     constexpr int E = OUT16 ? 2 : 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool vec = (reinterpret_cast<uintptr_t>(C) & (4 * E - 1)) == 0 && (ldc & 3) == 0;
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
         const int row = m0 + (wave / T::WAVES_N) * T::WM + mi * 16 + (lane & 15);
@@ -168,7 +172,7 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[T::MI][T::NB], int
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) {
             const int col = n0 + (wave % T::WAVES_N) * T::WN + nb * 16 + 4 * (lane >> 4);
-            store4<F16, OUT16>(C + (long)row * ldc * E, col, N, vec, beta, acc[mi][nb] * alpha);
+            store4<F16, OUT16>(C + (long)row * ldc * E, col, N, beta, acc[mi][nb] * alpha);
         }
     }
 }

@@ -382,14 +382,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
         static_for<0, Q>([&](auto qc) { finish(IntC<STEPS - 1>{}, qc); });
     }
     constexpr int E = OUT16 ? 2 : 4;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.C) & (4 * E - 1)) == 0 && (p.ldc & 3) == 0;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
         const int row = m0 + (wm * MI + mi) * 16 + lr;
         if (row >= p.M) continue;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            store4<F16, OUT16>(p.C + (long)row * p.ldc * E, n0 + (wn * NB + b) * 16 + 4 * lg, p.N, vec, p.beta,
+            store4<F16, OUT16>(p.C + (long)row * p.ldc * E, n0 + (wn * NB + b) * 16 + 4 * lg, p.N, p.beta,
                                total[mi][b] * p.alpha);
     }
 }
@@ -463,10 +462,16 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(PackArgs p) {
         const bool none = !(s > 0.f);                       // 0 or NaN
         const float step = none ? 1.f : s;
         const float z = ZEROS ? (s == s ? fminf(rintf(-lo / step), 15.f) : 0.f) : 8.f;
+        // round(w / s) without the division where w * (1 / s), off by less than
+        // 2^-17 for |w / s| below 32, is further than that from a half (the
+        // divisions took over half of the kernel's time)
+        const float inverse = __builtin_amdgcn_rcpf(step);
         unsigned word = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float q = none ? z : fminf(fmaxf(rintf(w[e] / step) + z, 0.f), 15.f);
+            float n = w[e] * inverse, r = rintf(n);
+            if (!(fabsf(n - r) < 0.4999f && fabsf(n) < 32.f)) r = rintf(w[e] / step);
+            const float q = none ? z : fminf(fmaxf(r + z, 0.f), 15.f);
             word |= (unsigned)q << (4 * (e >> 1) + 16 * (e & 1));
         }
         const int c = i >> 4, in = i & 15;                  // word s = in / 4 of run j = in % 4

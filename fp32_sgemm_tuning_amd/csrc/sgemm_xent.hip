@@ -68,7 +68,7 @@ struct XentArgs {
 
 __device__ __forceinline__ float max_abs(float a, float b) { return fmaxf(a, fabsf(b)); }
 
-constexpr int kCompactRows = 32;
+constexpr int kCompactRows = 16;
 
 // Block b lists the rows b * kCompactRows ...: it counts the rows before
 // them itself (a pass over the targets, which stay in L2), so one launch
@@ -82,11 +82,23 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
     const int r0 = blockIdx.x * kCompactRows;
     int nb = 0, na = 0;
     float gm = 0.f;
-    for (int i = tid; i < p.M; i += 256) {
-        if (p.target[i] == p.ignore) continue;
-        ++na;
-        nb += i < r0;
-        if (GRAD) gm = max_abs(gm, p.dloss[i * p.dloss_stride]);
+    // (eight rows of a thread at a time, so that their loads overlap)
+    for (int i0 = tid; i0 < p.M; i0 += 8 * 256) {
+        long long t[8];
+        float d[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + 256 * u, at = min(i, p.M - 1);
+            t[u] = i < p.M ? p.target[at] : p.ignore;
+            d[u] = GRAD ? p.dloss[at * p.dloss_stride] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (t[u] == p.ignore) continue;
+            ++na;
+            nb += i0 + 256 * u < r0;
+            gm = max_abs(gm, d[u]);
+        }
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
@@ -106,10 +118,10 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
     if (!(gm > 0.f && gm < __builtin_inff())) gm = 1.f;
     if (blockIdx.x == 0 && tid == 0) *p.head = {na, gm};
     const bool copy = !(p.take_x && na == p.M);
-    // each wave: 8 rows in turn
-    const int mine = r0 + (lane & 31);
+    // each wave: every fourth row
+    const int mine = r0 + (lane & (kCompactRows - 1));
     const long long t = mine < p.M ? p.target[mine] : p.ignore;
-    const unsigned listed = (unsigned)__ballot(t != p.ignore);        // bit r: row r0 + r (lanes 0-31)
+    const unsigned listed = (unsigned)__ballot(t != p.ignore);        // bit r: row r0 + r
     for (int r = wave; r < kCompactRows && r0 + r < p.M; r += 4) {
         const int row = r0 + r;
         if (!(listed >> r & 1)) {
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
     accumulate16<T, F16, false, false>(q, m0, n0, lds, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float scale = p.alpha * p.head->gmax;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0, place = last && gridDim.y == 1;
+    const bool place = last && gridDim.y == 1;
     float *sums = p.sum + (long)blockIdx.y * p.M * p.ldxc;
 #pragma unroll
     for (int mi = 0; mi < T::MI; ++mi) {
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
             if (col >= p.K) continue;
             f32x4 v = acc[mi][nb];
             if (!first) v += *reinterpret_cast<const f32x4 *>(sum + col);
-            if (place) store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
+            if (place) store4<F16, true>(out, col, p.K, 0.f, v * scale);
             else *reinterpret_cast<f32x4 *>(sum + col) = v;
         }
     }
@@ -386,13 +398,12 @@ __global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int share
     const int row = blockIdx.x;
     if (row >= p.head->rows) return;
     const float scale = p.alpha * p.head->gmax;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.dX) & 7) == 0 && (p.lddx & 3) == 0;
     char *out = p.dX + 2 * p.map[row] * p.lddx;
     for (int col = 4 * threadIdx.x; col < p.K; col += 1024) {
         const float *sum = p.sum + row * p.ldxc + col;
         f32x4 v = *reinterpret_cast<const f32x4 *>(sum);
         for (int y = 1; y < shares; ++y) v += *reinterpret_cast<const f32x4 *>(sum + (long)y * p.M * p.ldxc);
-        store4<F16, true>(out, col, p.K, vec, 0.f, v * scale);
+        store4<F16, true>(out, col, p.K, 0.f, v * scale);
     }
 }
 
