@@ -272,13 +272,18 @@ def _vector(t, name, dtype, size):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _run(device, stream, call):
+def _run(device, stream, call, *operands):
     """call(stream handle), with `device` current and `stream` (if given)
-    current on it, so that what it allocates belongs to the stream it runs on."""
+    current on it, so that what it allocates belongs to the stream it runs on;
+    the operands' memory is then kept until that stream has used it."""
     import torch
     if stream is None and device.index == torch.cuda.current_device():
         return call(_stream_handle(device, None))
     with _device_ctx(device), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
+        if stream is not None:
+            for t in operands:
+                if t is not None:
+                    t.record_stream(stream)
         return call(_stream_handle(device, stream))
 
 
@@ -373,11 +378,11 @@ def sgemm_grouped(A, B, offsets, C=None, alpha=1.0, beta=0.0, trans_b=False, out
 
     def call(h):
         out, code_c, ldc = _result(C, (M, N), out_dtype, device)
-        args = (code, op, groups, M, N, K, alpha, *operands, offsets.data_ptr(), beta, out.data_ptr(), ldc, code_c)
+        args = (code, op, groups, M, N, K, float(alpha), *operands, offsets.data_ptr(), float(beta), out.data_ptr(), ldc, code_c)
         _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped(*args, ws, size, h),
                         lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *operands))
         return out
-    return _run(device, stream, call)
+    return _run(device, stream, call, A, B, offsets, C)
 
 
 def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
@@ -400,12 +405,12 @@ def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=No
 
     def call(h):
         out, code_c, ldc = _result(C, (groups, K, N), out_dtype, device)
-        args = (code, groups, M, N, K, alpha, *operands, offsets.data_ptr(), beta, out.data_ptr(), ldc,
+        args = (code, groups, M, N, K, float(alpha), *operands, offsets.data_ptr(), float(beta), out.data_ptr(), ldc,
                 out.stride(0) if groups > 1 else 0, code_c)
         _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped_wgrad(*args, ws, size, h),
-                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(M, N, K, *operands))
+                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(groups, M, N, K, *operands))
         return out
-    return _run(device, stream, call)
+    return _run(device, stream, call, A, D, offsets, C)
 
 
 def _xent_args(X, W, target):
@@ -438,10 +443,10 @@ def sgemm_xent(X, W, target, alpha=1.0, ignore_index=-100, stream=None):
         out = torch.empty((2, M), dtype=torch.float32, device=device)
         loss, lse = out.unbind()
         ws = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(capi.sgemm_lowp_xent(code, M, N, K, alpha, *operands, target.data_ptr(), ignore_index, loss.data_ptr(),
+        _check(capi.sgemm_lowp_xent(code, M, N, K, float(alpha), *operands, target.data_ptr(), int(ignore_index), loss.data_ptr(),
                                     lse.data_ptr(), ws.data_ptr(), size, h))
         return loss, lse
-    return _run(device, stream, call)
+    return _run(device, stream, call, X, W, target)
 
 
 def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need_dx=True, need_dw=True, stream=None):
@@ -468,11 +473,11 @@ def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need
         dX = torch.empty((M, K), dtype=X.dtype, device=device) if need_dx else None
         dW = torch.empty((N, K), dtype=X.dtype, device=device) if need_dw else None
         ws = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(capi.sgemm_lowp_xent_grad(code, M, N, K, alpha, *operands, target.data_ptr(), ignore_index,
+        _check(capi.sgemm_lowp_xent_grad(code, M, N, K, float(alpha), *operands, target.data_ptr(), int(ignore_index),
                                          lse.data_ptr(), dloss.data_ptr(), step, _address(dX), max(K, 1), _address(dW),
                                          max(K, 1), ws.data_ptr(), size, h))
         return dX, dW
-    return _run(device, stream, call)
+    return _run(device, stream, call, X, W, target, lse, dloss)
 
 
 class W4Weight(NamedTuple):
@@ -536,12 +541,12 @@ def sgemm_w4(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     def call(h):
         out, code_c, ldc = _result(C, (M, N), out_dtype, device)
         x = X.data_ptr()
-        args = (code, M, N, K, alpha, x, ldx, packed.data_ptr(), scales.data_ptr(), _address(zeros), group, beta,
+        args = (code, M, N, K, float(alpha), x, ldx, packed.data_ptr(), scales.data_ptr(), _address(zeros), group, float(beta),
                 out.data_ptr(), ldc, code_c)
         _with_workspace(device, lambda ws, size: capi.sgemm_w4(*args, ws, size, h),
                         lambda: capi.sgemm_w4_workspace(M, K, x, ldx))
         return out
-    return _run(device, stream, call)
+    return _run(device, stream, call, X, packed, scales, zeros, C)
 
 
 def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
@@ -562,7 +567,7 @@ def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
         _check(capi.sgemm_w4_quantize(code, N, K, W.data_ptr(), ldw, group, out.packed.data_ptr(),
                                       out.scales.data_ptr(), _address(out.zeros), h))
         return out
-    return _run(device, stream, call)
+    return _run(device, stream, call, W)
 
 
 def sgemm_w4_dequantize(W, stream=None):
@@ -577,4 +582,4 @@ def sgemm_w4_dequantize(W, stream=None):
         _check(capi.sgemm_w4_dequantize(_codes()[out.dtype], N, K, packed.data_ptr(), scales.data_ptr(),
                                         _address(zeros), group, out.data_ptr(), max(K, 1), h))
         return out
-    return _run(device, stream, call)
+    return _run(device, stream, call, packed, scales, zeros)

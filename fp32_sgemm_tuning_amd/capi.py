@@ -129,7 +129,7 @@ def open_library(path: str) -> ctypes.CDLL:
             ("sgemm_lowp_grouped", [i, i, i, i, i, i, f, vp, i, vp, i, ll, vp, f, vp, i, i, vp, ll, vp], i),
             ("sgemm_lowp_grouped_workspace", [i, i, i, i, i, vp, i, vp, i, ll], ll),
             ("sgemm_lowp_grouped_wgrad", [i, i, i, i, i, f, vp, i, vp, i, vp, f, vp, i, ll, i, vp, ll, vp], i),
-            ("sgemm_lowp_grouped_wgrad_workspace", [i, i, i, vp, i, vp, i], ll),
+            ("sgemm_lowp_grouped_wgrad_workspace", [i, i, i, i, vp, i, vp, i], ll),
             ("sgemm_lowp_xent", [i, i, i, i, f, vp, i, vp, i, vp, ll, vp, vp, vp, ll, vp], i),
             ("sgemm_lowp_xent_grad",
              [i, i, i, i, f, vp, i, vp, i, vp, ll, vp, vp, i, vp, i, vp, i, vp, ll, vp], i),
@@ -243,8 +243,8 @@ def sgemm_lowp_grouped_wgrad(dtype, groups, M, N, K, alpha, A, lda, D, ldd, offs
                                            stride_c, dtype_c, workspace, workspace_bytes, stream)
 
 
-def sgemm_lowp_grouped_wgrad_workspace(M, N, K, A, lda, D, ldd):
-    return load().sgemm_lowp_grouped_wgrad_workspace(M, N, K, A, lda, D, ldd)
+def sgemm_lowp_grouped_wgrad_workspace(groups, M, N, K, A, lda, D, ldd):
+    return load().sgemm_lowp_grouped_wgrad_workspace(groups, M, N, K, A, lda, D, ldd)
 
 
 def sgemm_lowp_xent(dtype, M, N, K, alpha, X, ldx, W, ldw, target, ignore_index, loss, lse, workspace,

@@ -138,7 +138,8 @@ __device__ __forceinline__ int longest_first(const GroupArgs &p, int turn) {
 // A [M][K] and B [M][N] by rows; C[g] is K x N, the sum runs over the
 // group's rows.  A group's tiles go round the XCDs in runs of their own, so
 // that uneven groups still load the XCDs evenly, and the longest groups go
-// first, so that the last tiles to run are short ones.
+// first, so that the last tiles to run are short ones.  Block y of gridDim.y
+// takes its share of the group's rows, into C's of its own.
 template <class T, bool F16, bool OUT16>
 __global__ void __launch_bounds__(T::NT) group_k_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
@@ -152,11 +153,27 @@ __global__ void __launch_bounds__(T::NT) group_k_kernel(GroupArgs p) {
     lo = __builtin_amdgcn_readfirstlane(lo);
     rows = __builtin_amdgcn_readfirstlane(rows);
     raster(id, tiles_m, tiles_n, tm, tn);
+    const int shares = gridDim.y, part = (rows + 64 * shares - 1) / (64 * shares) * 64;        // whole K tiles
+    lo += min(part * (int)blockIdx.y, rows);
+    rows = min(part, max(rows - part * (int)blockIdx.y, 0));
     const Operands16 q = {p.A + 2L * lo * p.lda, p.B + 2L * lo * p.ldb, p.lda, p.ldb, p.K, p.N, rows};
     f32x4 acc[T::MI][T::NB];
     accumulate16<T, F16, true, false>(q, tm * T::BM, tn * T::BN, lds, acc);
-    store_tile<T, F16, OUT16>(acc, tm * T::BM, tn * T::BN, p.K, p.N, p.C + (OUT16 ? 2L : 4L) * g * p.strideC, p.ldc,
+    const long at = g + (long)blockIdx.y * p.groups;
+    store_tile<T, F16, OUT16>(acc, tm * T::BM, tn * T::BN, p.K, p.N, p.C + (OUT16 ? 2L : 4L) * at * p.strideC, p.ldc,
                               p.alpha, p.beta);
+}
+
+// C = alpha * the sum of the shares' products + beta * C, the shares in order;
+// a thread per four columns.
+template <bool F16, bool OUT16>
+__global__ void __launch_bounds__(256) group_join_kernel(GroupArgs p, const float *parts, long ld, int shares) {
+    const long quads = (p.N + 3) / 4, t = blockIdx.x * 256L + threadIdx.x;
+    if (t >= quads * p.K * p.groups) return;
+    const long row = t / quads, g = row / p.K;              // row: of all groups' matrices
+    const int col = 4 * (int)(t - row * quads);
+    const f32x4 v = sum_shares(parts + row * ld + col, (long)p.groups * p.K * ld, shares);
+    store4<F16, OUT16>(p.C + (OUT16 ? 2L : 4L) * (g * p.strideC + (row - g * p.K) * p.ldc), col, p.N, p.beta, v * p.alpha);
 }
 
 // One 16-byte chunk of dst per thread and step, from rows of any alignment
@@ -217,9 +234,9 @@ hipError_t launch_mixed(const GroupArgs &p, bool f16, bool out16, hipStream_t s)
 }
 
 template <class T>
-hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
+hipError_t launch_wgrad(const GroupArgs &p, int shares, bool f16, bool out16, hipStream_t s) {
     const long tiles = (long)((p.K + T::BM - 1) / T::BM) * ((p.N + T::BN - 1) / T::BN);
-    const dim3 grid((unsigned)(ceil_to(tiles, 8) * p.groups));
+    const dim3 grid((unsigned)(ceil_to(tiles, 8) * p.groups), (unsigned)shares);
     return GROUP_FORMS(group_k_kernel, T::NT, T COMMA, );
 }
 
@@ -233,12 +250,41 @@ hipError_t launch_rows(const GroupArgs &p, bool tb, bool f16, bool out16, hipStr
     return tb ? launch_mixed<true>(p, f16, out16, s) : launch_mixed<false>(p, f16, out16, s);
 }
 
+// Shares of the rows of each group: small matrices over many rows would leave
+// most of the chip idle, so as many as fill it, of 256 rows of an average group
+// at least (6984 rows in 2 groups, 192 x 656 each: 41 -> 14 us).
+int wgrad_shares(int groups, int M, int N, int K) {
+    const long tiles = (K + 127L) / 128 * ((N + 127L) / 128) * std::max(groups, 1);
+    return (int)std::max(1L, std::min(512 / std::max(tiles, 1L), M / std::max(groups, 1) / 256L));
+}
+
+long join_bytes(int groups, int M, int N, int K) {          // the shares' FP32 products
+    const int shares = wgrad_shares(groups, M, N, K);
+    return shares > 1 ? 4L * shares * groups * K * ceil_to(N, 4) : 0;
+}
+
 // Fewer than a round of the large tiles: the next smaller that fill it.
-hipError_t launch_wgrad(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
+hipError_t launch_wgrad(const GroupArgs &p, float *parts, bool f16, bool out16, hipStream_t s) {
+    const int shares = wgrad_shares(p.groups, p.M, p.N, p.K);
+    if (shares > 1) {
+        GroupArgs q = p;
+        q.C = reinterpret_cast<char *>(parts);
+        q.ldc = ceil_to(p.N, 4);
+        q.strideC = p.K * q.ldc;
+        q.alpha = 1.f;
+        q.beta = 0.f;
+        const hipError_t e = launch_wgrad<Tile128>(q, shares, f16, false, s);
+        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)(((p.N + 3L) / 4 * p.K * p.groups + 255) / 256)), block(256);
+        if (f16) return out16 ? launch_k(group_join_kernel<true, true>, grid, block, s, p, parts, q.ldc, shares)
+                              : launch_k(group_join_kernel<true, false>, grid, block, s, p, parts, q.ldc, shares);
+        return out16 ? launch_k(group_join_kernel<false, true>, grid, block, s, p, parts, q.ldc, shares)
+                     : launch_k(group_join_kernel<false, false>, grid, block, s, p, parts, q.ldc, shares);
+    }
     const long n256 = (p.N + 255) / 256, m128 = (p.K + 127) / 128;
-    if ((p.K + 255) / 256 * n256 * p.groups >= 256) return launch_wgrad<Tile256>(p, f16, out16, s);
-    if (m128 * n256 * p.groups >= 256) return launch_wgrad<TileWide>(p, f16, out16, s);
-    return launch_wgrad<Tile128>(p, f16, out16, s);
+    if ((p.K + 255) / 256 * n256 * p.groups >= 256) return launch_wgrad<Tile256>(p, 1, f16, out16, s);
+    if (m128 * n256 * p.groups >= 256) return launch_wgrad<TileWide>(p, 1, f16, out16, s);
+    return launch_wgrad<Tile128>(p, 1, f16, out16, s);
 }
 
 bool in_dtype(int d) { return d == SGEMM_DTYPE_BF16 || d == SGEMM_DTYPE_F16; }
@@ -260,7 +306,7 @@ Copies rows_copies(bool tb, int groups, int M, int N, int K, const void *A, int 
 
 Copies k_copies(int M, int N, int K, const void *A, int lda, const void *D, int ldd) {
     return {chunk_rows(A, lda, K) ? 0 : ceil_to(2L * M * ceil_to(K, 8), 256),
-            chunk_rows(D, ldd, N) ? 0 : 2L * M * ceil_to(N, 8)};
+            chunk_rows(D, ldd, N) ? 0 : ceil_to(2L * M * ceil_to(N, 8), 256)};
 }
 
 bool scratch_ok(long need, const void *workspace, long long bytes) {
@@ -321,11 +367,12 @@ int sgemm_lowp_grouped(int dtype, int op_b, int groups, int M, int N, int K, flo
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
-long long sgemm_lowp_grouped_wgrad_workspace(int M, int N, int K, const void *A, int lda, const void *D, int ldd) {
-    if (M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
-    if (M == 0 || N == 0 || K == 0) return 0;
+long long sgemm_lowp_grouped_wgrad_workspace(int groups, int M, int N, int K, const void *A, int lda, const void *D,
+                                             int ldd) {
+    if (groups < 0 || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
+    if (groups == 0 || M == 0 || N == 0 || K == 0) return 0;
     const Copies c = k_copies(M, N, K, A, lda, D, ldd);
-    return c.a + c.b;
+    return c.a + c.b + join_bytes(groups, M, N, K);
 }
 
 int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float alpha, const void *A, int lda,
@@ -344,10 +391,10 @@ int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float a
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     GroupArgs p = {static_cast<const char *>(A), static_cast<const char *>(D), static_cast<char *>(C), lda, ldd, ldc,
                    0, stride_c, offsets, groups, M, N, K, alpha, beta};
+    char *w = static_cast<char *>(workspace);
+    const Copies c = M > 0 ? k_copies(M, N, K, A, lda, D, ldd) : Copies{0, 0};
+    if (!scratch_ok(c.a + c.b + join_bytes(groups, M, N, K), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     if (M > 0) {
-        const Copies c = k_copies(M, N, K, A, lda, D, ldd);
-        if (!scratch_ok(c.a + c.b, workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
-        char *w = static_cast<char *>(workspace);
         hipError_t e = hipSuccess;
         if (c.a) {
             e = pad_rows(A, lda, 0, 1, M, K, w, s);
@@ -361,7 +408,7 @@ int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float a
         }
         if (e != hipSuccess) return hip_status(e, "kernel launch");
     }
-    const hipError_t e = launch_wgrad(p, f16, out16, s);
+    const hipError_t e = launch_wgrad(p, reinterpret_cast<float *>(w + c.a + c.b), f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 

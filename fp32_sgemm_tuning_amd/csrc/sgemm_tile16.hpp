@@ -177,6 +177,21 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[T::MI][T::NB], int
     }
 }
 
+// The sum of `shares` groups of four values `step` floats apart, in order, with
+// sixteen loads in flight.
+__device__ __forceinline__ f32x4 sum_shares(const float *at, long step, int shares) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int y = 0; y < shares; y += 16) {
+        f32x4 x[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) x[u] = *reinterpret_cast<const f32x4 *>(at + min(y + u, shares - 1) * step);
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            if (y + u < shares) v += x[u];
+    }
+    return v;
+}
+
 inline long ceil_to(long n, long to) { return (n + to - 1) / to * to; }
 
 // Largest leading dimension of the 16-bit kernels' operands: 256 rows stay

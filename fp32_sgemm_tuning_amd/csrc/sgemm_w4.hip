@@ -613,6 +613,7 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx
     if (st != SGEMM_STATUS_OK) return st;
     if (dtype_c != dtype && dtype_c != SGEMM_DTYPE_F32) return SGEMM_STATUS_INVALID_DTYPE;
     if (M < 0 || M > kMaxRows || ldx < std::max(K, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if ((M + 31L) / 32 * ((N + 63) / 64) > 0x7fffffffL) return SGEMM_STATUS_INVALID_DIM;
     if (M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || (K > 0 && (X == nullptr || packed == nullptr || scales == nullptr)))
         return SGEMM_STATUS_NULL_POINTER;

@@ -49,6 +49,8 @@ struct XentArgs {
     XentHead *head;
     int *map;                           // row of X of each listed row
     int *label;                         // its target, -1 outside 0 .. N-1
+    int *seg_rows;                      // many rows: listed rows and max |dloss| per kSegment rows
+    float *seg_max;
     char *Xc;                           // the listed rows side by side, K rounded up to whole chunks
     long ldxc;
     bool take_x;                        // X can be used in place if no row is ignored
@@ -68,53 +70,93 @@ struct XentArgs {
 
 __device__ __forceinline__ float max_abs(float a, float b) { return fmaxf(a, fabsf(b)); }
 
-constexpr int kCompactRows = 16;
+constexpr int kCompactRows = 16, kSegment = 1024;
+constexpr int kOnePass = 16384;     // rows up to which a block counts all before it by itself
 
-// Block b lists the rows b * kCompactRows ...: it counts the rows before
-// them itself (a pass over the targets, which stay in L2), so one launch
-// does.  GRAD: also max|dloss|, each listed row's dloss and lse, and zeros
-// in dX for ignored rows; else zeros in loss and lse.
+// Adds up the rows [from, to) that are not ignored, those of them before r0,
+// and max|dloss|; eight rows of a thread at a time, so that their loads overlap.
 template <bool GRAD>
-__global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
-    __shared__ int before[4], all[4];
-    __shared__ float big[4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int r0 = blockIdx.x * kCompactRows;
-    int nb = 0, na = 0;
-    float gm = 0.f;
-    // (eight rows of a thread at a time, so that their loads overlap)
-    for (int i0 = tid; i0 < p.M; i0 += 8 * 256) {
+__device__ __forceinline__ void count_rows(const XentArgs &p, int from, int to, int r0, int &all, int &before, float &gm) {
+    for (int i0 = from + threadIdx.x; i0 < to; i0 += 8 * 256) {
         long long t[8];
         float d[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int i = i0 + 256 * u, at = min(i, p.M - 1);
-            t[u] = i < p.M ? p.target[at] : p.ignore;
+            const int i = i0 + 256 * u, at = min(i, to - 1);
+            t[u] = i < to ? p.target[at] : p.ignore;
             d[u] = GRAD ? p.dloss[at * p.dloss_stride] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if (t[u] == p.ignore) continue;
-            ++na;
-            nb += i0 + 256 * u < r0;
+            ++all;
+            before += i0 + 256 * u < r0;
             gm = max_abs(gm, d[u]);
         }
     }
+}
+
+// Sums of two counts and a maximum over the 256 threads of a block.
+__device__ __forceinline__ void block_sums(int &a, int &b, float &m) {
+    __shared__ int sa[4], sb[4];
+    __shared__ float sm[4];
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
-        nb += __shfl_xor(nb, d);
-        na += __shfl_xor(na, d);
-        gm = fmaxf(gm, __shfl_xor(gm, d));
+        a += __shfl_xor(a, d);
+        b += __shfl_xor(b, d);
+        m = fmaxf(m, __shfl_xor(m, d));
     }
-    if (lane == 0) {
-        before[wave] = nb;
-        all[wave] = na;
-        big[wave] = gm;
+    if ((threadIdx.x & 63) == 0) {
+        sa[threadIdx.x >> 6] = a;
+        sb[threadIdx.x >> 6] = b;
+        sm[threadIdx.x >> 6] = m;
     }
     __syncthreads();
-    nb = before[0] + before[1] + before[2] + before[3];
-    na = all[0] + all[1] + all[2] + all[3];
-    gm = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+    a = sa[0] + sa[1] + sa[2] + sa[3];
+    b = sb[0] + sb[1] + sb[2] + sb[3];
+    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+}
+
+// Many rows: what xent_compact_kernel needs of each segment.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) xent_segments_kernel(XentArgs p) {
+    int all = 0, before = 0;
+    float gm = 0.f;
+    const int from = blockIdx.x * kSegment;
+    count_rows<GRAD>(p, from, min(from + kSegment, p.M), 0, all, before, gm);
+    block_sums(all, before, gm);
+    if (threadIdx.x == 0) {
+        p.seg_rows[blockIdx.x] = all;
+        p.seg_max[blockIdx.x] = gm;
+    }
+}
+
+// Block b lists the rows b * kCompactRows ...: it counts the rows before
+// them itself (a pass over the targets, which stay in L2, so one launch does;
+// with many rows over the segments' counts and its own segment).  GRAD: also
+// max|dloss|, each listed row's dloss and lse, and zeros in dX for ignored
+// rows; else zeros in loss and lse.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int r0 = blockIdx.x * kCompactRows;
+    int nb = 0, na = 0;
+    float gm = 0.f;
+    if (p.M <= kOnePass) {
+        count_rows<GRAD>(p, 0, p.M, r0, na, nb, gm);
+    } else {
+        const int segment = r0 / kSegment, from = segment * kSegment;
+        int own = 0;
+        float ignored = 0.f;
+        count_rows<GRAD>(p, from, min(from + kSegment, p.M), r0, own, nb, ignored);
+        for (int i = tid; i < (p.M + kSegment - 1) / kSegment; i += 256) {
+            const int rows = p.seg_rows[i];
+            na += rows;
+            if (i < segment) nb += rows;
+            gm = fmaxf(gm, p.seg_max[i]);
+        }
+    }
+    block_sums(na, nb, gm);
     if (!(gm > 0.f && gm < __builtin_inff())) gm = 1.f;
     if (blockIdx.x == 0 && tid == 0) *p.head = {na, gm};
     const bool copy = !(p.take_x && na == p.M);
@@ -127,8 +169,8 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
         if (!(listed >> r & 1)) {
             if (GRAD) {
                 if (p.dX != nullptr)
-                    for (int k = lane; k < p.K; k += 64)
-                        reinterpret_cast<unsigned short *>(p.dX)[row * p.lddx + k] = 0;
+                    for (int k = 4 * lane; k < p.K; k += 256)
+                        store4<false, true>(p.dX + 2 * row * p.lddx, k, p.K, 0.f, f32x4{0.f, 0.f, 0.f, 0.f});
             } else if (lane == 0) {
                 p.loss[row] = 0.f;
                 p.lse[row] = 0.f;
@@ -152,11 +194,15 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
         if (copy) {
             const unsigned short *src = reinterpret_cast<const unsigned short *>(p.X) + row * p.ldx;
             unsigned short *dst = reinterpret_cast<unsigned short *>(p.Xc) + at * p.ldxc;
-            if (p.take_x) {
-                for (int k = 8 * lane; k < p.K; k += 512)
-                    *reinterpret_cast<i32x4 *>(dst + k) = *reinterpret_cast<const i32x4 *>(src + k);
-            } else {
-                for (int k = lane; k < p.ldxc; k += 64) dst[k] = k < p.K ? src[k] : (unsigned short)0;
+            for (int k = 8 * lane; k < p.K; k += 512) {             // (rows of any alignment)
+                unsigned short v[8];
+                if (k + 8 <= p.K) {
+                    __builtin_memcpy(v, src + k, 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = k + e < p.K ? src[k + e] : (unsigned short)0;
+                }
+                __builtin_memcpy(__builtin_assume_aligned(dst + k, 16), v, 16);
             }
         }
     }
@@ -400,9 +446,7 @@ __global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int share
     const float scale = p.alpha * p.head->gmax;
     char *out = p.dX + 2 * p.map[row] * p.lddx;
     for (int col = 4 * threadIdx.x; col < p.K; col += 1024) {
-        const float *sum = p.sum + row * p.ldxc + col;
-        f32x4 v = *reinterpret_cast<const f32x4 *>(sum);
-        for (int y = 1; y < shares; ++y) v += *reinterpret_cast<const f32x4 *>(sum + (long)y * p.M * p.ldxc);
+        const f32x4 v = sum_shares(p.sum + row * p.ldxc + col, p.M * p.ldxc, shares);
         store4<F16, true>(out, col, p.K, 0.f, v * scale);
     }
 }
@@ -446,6 +490,9 @@ long xent_layout(XentArgs &p, void *workspace, bool grad, char *&Wc) {
     p.head = reinterpret_cast<XentHead *>(l.take(sizeof(XentHead)));
     p.map = reinterpret_cast<int *>(l.take(4L * p.M));
     p.label = reinterpret_cast<int *>(l.take(4L * p.M));
+    const long segments = p.M > kOnePass ? (p.M + kSegment - 1) / kSegment : 0;
+    p.seg_rows = reinterpret_cast<int *>(l.take(4 * segments));
+    p.seg_max = reinterpret_cast<float *>(l.take(4 * segments));
     p.Xc = l.take(2L * p.M * p.ldxc);
     Wc = chunk_rows(p.W, p.ldw, p.K) ? nullptr : l.take(2L * p.N * p.ldxc);
     if (!grad) {
@@ -466,7 +513,7 @@ int check(int dtype, int M, int N, int K, int ldx, int ldw) {
     if (dtype != SGEMM_DTYPE_BF16 && dtype != SGEMM_DTYPE_F16) return SGEMM_STATUS_INVALID_DTYPE;
     // (the vocabulary must hold a column for the sums to have a term)
     if (M < 0 || N < 1 || K < 0 || ldx < std::max(K, 1) || ldw < std::max(K, 1) || K > kMaxLd16 ||
-        M > (1 << 30) || N > (1 << 30) || (M + 31L) / 32 * ((N + 127L) / 128) > 0x7fffffffL)
+        M > (1 << 24) || N > (1 << 30) || (M + 31L) / 32 * ((N + 127L) / 128) > 0x7fffffffL)
         return SGEMM_STATUS_INVALID_DIM;
     return SGEMM_STATUS_OK;
 }
@@ -476,6 +523,16 @@ bool scratch_ok(long need, const void *workspace, long long bytes) {
 }
 
 unsigned tiles(long m, long n, int bm, int bn) { return (unsigned)((m + bm - 1) / bm * ((n + bn - 1) / bn)); }
+
+template <bool GRAD>
+hipError_t launch_compact(const XentArgs &p, hipStream_t s) {
+    if (p.M > kOnePass) {
+        const hipError_t e = launch_k(xent_segments_kernel<GRAD>, dim3((p.M + kSegment - 1) / kSegment), dim3(256), s, p);
+        if (e != hipSuccess) return e;
+    }
+    // (M == 0: one block, which finds no row)
+    return launch_k(xent_compact_kernel<GRAD>, dim3(std::max((p.M + kCompactRows - 1) / kCompactRows, 1)), dim3(256), s, p);
+}
 
 template <int STEP>
 hipError_t launch_mixed(const XentArgs &p, long m, long n, bool f16, hipStream_t s) {
@@ -548,7 +605,7 @@ int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha, const void *X, 
     xent_layout(p, workspace, false, Wc);
     const bool f16 = dtype == SGEMM_DTYPE_F16;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    hipError_t e = launch_k(xent_compact_kernel<false>, dim3((M + kCompactRows - 1) / kCompactRows), dim3(256), s, p);
+    hipError_t e = launch_compact<false>(p, s);
     if (e == hipSuccess && Wc != nullptr) {
         e = pad_rows(W, ldw, 0, 1, N, K, Wc, s);
         p.W = Wc;
@@ -593,8 +650,7 @@ int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void
     xent_layout(p, workspace, true, Wc);
     const bool f16 = dtype == SGEMM_DTYPE_F16;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    // (M == 0: one block, which finds no row; dW is then zeros)
-    hipError_t e = launch_k(xent_compact_kernel<true>, dim3(std::max((M + kCompactRows - 1) / kCompactRows, 1)), dim3(256), s, p);
+    hipError_t e = launch_compact<true>(p, s);
     if (e == hipSuccess && Wc != nullptr) {
         e = pad_rows(W, ldw, 0, 1, N, K, Wc, s);
         p.W = Wc;

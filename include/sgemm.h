@@ -391,8 +391,8 @@ int sgemm_lowp_strided_batched(int dtype, int op_a, int op_b, int M, int N, int 
  * B + g*stride_b, op as in sgemm_lowp_op():
  *   C[rows of g] = alpha * A[rows of g] * op(B[g]) + beta * C[rows of g].
  * `offsets` is a device array of groups + 1 row numbers that do not decrease,
- * within 0 .. M (others are clamped to that range, and rows that two groups
- * then claim hold either's result).  Groups may be empty; rows of no group
+ * within 0 .. M (others are clamped to that range; what an array that
+ * decreases leaves in rows of C is unspecified).  Groups may be empty; rows of no group
  * are left as they were.  dtype_c: `dtype` or SGEMM_DTYPE_F32.  The gradient
  * with respect to A is the same call with op_b turned round, the one with
  * respect to B sgemm_lowp_grouped_wgrad.  K and N below 2^22 - 64, groups up
@@ -414,14 +414,17 @@ long long sgemm_lowp_grouped_workspace(int op_b, int groups, int M, int N, int K
  *   C[g] = alpha * A[rows of g]^T * D[rows of g] + beta * C[g],
  * A [M,K], D [M,N], C[g] K x N at C + g*stride_c (stride_c >=
  * (K-1)*ldc + N when groups > 1).  An empty group gives beta * C[g]
- * (zeros when beta is 0).  Otherwise as sgemm_lowp_grouped().
+ * (zeros when beta is 0).  Small matrices over many rows are summed in several
+ * shares of the rows, whose FP32 products are in the workspace and are added in
+ * a fixed order.  Otherwise as sgemm_lowp_grouped().
  */
 int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float alpha,
                              const void *A, int lda, const void *D, int ldd,
                              const int *offsets, float beta, void *C, int ldc,
                              long long stride_c, int dtype_c,
                              void *workspace, long long workspace_bytes, void *stream);
-long long sgemm_lowp_grouped_wgrad_workspace(int M, int N, int K, const void *A, int lda,
+long long sgemm_lowp_grouped_wgrad_workspace(int groups, int M, int N, int K,
+                                             const void *A, int lda,
                                              const void *D, int ldd);
 
 /*
@@ -430,8 +433,8 @@ long long sgemm_lowp_grouped_wgrad_workspace(int M, int N, int K, const void *A,
  *   lse[i] = log(sum_v exp(l[i][v])),  loss[i] = lse[i] - l[i][target[i]],
  * both FP32, without the M x N logits being in memory.  Rows with
  * target[i] == ignore_index give 0 in both, whatever X holds there; any other
- * target outside 0 .. N-1 gives a NaN loss.  K below 2^22 - 64, M and N up to
- * 2^30.
+ * target outside 0 .. N-1 gives a NaN loss.  K below 2^22 - 64, M up to 2^24,
+ * N up to 2^30.
  */
 int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha,
                     const void *X, int ldx, const void *W, int ldw,

@@ -86,6 +86,20 @@ def test_larger(T, G, K, N, dtype):
     assert_within(torch, lib.sgemm_grouped_wgrad(A, D, dev), ref, (T + 1) * 2 ** -23 * big, "wgrad")
 
 
+@pytest.mark.parametrize("off", [[0, 3000, 6000], [0, 5999, 6000], [100, 100, 5000], [0, 6000]], ids=str)
+@pytest.mark.parametrize("K,N", [(72, 40), (5, 131), (264, 200)])
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+def test_small_matrices_over_many_rows(K, N, off, out):
+    """The weight gradient summed in shares of the rows; beta joins in once."""
+    torch = torch_cuda()
+    A, D = ints(torch, (6000, K), -2, 2, torch.bfloat16, 3), ints(torch, (6000, N), -2, 2, torch.bfloat16, 4)
+    C = ints(torch, (len(off) - 1, K, N), -8, 8, getattr(torch, out), 5)
+    want = 0.5 * wgrad_ref(torch, A, D, off) + 2 * C.double()
+    A[:off[0]], A[off[-1]:] = float("nan"), float("nan")
+    lib.sgemm_grouped_wgrad(A, D, torch.tensor(off, dtype=torch.int32, device="cuda"), C=C, alpha=0.5, beta=2.0)
+    assert_equal(torch, C, want)
+
+
 @pytest.mark.parametrize("out", ["float32", "float16"])
 @pytest.mark.parametrize("pads", [(8, 16, 4, 0), (3, 1, 1, 0), (8, 8, 2, 1), (0, 0, 3, 8)])
 def test_strides_alpha_beta(pads, out):
@@ -236,7 +250,7 @@ def test_race_check_build(monkeypatch):
     their refill."""
     torch = torch_cuda()
     monkeypatch.setattr(capi, "_lib", capi.open_library(capi.POISON_LIB_PATH))
-    for T, K, N in ((60, 200, 264), (900, 264, 392), (3000, 520, 520)):
+    for T, K, N in ((60, 200, 264), (900, 264, 392), (3000, 520, 520), (5000, 72, 136)):
         off = [0, T // 3, T // 2, T]
         dev = torch.tensor(off, dtype=torch.int32, device="cuda")
         A, B = ints(torch, (T, K), -3, 3, torch.bfloat16, 1), ints(torch, (3, K, N), -3, 3, torch.bfloat16, 2)

@@ -81,6 +81,13 @@ def test_vocabulary_in_pieces(dtype):
     check(torch, *problem(torch, T, V, H, getattr(torch, dtype), 0.25))
 
 
+@pytest.mark.parametrize("T", [16384, 16385, 40001])
+def test_many_rows(T):
+    """Above 16384 rows they are counted by segments first."""
+    torch = torch_cuda()
+    check(torch, *problem(torch, T, 300, 16, torch.bfloat16, 0.5))
+
+
 @pytest.mark.parametrize("alpha", [0.25, -1.0, 0.0])
 def test_scaled_logits(alpha):
     torch = torch_cuda()

@@ -40,11 +40,12 @@ REFUSED = [
         (DIM, dict(lda=15)), (DIM, dict(ldd=31)), (DIM, dict(ldc=31)), (DIM, dict(stride_c=511)),
         (DIM, dict(groups=60000, K=1 << 20, N=1 << 20, lda=1 << 20, ldd=1 << 20, ldc=1 << 20, stride_c=1 << 40)),
         (NULL, dict(A=None)), (NULL, dict(D=None)), (NULL, dict(C=None)), (NULL, dict(offsets=None)),
-        (SMALL, dict(ldd=33)), (SMALL, dict(K=15))]),
+        (SMALL, dict(ldd=33)), (SMALL, dict(K=15)), (SMALL, dict(M=4000)),
+        (SMALL, dict(M=4000, workspace=AL, workspace_bytes=7 * 2 * 16 * 32 * 4 - 1))]),
     (capi.sgemm_lowp_xent, XENT, [
         (TYPE, dict(dtype=3)), (DIM, dict(M=-1)), (DIM, dict(N=0)), (DIM, dict(K=-1)), (DIM, dict(ldx=15)),
-        (DIM, dict(ldw=15)), (NULL, dict(X=None)), (NULL, dict(W=None)), (NULL, dict(target=None)),
-        (NULL, dict(loss=None)), (NULL, dict(lse=None)), (SMALL, dict(workspace=None)),
+        (DIM, dict(ldw=15)), (DIM, dict(M=(1 << 24) + 1)), (DIM, dict(N=(1 << 30) + 1)),
+        (NULL, dict(X=None)), (NULL, dict(W=None)), (NULL, dict(target=None)), (NULL, dict(loss=None)), (NULL, dict(lse=None)), (SMALL, dict(workspace=None)),
         (SMALL, dict(workspace=MIS)), (SMALL, dict(workspace_bytes=100))]),
     (capi.sgemm_lowp_xent_grad, GRAD, [
         (TYPE, dict(dtype=3)), (DIM, dict(M=-1)), (DIM, dict(N=0)), (DIM, dict(ldx=15)), (DIM, dict(lddx=15)),
@@ -56,7 +57,8 @@ REFUSED = [
         (DIM, dict(group=16)), (DIM, dict(group=256)), (DIM, dict(ldx=127)), (DIM, dict(ldc=31)),
         (NULL, dict(X=None)), (NULL, dict(packed=None)), (NULL, dict(scales=None)), (NULL, dict(C=None)),
         (UNSUP, dict(packed=0x10008)), (UNSUP, dict(scales=0x10004)), (UNSUP, dict(zeros=0x10002)),
-        (DIM, dict(M=(1 << 24) + 1)), (DIM, dict(K=1 << 23, ldx=1 << 23)), (SMALL, dict(X=MIS)),
+        (DIM, dict(M=(1 << 24) + 1)), (DIM, dict(K=1 << 23, ldx=1 << 23)),
+        (DIM, dict(M=1 << 24, N=1 << 30, ldc=1 << 30)), (SMALL, dict(X=MIS)),
         (SMALL, dict(ldx=129, workspace=AL, workspace_bytes=3 * 256 - 1))]),
     (capi.sgemm_w4_quantize, PACK, [
         (TYPE, dict(dtype=3)), (DIM, dict(N=-1)), (DIM, dict(group=48)), (DIM, dict(ldw=127)), (NULL, dict(W=None)),
@@ -92,8 +94,11 @@ def test_workspaces():
     assert ws(0, 2, 64, 32, 13, AL, 13, AL, 32, 512) == 64 * 16 * 2           # rows of B past K are not read
     assert ws(1, 2, 64, 30, 13, AL, 13, AL, 13, 390) == 64 * 16 * 2 + 2 * 30 * 16 * 2
     assert ws(2, 2, 64, 32, 16, AL, 16, AL, 32, 512) == OP
-    assert capi.sgemm_lowp_grouped_wgrad_workspace(64, 32, 16, AL, 16, AL, 32) == 0
-    assert capi.sgemm_lowp_grouped_wgrad_workspace(64, 30, 16, AL, 16, AL, 30) == 64 * 32 * 2
+    assert capi.sgemm_lowp_grouped_wgrad_workspace(2, 64, 32, 16, AL, 16, AL, 32) == 0
+    assert capi.sgemm_lowp_grouped_wgrad_workspace(2, 64, 30, 16, AL, 16, AL, 30) == 64 * 32 * 2
+    # 4000 rows of 2 groups: seven shares of 256 rows or more
+    assert capi.sgemm_lowp_grouped_wgrad_workspace(2, 4000, 32, 16, AL, 16, AL, 32) == 7 * 2 * 16 * 32 * 4
+    assert capi.sgemm_lowp_grouped_wgrad_workspace(2, 4000, 4096, 4096, AL, 4096, AL, 4096) == 0
     assert capi.sgemm_lowp_xent_workspace(0, 100, 16, AL, 16, AL, 16, 0) == 0
     # the backward keeps one piece of the vocabulary: far less than the logits
     M, N, K = 8192, 128000, 4096
