@@ -253,14 +253,14 @@ def _same_type(a, a_name, b, b_name):
 
 
 def _one_device(first, *named):
-    """The device of `first` and of the (name, tensor) pairs (None tensors left out)."""
-    device = first.device
-    if device.type != "cuda":
+    """The index of the device of `first` and of the (name, tensor) pairs (None tensors left out)."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("operands must be device tensors")
     for name, t in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"operands must be on one device: {name} is on {t.device}, not on {device}")
-    return device
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"operands must be on one device: {name} is on {t.device}, not on {first.device}")
+    return index
 
 
 def _vector(t, name, dtype, size):
@@ -272,19 +272,19 @@ def _vector(t, name, dtype, size):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _run(device, stream, call, *operands):
-    """call(stream handle), with `device` current and `stream` (if given)
+def _run(index, stream, call, *operands):
+    """call(stream handle), with the device current and `stream` (if given)
     current on it, so that what it allocates belongs to the stream it runs on;
     the operands' memory is then kept until that stream has used it."""
     import torch
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(_stream_handle(device, None))
-    with _device_ctx(device), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
+    if stream is None and index == torch.cuda.current_device():
+        return call(_stream_handle(operands[0].device, None))
+    with torch.cuda.device(index), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
         if stream is not None:
             for t in operands:
                 if t is not None:
                     t.record_stream(stream)
-        return call(_stream_handle(device, stream))
+        return call(_stream_handle(operands[0].device, stream))
 
 
 def _check(status):
@@ -293,14 +293,13 @@ def _check(status):
     return status
 
 
-def _with_workspace(device, call, size):
-    """call(workspace address, bytes), with a workspace of size() bytes if it
-    asks for one (it has then enqueued nothing)."""
-    status = call(None, 0)
+def _finish(status, call, size, operand):
+    """After call(None, 0) gave `status`: an error, or again with a workspace
+    of size() bytes if it asks for one (it has then enqueued nothing)."""
     if status == capi.SGEMM_STATUS_SCRATCH_TOO_SMALL:
         import torch
         n = _check(size())
-        keep = torch.empty(n, dtype=torch.uint8, device=device)
+        keep = operand.new_empty(n, dtype=torch.uint8)
         status = call(keep.data_ptr(), n)
     _check(status)
 
@@ -324,13 +323,13 @@ def _check_result(C, shape, out_dtype, operand, beta):
         raise ValueError("C must have unit column stride (row-major)")
 
 
-def _result(C, shape, out_dtype, device):
+def _result(C, shape, out_dtype, operand):
     """(C, its type's code, leading dimension), allocated here where it is None."""
     import torch
     rows, cols = shape[-2:]
     if C is None:
         dtype = out_dtype or torch.float32
-        return torch.empty(shape, dtype=dtype, device=device), _CODES[dtype], max(cols, 1)
+        return operand.new_empty(shape, dtype=dtype), _CODES[dtype], max(cols, 1)
     step = C.stride(-2)
     return C, _CODES[C.dtype], step if rows > 1 or step >= cols > 0 else max(cols, 1)
 
@@ -377,10 +376,14 @@ def sgemm_grouped(A, B, offsets, C=None, alpha=1.0, beta=0.0, trans_b=False, out
     operands = (A.data_ptr(), lda, B.data_ptr(), ldb, sb if held > 1 else 0)
 
     def call(h):
-        out, code_c, ldc = _result(C, (M, N), out_dtype, device)
-        args = (code, op, groups, M, N, K, float(alpha), *operands, offsets.data_ptr(), float(beta), out.data_ptr(), ldc, code_c)
-        _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped(*args, ws, size, h),
-                        lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *operands))
+        out, code_c, ldc = _result(C, (M, N), out_dtype, A)
+        args = (code, op, groups, M, N, K, float(alpha), *operands, offsets.data_ptr(), float(beta), out.data_ptr(),
+                ldc, code_c)
+        product = capi.load().sgemm_lowp_grouped
+        status = product(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: product(*args, ws, size, h),
+                    lambda: capi.sgemm_lowp_grouped_workspace(op, groups, M, N, K, *operands), A)
         return out
     return _run(device, stream, call, A, B, offsets, C)
 
@@ -404,11 +407,14 @@ def sgemm_grouped_wgrad(A, D, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=No
     operands = (A.data_ptr(), lda, D.data_ptr(), ldd)
 
     def call(h):
-        out, code_c, ldc = _result(C, (groups, K, N), out_dtype, device)
+        out, code_c, ldc = _result(C, (groups, K, N), out_dtype, A)
         args = (code, groups, M, N, K, float(alpha), *operands, offsets.data_ptr(), float(beta), out.data_ptr(), ldc,
                 out.stride(0) if groups > 1 else 0, code_c)
-        _with_workspace(device, lambda ws, size: capi.sgemm_lowp_grouped_wgrad(*args, ws, size, h),
-                        lambda: capi.sgemm_lowp_grouped_wgrad_workspace(groups, M, N, K, *operands))
+        product = capi.load().sgemm_lowp_grouped_wgrad
+        status = product(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: product(*args, ws, size, h),
+                    lambda: capi.sgemm_lowp_grouped_wgrad_workspace(groups, M, N, K, *operands), A)
         return out
     return _run(device, stream, call, A, D, offsets, C)
 
@@ -440,9 +446,8 @@ def sgemm_xent(X, W, target, alpha=1.0, ignore_index=-100, stream=None):
     size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *operands, 0))
 
     def call(h):
-        out = torch.empty((2, M), dtype=torch.float32, device=device)
-        loss, lse = out.unbind()
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        loss, lse = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
+        ws = X.new_empty(size, dtype=torch.uint8)
         _check(capi.sgemm_lowp_xent(code, M, N, K, float(alpha), *operands, target.data_ptr(), int(ignore_index), loss.data_ptr(),
                                     lse.data_ptr(), ws.data_ptr(), size, h))
         return loss, lse
@@ -470,9 +475,9 @@ def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need
     size = _check(capi.sgemm_lowp_xent_workspace(M, N, K, *operands, 1))
 
     def call(h):
-        dX = torch.empty((M, K), dtype=X.dtype, device=device) if need_dx else None
-        dW = torch.empty((N, K), dtype=X.dtype, device=device) if need_dw else None
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        dX = X.new_empty((M, K)) if need_dx else None
+        dW = X.new_empty((N, K)) if need_dw else None
+        ws = X.new_empty(size, dtype=torch.uint8)
         _check(capi.sgemm_lowp_xent_grad(code, M, N, K, float(alpha), *operands, target.data_ptr(), int(ignore_index),
                                          lse.data_ptr(), dloss.data_ptr(), step, _address(dX), max(K, 1), _address(dW),
                                          max(K, 1), ws.data_ptr(), size, h))
@@ -539,12 +544,14 @@ def sgemm_w4(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     _check_result(C, (M, N), out_dtype, X, beta)
 
     def call(h):
-        out, code_c, ldc = _result(C, (M, N), out_dtype, device)
+        out, code_c, ldc = _result(C, (M, N), out_dtype, X)
         x = X.data_ptr()
-        args = (code, M, N, K, float(alpha), x, ldx, packed.data_ptr(), scales.data_ptr(), _address(zeros), group, float(beta),
-                out.data_ptr(), ldc, code_c)
-        _with_workspace(device, lambda ws, size: capi.sgemm_w4(*args, ws, size, h),
-                        lambda: capi.sgemm_w4_workspace(M, K, x, ldx))
+        args = (code, M, N, K, float(alpha), x, ldx, packed.data_ptr(), scales.data_ptr(), _address(zeros), group,
+                float(beta), out.data_ptr(), ldc, code_c)
+        product = capi.load().sgemm_w4
+        status = product(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: product(*args, ws, size, h), lambda: capi.sgemm_w4_workspace(M, K, x, ldx), X)
         return out
     return _run(device, stream, call, X, packed, scales, zeros, C)
 
@@ -561,9 +568,8 @@ def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
     device = _one_device(W)
 
     def call(h):
-        out = W4Weight(torch.empty((N, Kp // 2), dtype=torch.uint8, device=device),
-                       torch.empty((N, Kp // group), dtype=W.dtype, device=device),
-                       torch.empty((N, Kp // group), dtype=torch.uint8, device=device) if zeros else None, K, group)
+        out = W4Weight(W.new_empty((N, Kp // 2), dtype=torch.uint8), W.new_empty((N, Kp // group)),
+                       W.new_empty((N, Kp // group), dtype=torch.uint8) if zeros else None, K, group)
         _check(capi.sgemm_w4_quantize(code, N, K, W.data_ptr(), ldw, group, out.packed.data_ptr(),
                                       out.scales.data_ptr(), _address(out.zeros), h))
         return out
@@ -572,13 +578,12 @@ def sgemm_w4_quantize(W, group=128, zeros=False, stream=None):
 
 def sgemm_w4_dequantize(W, stream=None):
     """The values [N,K] a W4Weight stands for, rounded to its scales' type."""
-    import torch
     N = _w4(W)
     packed, scales, zeros, K, group = W
     device = _one_device(packed, ("scales", scales), ("zeros", zeros))
 
     def call(h):
-        out = torch.empty((N, K), dtype=scales.dtype, device=device)
+        out = scales.new_empty((N, K))
         _check(capi.sgemm_w4_dequantize(_codes()[out.dtype], N, K, packed.data_ptr(), scales.data_ptr(),
                                         _address(zeros), group, out.data_ptr(), max(K, 1), h))
         return out
