@@ -252,7 +252,7 @@ hipError_t launch_rows(const GroupArgs &p, bool tb, bool f16, bool out16, hipStr
 
 // Shares of the rows of each group: small matrices over many rows would leave
 // most of the chip idle, so as many as fill it, of 256 rows of an average group
-// at least (6984 rows in 2 groups, 192 x 656 each: 41 -> 14 us).
+// at least (6984 rows in 2 groups, 192 x 656 each: 39.5 -> 19 us).
 int wgrad_shares(int groups, int M, int N, int K) {
     const long tiles = (K + 127L) / 128 * ((N + 127L) / 128) * std::max(groups, 1);
     return (int)std::max(1L, std::min(512 / std::max(tiles, 1L), M / std::max(groups, 1) / 256L));

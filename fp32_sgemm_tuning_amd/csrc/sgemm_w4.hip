@@ -232,10 +232,10 @@ __device__ __forceinline__ i32x4 centred(unsigned w, unsigned zs) {
 // to the FP32 total with the group's scale.  Those multiply-adds and the
 // unpacking take about as many cycles as the matrix instructions, so every
 // matrix instruction is followed by its share of them: left to itself the
-// compiler gathers each kind, and the same tile runs 169 us instead of 152
-// (2048 x 8192 x 4096, groups of 64 with zero points, FP16: 903 TFLOP/s).  Two
-// workgroups of four waves share a compute unit; one of eight, in step at
-// every barrier, takes 167 us.  The product is formed transposed, as in
+// compiler gathers each kind, and the same tile took a ninth longer.  2048 x
+// 8192 x 4096, groups of 64 with zero points, FP16: 165 us, 833 TFLOP/s; two
+// workgroups of four waves share a compute unit (one of eight, in step at every
+// barrier, takes 170 us).  The product is formed transposed, as in
 // sgemm_lowp.hpp: lane l holds row l%16 and columns 4*(l/16) .. +3.
 template <int MI, int NB, int WM, int WN, int GROUP, bool ZEROS, bool F16, bool OUT16>
 __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
@@ -554,13 +554,14 @@ hipError_t launch_tile(const W4Args &p, int group, bool f16, bool out16, hipStre
 
 // Up to 64 rows: the widest block of W that still leaves 200 workgroups (more
 // columns share the loads of X, fewer workgroups leave compute units idle:
-// 8 x 14336 x 4096 17.9 / 16.4 / 14.1 us on 16, 32 and 64 columns, 1 x 4096 x
-// 4096 5.3 / 6.6 / 10.1 us).  More rows: the shortest of three predicted times,
-// all for K = 4096, per 256 workgroups of a kernel once a compute unit's share
-// is full: 32 x 64 blocks of the first kernel 19.6 us, 64 x 128 tiles 27 us
-// (41 at least), 128 x 128 tiles 38 us (51 at least); measured on N = 8192 for
-// 128 rows 37.7 / 42.6 / 51.4 us, for 256 rows 73.9 / 42.0 / 57, for 2048 rows
-// 590 / 216 / 152.
+// 8 x 14336 x 4096 18.6 / 16.7 / 14.2 us on 16, 32 and 64 columns, 16 x 8192 x
+// 4096 12.7 / 9.3 / 11.8, 1 x 4096 x 4096 5.3 / 6.6 / 10.1).  More rows: the
+// shortest of three predicted times, all for K = 4096, per 256 workgroups of a
+// kernel once a compute unit's share is full: 32 x 64 blocks of the first
+// kernel 19.6 us, 64 x 128 tiles 27 us (41 at least), 128 x 128 tiles 41 us (51
+// at least); measured on N = 8192 for 128 rows 37.7 / 42.3 / 51.6 us, for 256
+// rows 73.9 / 43.9 / 51.7, for 512 rows - / 59.0 / 53.3, for 2048 rows
+// - / 220 / 165.
 hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
     auto blocks = [&](int bm, int bn) { return (p.M + bm - 1L) / bm * ((p.N + bn - 1L) / bn); };
     if (p.M <= 16)
@@ -568,7 +569,7 @@ hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream
                : blocks(16, 32) >= 200 ? launch_rows<1, 2, 8>(p, group, f16, out16, s)
                                        : launch_rows<1, 1, 8>(p, group, f16, out16, s);
     const double rows = std::max(19.6, 19.6 * blocks(32, 64) / 256), t64 = std::max(41.0, 27.0 * blocks(64, 128) / 256),
-                 t128 = std::max(51.0, 38.0 * blocks(128, 128) / 256);
+                 t128 = std::max(51.0, 41.0 * blocks(128, 128) / 256);
     if (p.M <= 64 || (rows <= t64 && rows <= t128))
         return blocks(32, 64) >= 200   ? launch_rows<2, 4, 4>(p, group, f16, out16, s)
                : blocks(32, 32) >= 200 ? launch_rows<2, 2, 8>(p, group, f16, out16, s)
