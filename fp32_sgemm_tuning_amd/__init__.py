@@ -279,6 +279,8 @@ def _run(index, stream, call, *operands):
     import torch
     if stream is None and index == torch.cuda.current_device():
         return call(_stream_handle(operands[0].device, None))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream belongs to {stream.device}, the operands to {operands[0].device}")
     with torch.cuda.device(index), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
         if stream is not None:
             for t in operands:

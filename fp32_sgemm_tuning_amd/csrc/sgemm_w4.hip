@@ -409,73 +409,101 @@ struct PackArgs {
     bool vec;                           // rows of W are whole aligned 16-byte chunks
 };
 
-// Eight elements k .. k+7 of a row, zero behind K.
-__device__ __forceinline__ void load8(const unsigned short *row, int k, int K, bool vec, unsigned short (&v)[8]) {
-    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-    if (vec && k < K) {
-        const u16x8 x = *reinterpret_cast<const u16x8 *>(row + k);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = x[e];
+// Eight elements k .. k+7 of a row, zero behind K, two to a register.
+__device__ __forceinline__ i32x4 load8(const unsigned short *row, int k, int K, bool vec) {
+    i32x4 v = {0, 0, 0, 0};
+    if (vec) {
+        if (k < K) v = *reinterpret_cast<const i32x4 *>(row + k);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = k + e < K ? row[k + e] : (unsigned short)0;
+        for (int e = 0; e < 8; ++e)
+            if (k + e < K) v[e >> 1] |= (int)row[k + e] << (16 * (e & 1));
     }
+    return v;
 }
 
-// One thread per 8 consecutive k; the GROUP / 8 threads of a group find its
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// One thread per 32 consecutive k (word (j, s) of a chunk holds k = 32 s + 8 j:
+// a thread's four words have its s); the GROUP / 32 threads of a group find its
 // extremes together.  s is rounded to 16 bits first and q chosen for the
 // rounded s: symmetric s = max|w| / 7, z = 8; with zero points
 // s = (max(w, 0) - min(w, 0)) / 15, z = round(-min(w, 0) / s);
 // q = round(w / s) + z within 0 .. 15, halves to even.  s == 0 (a group of
 // zeros, or one whose s rounds to 0) gives q = z.  A NaN or an infinity in a
-// group makes its s NaN.
+// group makes its s NaN.  What does not depend on an element (the place, the
+// extremes, s) is done once per 32 of them: 14336 x 4096 42 us, 2.8 TB/s of W;
+// a thread per 8 was bound by its vector instructions, at 50.
 template <int GROUP, bool ZEROS, bool F16>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(PackArgs p) {
-    constexpr int TG = GROUP / 8;
-    const long per_row = (long)p.chunks * 16, all = per_row * p.N;
-    for (long t0 = blockIdx.x * 256L; t0 < all; t0 += gridDim.x * 256L) {       // whole groups: 256 and all are multiples of 16
+    constexpr int TG = GROUP / 32;
+    const long per_row = (long)p.chunks * 4, all = per_row * p.N;
+    for (long t0 = blockIdx.x * 256L; t0 < all; t0 += gridDim.x * 256L) {       // whole groups: 256 and all are multiples of 4
         const long t = t0 + threadIdx.x;
         if (t >= all) continue;
         const long row = t / per_row;
-        const int i = (int)(t - row * per_row), k = 8 * i;
-        unsigned short raw[8];
-        load8(p.W + row * p.ldw, k, p.K, p.vec, raw);
-        float w[8], lo = 0.f, hi = 0.f;
-        bool bad = false;
+        const int i = (int)(t - row * per_row);
+        i32x4 raw[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] = widen16<F16>(raw[e]);
-            lo = fminf(lo, w[e]);
-            hi = fmaxf(hi, w[e]);
-            bad |= !(fabsf(w[e]) < __builtin_inff());
+        for (int j = 0; j < 4; ++j) raw[j] = load8(p.W + row * p.ldw, 32 * i + 8 * j, p.K, p.vec);
+        // The extremes from the bits, two values to an instruction: the largest
+        // signed 16-bit integer is the largest value, if any is above 0, the
+        // largest unsigned one the most negative, if any is below; then both
+        // magnitudes of the group's threads together.
+        s16x2 high = {0, 0};
+        u16x2 low = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int two = raw[e / 4][e % 4];
+            high = __builtin_elementwise_max(high, __builtin_bit_cast(s16x2, two));
+            low = __builtin_elementwise_max(low, __builtin_bit_cast(u16x2, two));
         }
-        if (bad) hi = __builtin_inff();
+        const unsigned top = max((int)high[0], (int)high[1]), bottom = max((unsigned)low[0], (unsigned)low[1]);
+        u16x2 both = {(unsigned short)top, (unsigned short)(bottom > 0x8000u ? bottom & 0x7FFFu : 0u)};
 #pragma unroll
         for (int d = 1; d < TG; d <<= 1) {
-            lo = fminf(lo, __shfl_xor(lo, d));
-            hi = fmaxf(hi, __shfl_xor(hi, d));
+            const int other = __shfl_xor(__builtin_bit_cast(int, both), d);
+            both = __builtin_elementwise_max(both, __builtin_bit_cast(u16x2, other));
         }
-        float s = ZEROS ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
-        if (hi == __builtin_inff()) s = __builtin_nanf("");
+        const float hi = widen16<F16>(both[0]), lo = widen16<F16>(both[1]);       // lo: -min(w, 0)
+        constexpr unsigned short kInfinite = F16 ? 0x7C00 : 0x7F80;
+        float s = ZEROS ? (hi + lo) / 15.f : fmaxf(hi, lo) / 7.f;
+        if (both[0] >= kInfinite || both[1] >= kInfinite) s = __builtin_nanf("");
         const unsigned short s16 = to16<F16>(s);
         s = widen16<F16>(s16);
         const bool none = !(s > 0.f);                       // 0 or NaN
         const float step = none ? 1.f : s;
-        const float z = ZEROS ? (s == s ? fminf(rintf(-lo / step), 15.f) : 0.f) : 8.f;
-        // round(w / s) without the division where w * (1 / s), off by less than
-        // 2^-17 for |w / s| below 32, is further than that from a half (the
-        // divisions took over half of the kernel's time)
-        const float inverse = __builtin_amdgcn_rcpf(step);
-        unsigned word = 0;
+        const float z = ZEROS ? (s == s ? fminf(rintf(lo / step), 15.f) : 0.f) : 8.f;
+        // round(w / s) without divisions where w * (1 / s), off by less than
+        // 2^-17 for |w / s| below 32, lies further than that from a half
+        const float inverse = none ? 0.f : __builtin_amdgcn_rcpf(step);
+        const int c = i >> 2, run = i & 3;
+        unsigned *words = reinterpret_cast<unsigned *>(p.packed + (row * p.chunks + c) * 64 + 4 * run);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float n = w[e] * inverse, r = rintf(n);
-            if (!(fabsf(n - r) < 0.4999f && fabsf(n) < 32.f)) r = rintf(w[e] / step);
-            const float q = none ? z : fminf(fmaxf(r + z, 0.f), 15.f);
-            word |= (unsigned)q << (4 * (e >> 1) + 16 * (e & 1));
+        for (int j = 0; j < 4; ++j) {
+            auto value = [&](int e) {
+                return widen16<F16>((unsigned short)((unsigned)raw[j][e >> 1] >> (16 * (e & 1))));
+            };
+            float n[8], far = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = value(e) * inverse;
+                n[e] = rintf(x);
+                far = fmaxf(far, fabsf(x - n[e]));
+            }
+            if (!none && (!(far < 0.4999f) || step < 0x1p-100f)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) n[e] = rintf(value(e) / step);
+            }
+            unsigned word = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float q = none ? z : fminf(fmaxf(n[e] + z, 0.f), 15.f);
+                word |= (unsigned)q << (4 * (e >> 1) + 16 * (e & 1));
+            }
+            words[4 * j] = word;
         }
-        const int c = i >> 4, in = i & 15;                  // word s = in / 4 of run j = in % 4
-        *reinterpret_cast<unsigned *>(p.packed + (row * p.chunks + c) * 64 + 16 * (in & 3) + 4 * (in >> 2)) = word;
         if (i % TG == 0) {
             const long g = row * p.chunks * (kChunk / GROUP) + i / TG;
             p.scales[g] = s16;
@@ -593,7 +621,7 @@ bool packed_ok(const void *packed, const void *scales, const void *zeros) {
 
 int chunks_of(int K) { return (K + kChunk - 1) / kChunk; }
 
-unsigned pack_blocks(const PackArgs &p) { return (unsigned)std::min((p.N * p.chunks * 16L + 255) / 256, 8192L); }
+unsigned pack_blocks(long threads) { return (unsigned)std::min((threads + 255) / 256, 8192L); }
 
 }  // namespace
 }  // namespace sgemm_mi355x
@@ -652,7 +680,7 @@ int sgemm_w4_quantize(int dtype, int N, int K, const void *W, int ldw, int group
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const hipError_t e = with_form(group, zeros != nullptr, dtype == SGEMM_DTYPE_F16, [&](auto g, auto z, auto f) {
         return launch_k(w4_quantize_kernel<decltype(g)::value, decltype(z)::value, decltype(f)::value>,
-                        dim3(pack_blocks(p)), dim3(256), s, p);
+                        dim3(pack_blocks(p.N * p.chunks * 4L)), dim3(256), s, p);
     });
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
@@ -673,7 +701,7 @@ int sgemm_w4_dequantize(int dtype, int N, int K, const void *packed, const void 
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const hipError_t e = with_form(group, zeros != nullptr, dtype == SGEMM_DTYPE_F16, [&](auto g, auto z, auto f) {
         return launch_k(w4_dequantize_kernel<decltype(g)::value, decltype(z)::value, decltype(f)::value>,
-                        dim3(pack_blocks(p)), dim3(256), s, p);
+                        dim3(pack_blocks(p.N * p.chunks * 16L)), dim3(256), s, p);
     });
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }

@@ -51,3 +51,51 @@ def test_training_step_then_token():
     # the product takes the weights unrounded, the values were rounded once to bf16
     assert ((logits.double() - ref).abs() <= 2 ** -7 * (token.double().abs() @ values.abs().T.contiguous())).all()
     assert ((logits.double() - ref).norm() / ref.norm()).item() < 2 ** -8
+
+
+def test_weights_past_32_bits():
+    """Weights of more than 2^32 bytes (the last rows of each lie behind)."""
+    torch = torch_cuda()
+    e = torch.bfloat16
+    # (products of -1, 0 and 1: sums are exact)
+    B = torch.randint(-1, 2, (3, 32768, 32768), device="cuda", dtype=torch.int8).to(e)
+    A = torch.randint(-1, 2, (70, 32768), device="cuda", dtype=torch.int8).to(e)
+    dev = torch.tensor([0, 20, 30, 70], dtype=torch.int32, device="cuda")
+    C = lib.sgemm_grouped(A, B, dev)
+    assert torch.equal(C[30:, -300:].double(), A[30:].double() @ B[2][:, -300:].double().contiguous())
+    C = lib.sgemm_grouped(A, B, dev, trans_b=True)
+    assert torch.equal(C[30:, -300:].double(), A[30:].double() @ B[2][-300:].double().T.contiguous())
+    del B, C
+    D = torch.randint(-1, 2, (70, 32768), device="cuda", dtype=torch.int8).to(e)
+    G = lib.sgemm_grouped_wgrad(A, D, dev, out_dtype=e)
+    assert torch.equal(G[2][-300:].double(), A[30:, -300:].double().T.contiguous() @ D[30:].double())
+    del G
+    W = torch.randint(-1, 2, (600001, 4096), device="cuda", dtype=torch.int8).to(e)
+    X = torch.randint(-1, 2, (40, 4096), device="cuda", dtype=torch.int8).to(e)
+    target = torch.arange(600001 - 40, 600001, device="cuda")
+    loss, lse = lib.sgemm_xent(X, W, target, alpha=2.0 ** -6)
+    logits = torch.cat([2.0 ** -6 * (X.double() @ w.double().T.contiguous()) for w in W.split(50000)], 1)
+    ref = torch.logsumexp(logits, 1)
+    # exact logits: lse is off by (17 + V / 8192) * 2^-22 at most for the exponentials and the sum, and the logarithm
+    tol = (17 + 600001 / 8192) * 2 ** -22 + 2 ** -21 * (ref.abs() + 1)
+    assert ((lse.double() - ref).abs() <= tol).all()
+    rows = torch.arange(40, device="cuda")
+    assert ((loss.double() - (ref - logits[rows, target])).abs() <= 2 * tol).all()
+    _, dW = lib.sgemm_xent_grad(X, W, target, lse, torch.ones(40, device="cuda"), alpha=2.0 ** -6, need_dx=False)
+    P = torch.exp(logits[:, -100:] - ref[:, None])
+    P[rows, 60 + rows] -= 1
+    want = 2.0 ** -6 * (P.T.contiguous() @ X.double())
+    big = 2.0 ** -6 * (P.abs().T.contiguous() @ X.double().abs())
+    assert ((dW[-100:].double() - want).abs() <= (2 ** -8 + 2 ** -12) * big + 2 ** -8 * want.abs()).all()
+    del W, dW, logits
+    packed = torch.randint(0, 256, (300000, 16384), dtype=torch.uint8, device="cuda")
+    scales = torch.ones(300000, 256, dtype=e, device="cuda")
+    for M in (1, 100):
+        x = torch.randint(-1, 2, (M, 32768), device="cuda", dtype=torch.int8).to(e)
+        whole = lib.sgemm_w4(x, lib.W4Weight(packed, scales, None, 32768, 128))
+        last = lib.W4Weight(packed[-70:].clone(), scales[-70:].clone(), None, 32768, 128)
+        assert torch.equal(whole[:, -70:], lib.sgemm_w4(x, last))
+        values = lib.sgemm_w4_dequantize(last).double()        # exact in bf16 here
+        assert torch.equal(whole[:, -70:].double(), x.double() @ values.T.contiguous())
+    tail = lib.sgemm_w4_dequantize(lib.W4Weight(packed, scales, None, 32768, 128))[-70:]
+    assert torch.equal(tail.double(), values)
