@@ -2,10 +2,11 @@
 // of A are in groups (offsets[g] .. offsets[g+1], read on the device), each
 // with a matrix B[g] of its own.
 //
-//   group_rows_kernel   C[rows of g] = alpha * A[rows of g] * op(B[g]) + beta * C
+//   group_rows_kernel,
+//   group_mixed_kernel  C[rows of g] = alpha * A[rows of g] * op(B[g]) + beta * C
 //   group_k_kernel      C[g] = alpha * A[rows of g]^T * D[rows of g] + beta * C[g]
 //
-// Both run the K loop of sgemm_lowp.hpp on one block tile.  The host does
+// They run the K loop of sgemm_lowp.hpp on one block tile.  The host does
 // not know the groups' sizes, so the first kernels' grids cover the most
 // tiles that any split of the rows can have, floor((M + g*(BM-1)) / BM) tile
 // rows for g = min(groups, M) groups, and a workgroup finds its tile from
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
     if ((int)blockIdx.x >= list.total) return;
     int g = 0, lo = 0, rows = 0, tm = 0, tn = 0;
     list.find(xcd_run(blockIdx.x, list.total), g, lo, rows, tm, tn);
-    group_tile<T, F16, TB, OUT16>(p, lds, g, lo, rows, tm * T::BM, tn * T::BN);
+    if (tm * T::BM < rows) group_tile<T, F16, TB, OUT16>(p, lds, g, lo, rows, tm * T::BM, tn * T::BN);
 }
 
 // Tiles of 256 x 256 with a finer last round.
