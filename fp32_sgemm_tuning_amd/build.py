@@ -6,8 +6,8 @@ twin libsgemm_poison.so.
 libsgemm_poison.so is the same library with the lean FP32 and the 16-bit
 kernel units compiled with SGEMM_LDS_POISON=1: every LDS stage is filled
 with NaN bits as soon as its last reader has passed its barrier, so a
-missing barrier gives a wrong result (tests only; the C-ABI object is the
-normal build's).
+missing barrier gives a wrong result (tests only; the units without such
+kernels are the normal build's).
 
 Flags: -O3 for gfx950 only, packed-FP32 instructions disabled
 (``-Xclang -target-feature -Xclang -packed-fp32-ops``; the host pass warns
@@ -45,9 +45,10 @@ UNITS = [
     ("sgemm_w4.hip", VGPR_FORM),
 ]
 SOURCES = [os.path.join(CSRC, u) for u, _ in UNITS]
-# units rebuilt with the LDS poison for the race-check library (the rest of
-# that library is the normal build's sgemm.o)
-POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u != "sgemm.hip"]
+# units rebuilt with the LDS poison for the race-check library; the others,
+# which hold no kernel on the poisoned K loops, are linked as they are
+PLAIN_UNITS = ("sgemm.hip", "sgemm_w4.hip")
+POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u not in PLAIN_UNITS]
 DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp", "sgemm_lowp.hpp",
                                                      "sgemm_tile16.hpp")] + \
     [os.path.join(INCLUDE, "sgemm.h")]
@@ -113,8 +114,8 @@ def build(verbose: bool = False, isa: bool = False) -> str:
     if failed:
         raise RuntimeError("hipcc failed on " + ", ".join(u for u, _ in failed))
     _link(objs, LIB, verbose)
-    # the race-check library: the normal C-ABI object and the poisoned kernels
-    _link([objs[0]] + poison_objs, POISON_LIB, verbose)
+    # the race-check library: the normal objects of the plain units and the poisoned kernels
+    _link([o for (u, _), o in zip(UNITS, objs) if u in PLAIN_UNITS] + poison_objs, POISON_LIB, verbose)
     return LIB
 
 
