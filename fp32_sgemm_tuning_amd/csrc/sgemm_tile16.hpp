@@ -198,9 +198,12 @@ __device__ __forceinline__ f32x4 sum_shares(const float *at, long step, int shar
 
 inline long ceil_to(long n, long to) { return (n + to - 1) / to * to; }
 
-// Largest leading dimension of the 16-bit kernels' operands: 256 rows stay
-// within the 31-bit range of a buffer descriptor.
+// Largest leading dimension of the 16-bit kernels' operands: 256 rows of a K
+// tile, or with the operand transposed the K tile's 64 of 256 columns, stay
+// within the 31-bit range of a buffer descriptor, so that kOutOfRange lies
+// behind it.
 constexpr int kMaxLd16 = (1 << 22) - 64;
+static_assert(2L * (255L * kMaxLd16 + 64) <= kOutOfRange && 2L * (63L * kMaxLd16 + 256) <= kOutOfRange, "descriptor range");
 
 inline bool chunk_rows(const void *p, long ld, long cols) {     // rows of whole 16-byte chunks
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= kMaxLd16;

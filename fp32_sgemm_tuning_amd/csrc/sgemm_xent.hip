@@ -464,8 +464,10 @@ __global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int share
 // kernel that writes it and the two that read it.
 constexpr long kPieceBytes = 256L << 20;
 
+// (and of the columns of P what the K loop takes as a leading dimension, which
+// few rows would pass)
 long piece_columns(int M, int N) {
-    const long most = std::max(kPieceBytes / 2 / std::max(M, 1) / 256 * 256, 1024L);
+    const long most = std::min(std::max(kPieceBytes / 2 / std::max(M, 1) / 256 * 256, 1024L), kMaxLd16 / 256 * 256L);
     const long pieces = (N + most - 1) / most;
     return ceil_to((N + pieces - 1) / pieces, 256);
 }
