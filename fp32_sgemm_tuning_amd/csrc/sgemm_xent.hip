@@ -19,12 +19,21 @@
 // dlogits_tile forms the piece of the logits again and stores
 // P_iv * dloss_i / max|dloss| in 16 bits, then xent_dx_kernel adds its
 // product with the piece of W to an FP32 sum, and dw_tile writes the piece of
-// dW.  P lies in [-1, 1] and the scaled dloss too, so no 16-bit
-// range is left whatever the loss is scaled by; the factor max|dloss| is put
-// back in FP32.  Rounding this product to the inputs' 16 bits is what lets
-// the two gradient products run on the 16-bit matrix instructions; it is off
-// by at most half a step of each term (bf16 2^-8, fp16 2^-11 relative to
+// dW.  P lies in [-1, 1] and the scaled dloss too, so the top of the 16-bit
+// range is never passed whatever the loss is scaled by; the factor max|dloss|
+// is put back in FP32.  Rounding this product to the inputs' 16 bits is what
+// lets the two gradient products run on the 16-bit matrix instructions; it is
+// off by at most half a step of each term (bf16 2^-8, fp16 2^-11 relative to
 // the term), the size of the gradients' own final rounding.
+//
+// FP16 has no values below 2^-24 and only ones with fewer bits below 2^-14,
+// where most of P lies.  There P is stored times 2^15, powers of two stand in
+// place of max|dloss| (the next above it), and a row whose |dloss| is below 2^-6
+// of that is stored over the next power above its own |dloss|, so that its dX
+// does not depend on the other rows': a term is off by 2^-11 of itself or, if
+// that is more, 2^-34 of its row's |dloss|.  Before the product of dW, which
+// sums over the rows, xent_rescale_kernel brings such rows to the common power:
+// its terms are off by 2^-11 of themselves or 2^-39 of max|dloss|.
 #include <algorithm>
 
 #include "sgemm_tile16.hpp"
@@ -36,7 +45,7 @@ namespace {
 // In the workspace, per call.  `rows`: rows that are not ignored.
 struct XentHead {
     int rows;
-    float gmax;        // max |dloss| over them; 1 where that is 0 or infinite
+    float gmax;        // max |dloss| over them, FP16: the power of two above it; 1 where that is 0 or infinite
 };
 
 struct XentArgs {
@@ -62,7 +71,9 @@ struct XentArgs {
     // backward
     const float *lse_in, *dloss;
     long dloss_stride;
-    float *g, *lsec;                    // dloss / gmax and lse of the listed rows
+    bool f16;
+    float *g, *lsec;                    // of the listed rows: what P is multiplied by, its lse
+    float *back, *down;                 // what their dX is multiplied by, what P for dW
     char *dX, *dW, *P;
     long lddx, lddw, ldp;
     float *sum;                         // FP32 sum of dX over the pieces
@@ -132,6 +143,16 @@ __global__ void __launch_bounds__(256) xent_segments_kernel(XentArgs p) {
     }
 }
 
+// What P is stored times (P and dloss / gmax are at most 1).
+constexpr float p_scale(bool f16) { return f16 ? 0x1p15f : 1.f; }
+
+// The power of two above |d|.
+__device__ __forceinline__ float power_above(float d) {
+    int e;
+    (void)frexpf(d, &e);
+    return ldexpf(1.f, min(e, 127));
+}
+
 // Block b lists the rows b * kCompactRows ...: it counts the rows before
 // them itself (a pass over the targets, which stay in L2, so one launch does;
 // with many rows over the segments' counts and its own segment).  GRAD: also
@@ -159,6 +180,7 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
     }
     block_sums(na, nb, gm);
     if (!(gm > 0.f && gm < __builtin_inff())) gm = 1.f;
+    else if (GRAD && p.f16) gm = power_above(gm);
     if (blockIdx.x == 0 && tid == 0) *p.head = {na, gm};
     const bool copy = !(p.take_x && na == p.M);
     // each wave: every fourth row
@@ -185,8 +207,15 @@ __global__ void __launch_bounds__(256) xent_compact_kernel(XentArgs p) {
             p.label[at] = v >= 0 && v < p.N ? (int)v : -1;
             if (GRAD) {
                 const float d = p.dloss[row * p.dloss_stride];
+                float base = gm;
+                if (p.f16) {
+                    const float share = fabsf(d / gm);          // (above 1 next to an infinite one)
+                    if ((share < 0x1p-6f && d != 0.f) || (share > 1.f && share < __builtin_inff())) base = power_above(d);
+                    p.down[at] = base / gm;
+                }
                 // a target outside the vocabulary: NaN, as its loss is
-                p.g[at] = v >= 0 && v < p.N ? d / gm : __builtin_nanf("");
+                p.g[at] = v >= 0 && v < p.N ? d / base * p_scale(p.f16) : __builtin_nanf("");
+                p.back[at] = base / p_scale(p.f16);
                 p.lsec[at] = p.lse_in[row];
             }
         }
@@ -358,7 +387,27 @@ __device__ __forceinline__ void dw_tile(const XentArgs &p, int rows, char *lds, 
     f32x4 acc[T::MI][T::NB];
     accumulate16<T, F16, true, false>(q, m0, n0, lds, acc);
     store_tile<T, F16, true>(acc, m0, n0, p.n_count, p.K, p.dW + 2L * p.n_first * p.lddw, p.lddw,
-                             p.alpha * p.head->gmax, 0.f);
+                             p.alpha * (p.head->gmax / p_scale(F16)), 0.f);
+}
+
+// FP16, between the products of dX and of dW: the rows of P that stand for
+// dloss over a power of two of their own become shares of gmax like the others.
+// As a rule none do (8192 rows by 16128 columns: 5.5 us); where nearly all do
+// it is bound by reading and writing P (66 us, beside 800 for the product).
+__global__ void __launch_bounds__(256) xent_rescale_kernel(XentArgs p) {
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    const int rows = p.head->rows;
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float down = p.down[row];
+        if (down == 1.f) continue;
+        h8 *at = reinterpret_cast<h8 *>(p.P + 2 * row * p.ldp);
+        for (int c = blockIdx.y * 256 + threadIdx.x; 8 * c < p.n_count; c += gridDim.y * 256) {
+            h8 v = at[c];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (_Float16)((float)v[e] * down);
+            at[c] = v;
+        }
+    }
 }
 
 // STEP 0: stats_tile, 1: dlogits_tile, over the listed rows by the piece; 2:
@@ -425,7 +474,6 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
     f32x4 acc[T::MI][T::NB];
     accumulate16<T, F16, false, false>(q, m0, n0, lds, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const float scale = p.alpha * p.head->gmax;
     const bool place = last && gridDim.y == 1;
     float *sums = p.sum + (long)blockIdx.y * p.M * p.ldxc;
 #pragma unroll
@@ -434,6 +482,7 @@ __global__ void __launch_bounds__(T::NT) xent_dx_kernel(XentArgs p, int first, i
         if (row >= rows) continue;
         float *sum = sums + row * p.ldxc;                     // whole chunks of columns
         char *out = p.dX + 2 * p.map[row] * p.lddx;
+        const float scale = p.alpha * p.back[row];
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) {
             const int col = n0 + wave % T::WAVES_N * T::WN + nb * 16 + 4 * (lane >> 4);
@@ -452,7 +501,7 @@ template <bool F16>
 __global__ void __launch_bounds__(256) xent_dx_join_kernel(XentArgs p, int shares) {
     const int row = blockIdx.x;
     if (row >= p.head->rows) return;
-    const float scale = p.alpha * p.head->gmax;
+    const float scale = p.alpha * p.back[row];
     char *out = p.dX + 2 * p.map[row] * p.lddx;
     for (int col = 4 * threadIdx.x; col < p.K; col += 1024) {
         const f32x4 v = sum_shares(p.sum + row * p.ldxc + col, p.M * p.ldxc, shares);
@@ -512,6 +561,8 @@ long xent_layout(XentArgs &p, void *workspace, bool grad, char *&Wc) {
     } else {
         p.g = reinterpret_cast<float *>(l.take(4L * p.M));
         p.lsec = reinterpret_cast<float *>(l.take(4L * p.M));
+        p.back = reinterpret_cast<float *>(l.take(4L * p.M));
+        p.down = reinterpret_cast<float *>(l.take(4L * p.M));
         p.ldp = piece_columns(p.M, p.N);
         p.P = l.take(2L * p.M * p.ldp);
         const int shares = dx_shares(p.M, p.K, (int)std::min((long)p.N, p.ldp));
@@ -663,7 +714,7 @@ int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void
     char *Wc;
     if (!scratch_ok(xent_layout(p, nullptr, true, Wc), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     xent_layout(p, workspace, true, Wc);
-    const bool f16 = dtype == SGEMM_DTYPE_F16;
+    const bool f16 = p.f16 = dtype == SGEMM_DTYPE_F16;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = launch_compact<true>(p, s);
     if (e == hipSuccess && Wc != nullptr) {
@@ -680,6 +731,10 @@ int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha, const void
             e = M <= 32    ? launch_dx<Tile32>(p, shares, first, last, f16, s)
                 : M <= 128 ? launch_dx<Tile128>(p, shares, first, last, f16, s)
                            : launch_dx<Tile256>(p, shares, first, last, f16, s);
+        if (e == hipSuccess && M > 1 && dW != nullptr && f16 && dloss_stride != 0) {     // (else no row is apart)
+            const int across = std::min(M, 1024), along = std::min((p.n_count + 2047) / 2048, (1023 + across) / across);
+            e = launch_k(xent_rescale_kernel, dim3(across, along), dim3(256), s, p);
+        }
         if (e == hipSuccess && dW != nullptr) e = launch_mixed<2>(p, p.n_count, K, f16, s);
     }
     if (e == hipSuccess && M > 0 && dX != nullptr && shares > 1)

@@ -451,8 +451,11 @@ int sgemm_lowp_xent(int dtype, int M, int N, int K, float alpha,
  * is at dloss + i*dloss_stride (0: one value for all rows).  Ignored rows
  * give zeros in dX and nothing to dW; rows with a target outside 0 .. N-1
  * (and not ignored) give NaN.  The logits are formed again, a piece of the
- * vocabulary at a time, with P * dloss / max|dloss| of that piece in 16 bits
- * in the workspace.
+ * vocabulary at a time, with P * dloss of that piece in 16 bits in the
+ * workspace, scaled so that neither the size of dloss nor (FP16) its spread over
+ * the rows costs precision: a term of either sum is off by half a step of
+ * `dtype` relative to itself or, if that is more, (FP16) by 2^-34 of its row's
+ * |dloss| in dX and 2^-39 of max|dloss| in dW.
  */
 int sgemm_lowp_xent_grad(int dtype, int M, int N, int K, float alpha,
                          const void *X, int ldx, const void *W, int ldw,
