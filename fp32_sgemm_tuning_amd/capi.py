@@ -49,7 +49,8 @@ EXPORTS = ("sgemm", "sgemm_ex", "sgemm_select_variant", "sgemm_num_variants",
            "sgemm_lowp_strided_batched", "sgemm_workspace_bytes", "sgemm_release_workspaces",
            "sgemm_noalloc", "sgemm_lowp_grouped", "sgemm_lowp_grouped_workspace", "sgemm_lowp_grouped_wgrad",
            "sgemm_lowp_grouped_wgrad_workspace", "sgemm_lowp_xent", "sgemm_lowp_xent_grad",
-           "sgemm_lowp_xent_workspace", "sgemm_w4", "sgemm_w4_workspace", "sgemm_w4_quantize", "sgemm_w4_dequantize")
+           "sgemm_lowp_xent_workspace", "sgemm_w4", "sgemm_w4_workspace", "sgemm_w4_quantize", "sgemm_w4_dequantize",
+           "sgemm_w4_select_form")
 
 _lib = None
 
@@ -136,6 +137,7 @@ def open_library(path: str) -> ctypes.CDLL:
             ("sgemm_lowp_xent_workspace", [i, i, i, vp, i, vp, i, i], ll),
             ("sgemm_w4", [i, i, i, i, f, vp, i, vp, vp, vp, i, f, vp, i, i, vp, ll, vp], i),
             ("sgemm_w4_workspace", [i, i, vp, i], ll),
+            ("sgemm_w4_select_form", [i, i], i),
             ("sgemm_w4_quantize", [i, i, i, vp, i, i, vp, vp, vp, vp], i),
             ("sgemm_w4_dequantize", [i, i, i, vp, vp, vp, i, vp, i, vp], i)):
         getattr(lib, name).argtypes = args
@@ -271,6 +273,10 @@ def sgemm_w4(dtype, M, N, K, alpha, X, ldx, packed, scales, zeros, group, beta, 
 
 def sgemm_w4_workspace(M, K, X, ldx):
     return load().sgemm_w4_workspace(M, K, X, ldx)
+
+
+def sgemm_w4_select_form(M, N):
+    return load().sgemm_w4_select_form(M, N)
 
 
 def sgemm_w4_quantize(dtype, N, K, W, ldw, group, packed, scales, zeros, stream):

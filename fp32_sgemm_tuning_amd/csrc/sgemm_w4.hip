@@ -590,19 +590,30 @@ hipError_t launch_tile(const W4Args &p, int group, bool f16, bool out16, hipStre
 // at least); measured on N = 8192 for 128 rows 37.7 / 42.3 / 51.6 us, for 256
 // rows 73.9 / 43.9 / 51.7, for 512 rows - / 59.0 / 53.3, for 2048 rows
 // - / 220 / 165.
-hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
-    auto blocks = [&](int bm, int bn) { return (p.M + bm - 1L) / bm * ((p.N + bn - 1L) / bn); };
-    if (p.M <= 16)
-        return blocks(16, 64) >= 200   ? launch_rows<1, 4, 8>(p, group, f16, out16, s)
-               : blocks(16, 32) >= 200 ? launch_rows<1, 2, 8>(p, group, f16, out16, s)
-                                       : launch_rows<1, 1, 8>(p, group, f16, out16, s);
+// The forms as sgemm_w4_select_form() numbers them.
+enum Form { kRows16x16, kRows16x32, kRows16x64, kRows32x16, kRows32x32, kRows32x64, kTile64x128, kTile128x128 };
+
+Form select_form(int M, int N) {
+    auto blocks = [&](int bm, int bn) { return (M + bm - 1L) / bm * ((N + bn - 1L) / bn); };
+    if (M <= 16) return blocks(16, 64) >= 200 ? kRows16x64 : blocks(16, 32) >= 200 ? kRows16x32 : kRows16x16;
     const double rows = std::max(19.6, 19.6 * blocks(32, 64) / 256), t64 = std::max(41.0, 27.0 * blocks(64, 128) / 256),
                  t128 = std::max(51.0, 41.0 * blocks(128, 128) / 256);
-    if (p.M <= 64 || (rows <= t64 && rows <= t128))
-        return blocks(32, 64) >= 200   ? launch_rows<2, 4, 4>(p, group, f16, out16, s)
-               : blocks(32, 32) >= 200 ? launch_rows<2, 2, 8>(p, group, f16, out16, s)
-                                       : launch_rows<2, 1, 8>(p, group, f16, out16, s);
-    return t64 <= t128 ? launch_tile<4, 2, 1, 4>(p, group, f16, out16, s) : launch_tile<8, 2, 1, 4>(p, group, f16, out16, s);
+    if (M <= 64 || (rows <= t64 && rows <= t128))
+        return blocks(32, 64) >= 200 ? kRows32x64 : blocks(32, 32) >= 200 ? kRows32x32 : kRows32x16;
+    return t64 <= t128 ? kTile64x128 : kTile128x128;
+}
+
+hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
+    switch (select_form(p.M, p.N)) {
+        case kRows16x16: return launch_rows<1, 1, 8>(p, group, f16, out16, s);
+        case kRows16x32: return launch_rows<1, 2, 8>(p, group, f16, out16, s);
+        case kRows16x64: return launch_rows<1, 4, 8>(p, group, f16, out16, s);
+        case kRows32x16: return launch_rows<2, 1, 8>(p, group, f16, out16, s);
+        case kRows32x32: return launch_rows<2, 2, 8>(p, group, f16, out16, s);
+        case kRows32x64: return launch_rows<2, 4, 4>(p, group, f16, out16, s);
+        case kTile64x128: return launch_tile<4, 2, 1, 4>(p, group, f16, out16, s);
+        default: return launch_tile<8, 2, 1, 4>(p, group, f16, out16, s);
+    }
 }
 
 int check(int dtype, int N, int K, int group) {
@@ -664,6 +675,10 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx
     }
     const hipError_t e = launch_w4(p, group, f16, out16, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
+}
+
+int sgemm_w4_select_form(int M, int N) {
+    return M < 0 || N < 0 ? SGEMM_STATUS_INVALID_DIM : select_form(M, N);
 }
 
 int sgemm_w4_quantize(int dtype, int N, int K, const void *W, int ldw, int group, void *packed, void *scales,

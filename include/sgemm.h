@@ -491,6 +491,11 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha,
              void *workspace, long long workspace_bytes, void *stream);
 long long sgemm_w4_workspace(int M, int K, const void *X, int ldx);
 
+/* The launch form sgemm_w4() takes for M rows and a weight of N rows (no HIP
+ * call): 0, 1, 2 16 rows of X by 16, 32, 64 of W, 3, 4, 5 32 rows by 16, 32, 64,
+ * 6, 7 tiles through LDS of 64 x 128, 128 x 128; or SGEMM_STATUS_INVALID_DIM. */
+int sgemm_w4_select_form(int M, int N);
+
 /*
  * sgemm_w4_quantize: W [N,K] of `dtype` into the form above (zeros NULL:
  * without zero points).  s is rounded to `dtype` first and q chosen for the

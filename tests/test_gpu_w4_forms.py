@@ -1,0 +1,60 @@
+"""Every launch form of the products with 4-bit weights: groups, zero points,
+types, tails of K, strides, alpha and beta."""
+import pytest
+
+import fp32_sgemm_tuning_amd as lib
+from fp32_sgemm_tuning_amd import capi
+from gpu_util import torch_cuda
+from products_util import assert_equal, ints, padded
+from test_gpu_w4 import FORMS as KINDS, weight
+from w4_forms import SHAPES
+
+pytestmark = pytest.mark.gpu
+
+
+def values(torch, W):
+    """q - z and s of a W4Weight as 64-bit [N,K] arrays, on the device."""
+    K, dev = W.K, W.packed.device
+    k = torch.arange(K, device=dev)
+    word = k // 128 * 16 + 4 * (k % 32 // 8) + k % 128 // 32
+    bit = 4 * (k % 8 // 2) + 16 * (k % 2)
+    q = (W.packed.view(torch.int32)[:, word] >> bit) & 15
+    z = 8 if W.zeros is None else W.zeros[:, k // W.group].int()
+    return (q - z).double(), W.scales[:, k // W.group].double()
+
+
+def product(torch, X, W):
+    q, s = values(torch, W)
+    return X.double() @ (q * s).T.contiguous()
+
+
+@pytest.mark.parametrize("group,zeros,dtype", KINDS)
+@pytest.mark.parametrize("form,M,N", SHAPES)
+def test_exact(form, M, N, group, zeros, dtype):
+    """Integer X and scales 2^-2 .. 2: every sum of x * (16 + q), of x and of
+    x * (q - z) and of the scaled groups is a multiple of 1/4 below 2^22, so FP32
+    holds it.  K is whole chunks or fewer, ends inside a group, and is not a
+    multiple of 8 (then X is copied into padded rows)."""
+    torch = torch_cuda()
+    assert capi.sgemm_w4_select_form(M, N) == form
+    dtype = getattr(torch, dtype)
+    for K in (40, 384, 517, 1000, 2049):
+        W = weight(torch, N, K, group, zeros, dtype, seed=N + K, exact=True)
+        X = ints(torch, (M, K), -3, 3, dtype, 5)
+        ref = product(torch, X, W)
+        assert_equal(torch, lib.sgemm_w4(X, W), ref, f"K {K}")
+        assert_equal(torch, lib.sgemm_w4(X, W, out_dtype=dtype), ref, f"K {K}, 16-bit result")
+
+
+@pytest.mark.parametrize("out", ["float32", "float16"])
+@pytest.mark.parametrize("form,M,N", SHAPES)
+def test_strides_alpha_beta(form, M, N, out):
+    torch = torch_cuda()
+    K = 200
+    W = weight(torch, N, K, 64, True, torch.float16, exact=True)
+    X, C0 = ints(torch, (M, K), -3, 3, torch.float16, 1), ints(torch, (M, N), -8, 8, getattr(torch, out), 2)
+    for pad, base in ((8, 8), (3, 1)):
+        Xv, Cv = padded(torch, X, pad, base), padded(torch, C0, 5, base, fill=99.0)
+        lib.sgemm_w4(Xv, W, C=Cv, alpha=0.5, beta=-2.0)
+        assert_equal(torch, Cv, 0.5 * product(torch, X, W) - 2 * C0.double())
+        assert (torch.as_strided(Cv, (M, N + 5), (N + 5, 1))[:, N:] == 99.0).all()
