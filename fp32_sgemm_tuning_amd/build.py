@@ -46,8 +46,8 @@ UNITS = [
 ]
 SOURCES = [os.path.join(CSRC, u) for u, _ in UNITS]
 # units rebuilt with the LDS poison for the race-check library; the others,
-# which hold no kernel on the poisoned K loops, are linked as they are
-PLAIN_UNITS = ("sgemm.hip", "sgemm_w4.hip")
+# which hold no kernel whose LDS stages are poisoned, are linked as they are
+PLAIN_UNITS = ("sgemm.hip",)
 POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u not in PLAIN_UNITS]
 DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp", "sgemm_lowp.hpp",
                                                      "sgemm_tile16.hpp")] + \

@@ -265,6 +265,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
             dma16_lowp(corner + 2L * c * kChunk, range, lds0 + st * STAGE + (i * NWAVES + wave) * 1024,
                        (int)(inside && row0 + 4 * NWAVES * i < rows ? off0 + i * step : kOutOfRange));
     };
+    // Race-check build (SGEMM_LDS_POISON, see sgemm_lean.hpp): NaN bits into
+    // what this lane's loads of stage `st` fill, landed before they are issued.
+    auto poison = [&](int st) {
+        if constexpr (SGEMM_LDS_POISON) {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                *reinterpret_cast<i32x4 *>(lds + st * STAGE + (i * NWAVES + wave) * 1024 + 16 * lane) = i32x4{-1, -1, -1, -1};
+            wait_lgkmcnt0();
+        }
+    };
     // lane (lr, lg) loads for its row of W; the scale of the four columns that
     // a lane's results stand in comes from the lanes that hold them
     const unsigned char *wtile = p.packed + (long)n0 * p.chunks * 64, *ztile = ZEROS ? p.zeros + (long)n0 * p.chunks * GPC : nullptr;
@@ -313,6 +323,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
         return *reinterpret_cast<const i32x4 *>(stage + frag + mi * 16 * 256 + 16 * ((4 * step + lg) ^ lr));
     };
     if (p.chunks > 0) {
+        poison(0);
         load_x(0, 0);
         load_w(0);
         static_for<0, NB>([&](auto bc) {
@@ -336,6 +347,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
             cz[b] = zp[b];
         }
         const int next = min(c + 1, p.chunks - 1);          // (the last chunk's weights once more, unused)
+        poison((c + 1) & 1);
         if (c + 1 < p.chunks) load_x(c + 1, (c + 1) & 1);
         load_w(next);
         __builtin_amdgcn_sched_barrier(0);

@@ -1,5 +1,5 @@
 """Every launch form of the products with 4-bit weights: groups, zero points,
-types, tails of K, strides, alpha and beta."""
+types, tails of K, strides, alpha and beta, and the race check."""
 import pytest
 
 import fp32_sgemm_tuning_amd as lib
@@ -58,3 +58,17 @@ def test_strides_alpha_beta(form, M, N, out):
         lib.sgemm_w4(Xv, W, C=Cv, alpha=0.5, beta=-2.0)
         assert_equal(torch, Cv, 0.5 * product(torch, X, W) - 2 * C0.double())
         assert (torch.as_strided(Cv, (M, N + 5), (N + 5, 1))[:, N:] == 99.0).all()
+
+
+def test_race_check_build(monkeypatch):
+    """The tiles' two stages of X poisoned between their last read and their
+    refill."""
+    torch = torch_cuda()
+    monkeypatch.setattr(capi, "_lib", capi.open_library(capi.POISON_LIB_PATH))
+    for form, M, N in SHAPES:
+        if form < 6:
+            continue
+        for group, zeros, dtype in KINDS:
+            W = weight(torch, N, 1000, group, zeros, getattr(torch, dtype), seed=N, exact=True)
+            X = ints(torch, (M, 1000), -3, 3, getattr(torch, dtype), 5)
+            assert_equal(torch, lib.sgemm_w4(X, W), product(torch, X, W), f"{M} x {N}, groups of {group}")
