@@ -19,7 +19,10 @@
 // one with a matrix of ones gives the sum of x, and per group
 //     sum x * (q - z) * s = s * (sum x * (16 + q) - (16 + z) * sum x)
 // in FP32, so the weights are never rounded and the scale costs one
-// multiply-add per output and group.
+// multiply-add per output and group.  With an infinity in X, or BF16 values
+// above 2^128 / 31, the two sums may pass FP32's range where their difference
+// does not; what comes out is then infinite or NaN, and such an output is
+// formed again from q - z.
 #include <algorithm>
 
 #include "sgemm_tile16.hpp"
@@ -46,6 +49,25 @@ __device__ __forceinline__ int q_pair(unsigned w) {
     constexpr int to = (F16 ? 6 : 3) - 4 * I;              // shift left
     const unsigned v = to >= 0 ? w << (to >= 0 ? to : 0) : w >> (to < 0 ? -to : 0);
     return (int)((v & (F16 ? 0x03C003C0u : 0x00780078u)) | (F16 ? 0x4C004C00u : 0x41804180u));
+}
+
+// sum x * (q - z) * s for one output, a multiplication at a time.
+template <int GROUP, bool ZEROS, bool F16>
+__device__ __forceinline__ float w4_output(const W4Args &p, int row, int col) {
+    const unsigned short *x = reinterpret_cast<const unsigned short *>(p.X) + row * p.ldx;
+    const unsigned *words = reinterpret_cast<const unsigned *>(p.packed + (long)col * p.chunks * 64);
+    const long first = (long)col * p.chunks * (kChunk / GROUP);
+    float total = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < p.K; k0 += 8) {
+        const unsigned w = words[k0 / kChunk * 16 + k0 % 32 / 8 * 4 + k0 % kChunk / 32];
+        const float z = ZEROS ? (float)p.zeros[first + k0 / GROUP] : 8.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += widen16<F16>(x[k0 + e]) * ((float)(w >> (4 * (e >> 1) + 16 * (e & 1)) & 15) - z);
+        total += sum * widen16<F16>(p.scales[first + k0 / GROUP]);
+    }
+    return total;
 }
 
 // Few rows of X: MB blocks of 16 of them by NB blocks of 16 rows of W per
@@ -183,6 +205,7 @@ __global__ void __launch_bounds__(64 * NW) w4_rows_kernel(W4Args p) {
         for (int r = 0; r < 4; ++r) {
             const int row = m0 + 16 * (b / NB) + 4 * (l >> 4) + r;
             if (row >= p.M) continue;
+            if (!(fabsf(v[r]) < __builtin_inff())) v[r] = w4_output<GROUP, ZEROS, F16>(p, row, col);
             float o = p.alpha * v[r];
             if constexpr (OUT16) {
                 unsigned short *dst = reinterpret_cast<unsigned short *>(p.C) + row * p.ldc + col;

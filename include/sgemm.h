@@ -470,7 +470,9 @@ long long sgemm_lowp_xent_workspace(int M, int N, int K, const void *X, int ldx,
  * sgemm_w4: C = alpha * X * Wq^T + beta * C, X [M,K] of `dtype`, C [M,N] of
  * `dtype` or SGEMM_DTYPE_F32 (dtype_c), and a weight of 4-bit values,
  *   Wq[n][k] = (q[n][k] - z[n][k / group]) * s[n][k / group],
- * group 32, 64 or 128, the products and sums of unrounded weights in FP32.
+ * group 32, 64 or 128, the products and sums of unrounded weights in FP32: an
+ * infinity or NaN in X gives what this formula does, whatever M, as long as no
+ * sum of x * (q - z) over some k of one group passes FP32's range.
  * With Kp = K rounded up to a multiple of 128:
  *   packed  N rows of Kp / 2 bytes, 16-byte aligned, 64 bytes per 128 k: the
  *           32-bit word 4*j + s of a chunk (j, s = 0 .. 3) holds

@@ -1,5 +1,5 @@
 """Every launch form of the products with 4-bit weights: groups, zero points,
-types, tails of K, strides, alpha and beta, and the race check."""
+types, tails of K, strides, alpha and beta, infinities, and the race check."""
 import pytest
 
 import fp32_sgemm_tuning_amd as lib
@@ -58,6 +58,36 @@ def test_strides_alpha_beta(form, M, N, out):
         lib.sgemm_w4(Xv, W, C=Cv, alpha=0.5, beta=-2.0)
         assert_equal(torch, Cv, 0.5 * product(torch, X, W) - 2 * C0.double())
         assert (torch.as_strided(Cv, (M, N + 5), (N + 5, 1))[:, N:] == 99.0).all()
+
+
+@pytest.mark.parametrize("group,zeros,dtype", KINDS)
+@pytest.mark.parametrize("form,M,N", SHAPES)
+def test_infinities_and_values_near_the_end(form, M, N, group, zeros, dtype):
+    """An infinity gives what the formula gives (infinities of q - z's sign, NaN
+    where q is z), a NaN a row of NaN, and BF16 values whose product with 16 + q
+    passes FP32's range the number they stand for; other rows keep theirs."""
+    torch = torch_cuda()
+    dtype = getattr(torch, dtype)
+    K = 520
+    W = weight(torch, N, K, group, zeros, dtype, seed=N, exact=True)
+    X = ints(torch, (M, K), -3, 3, dtype, 5)
+    special = [(7, float("inf")), (K - 1, -float("inf")), (130, float("nan")), (300, float("inf"))]
+    if dtype == torch.bfloat16:
+        special += [(11, 2.0 ** 124), (400, -(2.0 ** 124))]
+    for i, (k, v) in enumerate(special):
+        if M <= len(special):                             # one of them in the last row, as seen from the seed
+            i = M - 1
+            k, v = special[(N + group) % len(special)]
+        row = i * ((M - 1) // len(special) or 1)
+        if abs(v) < float("inf"):
+            X[row] = 0                                    # (one term: exact)
+        X[row, k] = v
+    ref = product(torch, X, W)
+    got = lib.sgemm_w4(X, W)
+    assert not ref.isfinite().all() or dtype == torch.bfloat16
+    assert torch.equal(got.isnan(), ref.isnan())
+    live = ~ref.isnan()
+    assert_equal(torch, got[live], ref[live])
 
 
 def test_race_check_build(monkeypatch):
