@@ -43,6 +43,16 @@ struct W4Args {
     float alpha, beta;
 };
 
+// The scales of a row's chunk (in one register), those of groups wholly behind
+// K taken as 0: they belong to no weight, and a NaN there must not meet the
+// zeros that X counts as behind K.  `last`: of the row.
+template <int GROUP, class S>
+__device__ __forceinline__ S used_scales(S scales, bool last, int K) {
+    constexpr int GPC = kChunk / GROUP;
+    const int groups = ((K - 1) % kChunk) / GROUP + 1;     // of the last chunk that hold a k (K > 0)
+    return last && groups < GPC ? scales & (((S)1 << (16 * groups % (8 * sizeof(S)))) - 1) : scales;
+}
+
 // The two 16-bit values 16 + q of nibble i of each half of a word.
 template <bool F16, int I>
 __device__ __forceinline__ int q_pair(unsigned w) {
@@ -144,7 +154,8 @@ __global__ void __launch_bounds__(64 * NW) w4_rows_kernel(W4Args p) {
                 if (t == 0 || c0 + t < last)
                     w[t][b] = *reinterpret_cast<const i32x4 *>(wtile + ((first[b] + c0 + t) * 64 + 16 * lg));
             const unsigned at = first[b] + min(c0 + lg, last - 1);
-            if constexpr (GPC > 1) four_s[b] = *reinterpret_cast<const Scales *>(stile + at * GPC);
+            if constexpr (GPC > 1)
+                four_s[b] = used_scales<GROUP>(*reinterpret_cast<const Scales *>(stile + at * GPC), c0 + lg >= p.chunks - 1, p.K);
             else four_s[b] = stile[at];
             if constexpr (ZEROS && GPC == 4) four_z[b] = *reinterpret_cast<const unsigned *>(ztile + at * GPC);
             else if constexpr (ZEROS && GPC == 2) four_z[b] = *reinterpret_cast<const unsigned short *>(ztile + at * GPC);
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             cw[b] = w[b];
-            cs[b] = sc[b];
+            cs[b] = used_scales<GROUP>(sc[b], c == p.chunks - 1, p.K);     // (a chunk's first group is taken from sc: it holds a k)
             cz[b] = zp[b];
         }
         const int next = min(c + 1, p.chunks - 1);          // (the last chunk's weights once more, unused)

@@ -477,11 +477,11 @@ long long sgemm_lowp_xent_workspace(int M, int N, int K, const void *X, int ldx,
  *   packed  N rows of Kp / 2 bytes, 16-byte aligned, 64 bytes per 128 k: the
  *           32-bit word 4*j + s of a chunk (j, s = 0 .. 3) holds
  *           k = 32*s + 8*j .. + 7 of it, element 2i in bits 4i .. 4i+3 and
- *           element 2i+1 in bits 16+4i .. 16+4i+3; what it holds for k >= K
- *           is not used
+ *           element 2i+1 in bits 16+4i .. 16+4i+3
  *   scales  N rows of Kp / group values of `dtype`, 8-byte aligned
  *   zeros   N rows of Kp / group bytes 0 .. 15, 4-byte aligned, or NULL
  *           (every z is 8)
+ * What they hold for k >= K, or for a group of such k alone, is not used.
  * SGEMM_STATUS_UNSUPPORTED: one of them is not aligned so.  X whose rows are
  * not whole aligned 16-byte chunks is first copied into the workspace.  M up
  * to 2^24, K below 2^22 - 64.

@@ -90,6 +90,29 @@ def test_infinities_and_values_near_the_end(form, M, N, group, zeros, dtype):
     assert_equal(torch, got[live], ref[live])
 
 
+@pytest.mark.parametrize("group,zeros,dtype", [k for k in KINDS if k[0] < 128])
+@pytest.mark.parametrize("form,M,N", SHAPES)
+def test_what_lies_behind_K_is_not_used(form, M, N, group, zeros, dtype):
+    """The last chunk's values, scales and zero points behind K may hold
+    anything."""
+    torch = torch_cuda()
+    dtype = getattr(torch, dtype)
+    for K in (8, 129, 264, 351):
+        W = weight(torch, N, K, group, zeros, dtype, seed=K, exact=True)
+        X = ints(torch, (M, K), -3, 3, dtype, 5)
+        ref = product(torch, X, W)
+        used = (K + group - 1) // group
+        W.scales[:, used:] = float("nan")
+        if zeros:
+            W.zeros[:, used:] = 255
+        got = lib.sgemm_w4(X, W)
+        assert_equal(torch, got, ref, f"K {K}")
+        assert_equal(torch, lib.sgemm_w4_dequantize(W), (lambda q, s: q * s)(*values(torch, W)))
+        X[0, 0] = float("inf")
+        want, got = product(torch, X, W)[0], lib.sgemm_w4(X, W)[0]
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~want.isnan()].double(), want[~want.isnan()])
+
+
 def test_race_check_build(monkeypatch):
     """The tiles' two stages of X poisoned between their last read and their
     refill."""
