@@ -177,29 +177,32 @@ __global__ void __launch_bounds__(256) group_join_kernel(GroupArgs p, const floa
     store4<F16, OUT16>(p.C + (OUT16 ? 2L : 4L) * (g * p.strideC + (row - g * p.K) * p.ldc), col, p.N, p.beta, v * p.alpha);
 }
 
-// One 16-byte chunk of dst per thread and step, from rows of any alignment
-// (a 16-byte load needs none on this chip; the copy is bound by memory).
+// One 16-byte chunk of dst per thread and step, a row per workgroup and step,
+// from rows of any alignment (a 16-byte load needs none on this chip; the copy is
+// bound by memory).
 __global__ void __launch_bounds__(256) pad_rows_kernel(const unsigned short *src, long ld, long stride, int rows,
                                                        int cols, unsigned short *dst, int chunks) {
     typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-    const int r = blockIdx.x;
-    src += blockIdx.y * stride + r * ld;
-    dst += ((long)blockIdx.y * gridDim.x + r) * chunks * 8;
-    for (int q = threadIdx.x; q < chunks; q += 256) {
-        const int c = 8 * q;
-        u16x8 v;
-        if (c + 8 <= cols) {
-            __builtin_memcpy(&v, src + c, 16);
-        } else {
+    src += blockIdx.y * stride;
+    dst += (long)blockIdx.y * rows * chunks * 8;
+    for (long r = blockIdx.x; r < rows; r += gridDim.x) {
+        const unsigned short *from = src + r * ld;
+        for (int q = threadIdx.x; q < chunks; q += 256) {
+            const int c = 8 * q;
+            u16x8 v;
+            if (c + 8 <= cols) {
+                __builtin_memcpy(&v, from + c, 16);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? src[c + e] : (unsigned short)0;
+                for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? from[c + e] : (unsigned short)0;
+            }
+            reinterpret_cast<u16x8 *>(dst)[r * chunks + q] = v;
         }
-        reinterpret_cast<u16x8 *>(dst)[q] = v;
     }
 }
 
 hipError_t pad_rows(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, hipStream_t s) {
-    return launch_k(pad_rows_kernel, dim3((unsigned)rows, (unsigned)copies), dim3(256), s,
+    return launch_k(pad_rows_kernel, dim3((unsigned)std::min(rows, 1 << 22), (unsigned)copies), dim3(256), s,
                     static_cast<const unsigned short *>(src), ld, stride, rows, cols, static_cast<unsigned short *>(dst),
                     (cols + 7) / 8);
 }
@@ -239,6 +242,18 @@ hipError_t launch_wgrad(const GroupArgs &p, int shares, bool f16, bool out16, hi
     const long tiles = (long)((p.K + T::BM - 1) / T::BM) * ((p.N + T::BN - 1) / T::BN);
     const dim3 grid((unsigned)(ceil_to(tiles, 8) * p.groups), (unsigned)shares);
     return GROUP_FORMS(group_k_kernel, T::NT, T COMMA, );
+}
+
+// Whether launch_rows() can cover M rows.
+bool rows_fit(int groups, int M, int N) {
+    GroupArgs p = {};
+    p.groups = groups;
+    p.M = M;
+    p.N = N;
+    const int rows = groups > 0 && M > 0 ? M / std::min(groups, M) : 0;
+    return rows <= 32    ? launch_fits(most_tiles(p, 32, 128), Tile32::NT)
+           : rows <= 128 ? launch_fits(most_tiles(p, 128, 128), Tile128::NT)
+                         : launch_fits(mixed_grid(most_tiles(p, 256, 256)), 512);
 }
 
 // By the rows of an average group: tiles of 32 rows are bound by the weights'
@@ -339,7 +354,7 @@ int sgemm_lowp_grouped(int dtype, int op_b, int groups, int M, int N, int K, flo
     if (groups < 0 || groups > kMaxGroups || M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
     if (lda < std::max(K, 1) || ldb < std::max(tb ? K : N, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
     if (stride_b < 0 || K > kMaxLd16 || N > kMaxLd16) return SGEMM_STATUS_INVALID_DIM;
-    if (((long)M + (long)std::min(groups, M) * 31) / 32 * ((N + 127) / 128) > 0x7fffffffL) return SGEMM_STATUS_INVALID_DIM;
+    if (!rows_fit(groups, M, N)) return SGEMM_STATUS_INVALID_DIM;
     if (groups == 0 || M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || offsets == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return SGEMM_STATUS_NULL_POINTER;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -386,7 +401,7 @@ int sgemm_lowp_grouped_wgrad(int dtype, int groups, int M, int N, int K, float a
     if (lda < std::max(K, 1) || ldd < std::max(N, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
     if (K > kMaxLd16 || N > kMaxLd16) return SGEMM_STATUS_INVALID_DIM;
     if (groups > 1 && K > 0 && N > 0 && stride_c < (K - 1LL) * ldc + N) return SGEMM_STATUS_INVALID_DIM;
-    if ((K + 127L) / 128 * ((N + 127) / 128) + 8 > 0x7fffffffL / std::max(groups, 1)) return SGEMM_STATUS_INVALID_DIM;
+    if (!launch_fits(ceil_to((K + 127L) / 128 * ((N + 127L) / 128), 8) * groups, TileWide::NT)) return SGEMM_STATUS_INVALID_DIM;
     if (groups == 0 || N == 0 || K == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || offsets == nullptr || (M > 0 && (A == nullptr || D == nullptr))) return SGEMM_STATUS_NULL_POINTER;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -205,6 +205,10 @@ inline long ceil_to(long n, long to) { return (n + to - 1) / to * to; }
 constexpr int kMaxLd16 = (1 << 22) - 64;
 static_assert(2L * (255L * kMaxLd16 + 64) <= kOutOfRange && 2L * (63L * kMaxLd16 + 256) <= kOutOfRange, "descriptor range");
 
+// Whether one launch can have that many workgroups of `threads` (HIP takes
+// fewer than 2^32 threads).
+inline bool launch_fits(long workgroups, int threads) { return workgroups <= 0xffffffffL / threads; }
+
 inline bool chunk_rows(const void *p, long ld, long cols) {     // rows of whole 16-byte chunks
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && cols % 8 == 0 && ld <= kMaxLd16;
 }

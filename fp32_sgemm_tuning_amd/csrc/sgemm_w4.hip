@@ -649,6 +649,16 @@ Form select_form(int M, int N) {
     return t64 <= t128 ? kTile64x128 : kTile128x128;
 }
 
+// Whether one launch can cover the outputs (the kernel for few rows, which has
+// tile rows in gridDim.y, is taken for up to 536 tiles or up to 64 rows).
+bool form_fits(int M, int N) {
+    switch (select_form(M, N)) {
+        case kTile64x128: return launch_fits((M + 63L) / 64 * ((N + 127L) / 128), 256);
+        case kTile128x128: return launch_fits((M + 127L) / 128 * ((N + 127L) / 128), 256);
+        default: return launch_fits((N + 63L) / 64, 512);
+    }
+}
+
 hipError_t launch_w4(const W4Args &p, int group, bool f16, bool out16, hipStream_t s) {
     switch (select_form(p.M, p.N)) {
         case kRows16x16: return launch_rows<1, 1, 8>(p, group, f16, out16, s);
@@ -699,7 +709,7 @@ int sgemm_w4(int dtype, int M, int N, int K, float alpha, const void *X, int ldx
     if (st != SGEMM_STATUS_OK) return st;
     if (dtype_c != dtype && dtype_c != SGEMM_DTYPE_F32) return SGEMM_STATUS_INVALID_DTYPE;
     if (M < 0 || M > kMaxRows || ldx < std::max(K, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
-    if ((M + 31L) / 32 * ((N + 63) / 64) > 0x7fffffffL) return SGEMM_STATUS_INVALID_DIM;
+    if (!form_fits(M, N)) return SGEMM_STATUS_INVALID_DIM;
     if (M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || (K > 0 && (X == nullptr || packed == nullptr || scales == nullptr)))
         return SGEMM_STATUS_NULL_POINTER;

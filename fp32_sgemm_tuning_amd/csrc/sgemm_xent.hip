@@ -575,8 +575,11 @@ int check(int dtype, int M, int N, int K, int ldx, int ldw) {
     if (dtype != SGEMM_DTYPE_BF16 && dtype != SGEMM_DTYPE_F16) return SGEMM_STATUS_INVALID_DTYPE;
     // (the vocabulary must hold a column for the sums to have a term)
     if (M < 0 || N < 1 || K < 0 || ldx < std::max(K, 1) || ldw < std::max(K, 1) || K > kMaxLd16 ||
-        M > (1 << 24) || N > (1 << 30) || (M + 31L) / 32 * ((N + 127L) / 128) > 0x7fffffffL)
+        M > (1 << 24) || N > (1 << 30))
         return SGEMM_STATUS_INVALID_DIM;
+    // (the tiles of the logits, of dW and of dX; few rows take smaller ones, of which there are fewer)
+    auto fits = [](long m, long n) { return launch_fits(mixed_grid((m + 255) / 256 * ((n + 255) / 256)), 512); };
+    if (!fits(M, N) || !fits(N, K) || !fits(M, K)) return SGEMM_STATUS_INVALID_DIM;
     return SGEMM_STATUS_OK;
 }
 

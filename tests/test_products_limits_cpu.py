@@ -4,6 +4,7 @@ HIP call."""
 import pytest
 
 from fp32_sgemm_tuning_amd import capi
+from test_products_cpu import DIM, GROUPED, NULL, W4, WGRAD, XENT
 from w4_forms import FORMS, SHAPES
 
 AL = 0x10000                        # a fake device address, aligned; never dereferenced
@@ -32,3 +33,25 @@ def test_forms_of_4bit_products():
     assert seen == set(FORMS)
     for bad in ((-1, 5), (5, -1)):
         assert capi.sgemm_w4_select_form(*bad) == capi.SGEMM_STATUS_INVALID_DIM
+
+
+@pytest.mark.parametrize("call,good,fits,over", [
+    # tiles of 256 x 256, and 256 workgroups for the last round: 2^23 of 512 threads are one too many
+    (capi.sgemm_lowp_grouped, {**GROUPED, "C": None}, dict(M=2 ** 31 - 1 - (1 << 18)), dict(M=2 ** 31 - 1)),
+    (capi.sgemm_lowp_grouped, {**GROUPED, "C": None}, dict(M=1 << 24, N=30000, ldb=30000, ldc=30000),
+     dict(M=1 << 24, N=40000, ldb=40000, ldc=40000)),
+    # small groups, tiles of 32 x 128
+    (capi.sgemm_lowp_grouped, {**GROUPED, "C": None}, dict(M=60000, groups=60000, N=30000, ldb=30000, ldc=30000),
+     dict(M=60000, groups=60000, N=40000, ldb=40000, ldc=40000)),
+    (capi.sgemm_lowp_grouped_wgrad, {**WGRAD, "C": None}, dict(groups=1000, K=1, N=1 << 20, ldd=1 << 20, ldc=1 << 20, stride_c=1 << 20),
+     dict(groups=1100, K=1, N=1 << 20, ldd=1 << 20, ldc=1 << 20, stride_c=1 << 20)),
+    (capi.sgemm_lowp_xent, {**XENT, "loss": None}, dict(M=1 << 24, N=32512), dict(M=1 << 24, N=32768)),
+    (capi.sgemm_lowp_xent, {**XENT, "loss": None}, dict(M=32, N=1 << 30), dict(M=1024, N=1 << 30)),
+    (capi.sgemm_w4, {**W4, "C": None}, dict(M=1, N=2 ** 29 - 64, ldc=1 << 30), dict(M=1, N=1 << 29, ldc=1 << 30)),
+    (capi.sgemm_w4, {**W4, "C": None}, dict(M=1 << 24, N=4096, ldc=1 << 30), dict(M=1 << 24, N=1 << 16, ldc=1 << 30)),
+], ids=lambda v: getattr(v, "__name__", ""))
+def test_results_of_more_tiles_than_a_launch_covers(call, good, fits, over):
+    """Refused before anything is enqueued; what fits goes on to the next
+    check (a missing result)."""
+    assert call(**{**good, **fits}) == NULL
+    assert call(**{**good, **over}) == DIM
