@@ -39,8 +39,12 @@ __device__ __forceinline__ int wave_sum(int v) {
     return v;
 }
 
-// The groups' tiles of BM rows one after another: how many there are, and the
-// group and the tile of number `id`.  Wave-uniform.
+// The groups' tiles of BM rows one after another: how many there are, at most
+// `most`, and the group and the tile of number `id`.  Wave-uniform.  (Groups that
+// overlap, in offsets that decrease, can have more tiles than the grid covers and
+// than 32 bits count: products with the number of tile columns are formed in 64.
+// The tile rows of 64 groups fit 32 bits: 64 * 2^31 / 256, and M is at most 65535
+// times 32 or 128 where BM is less.)
 template <int BM>
 struct TileList {
     const GroupArgs &p;
@@ -50,12 +54,12 @@ struct TileList {
         if (g < p.groups) group_rows(p.offsets, g, p.M, l, r);
         return (r + BM - 1) / BM;
     }
-    __device__ __forceinline__ TileList(const GroupArgs &args, int bn) : p(args), tiles_n((args.N + bn - 1) / bn) {
+    __device__ __forceinline__ TileList(const GroupArgs &args, int bn, int most) : p(args), tiles_n((args.N + bn - 1) / bn) {
         const int lane = threadIdx.x & 63;
         first = tile_rows(lane);
-        int sum = wave_sum(first);
-        for (int base = 64; base < p.groups; base += 64) sum += wave_sum(tile_rows(base + lane));
-        total = __builtin_amdgcn_readfirstlane(sum) * tiles_n;
+        long sum = __builtin_amdgcn_readfirstlane(wave_sum(first));
+        for (int base = 64; base < p.groups; base += 64) sum += __builtin_amdgcn_readfirstlane(wave_sum(tile_rows(base + lane)));
+        total = (int)min(sum * tiles_n, (long)most);
     }
     // (id < total)
     __device__ __forceinline__ void find(int id, int &g, int &lo, int &rows, int &tm, int &tn) const {
@@ -68,7 +72,7 @@ struct TileList {
                 const int below = __shfl_up(upto, d);
                 if (lane >= d) upto += below;
             }
-            const unsigned long past = __ballot(id < upto * tiles_n);
+            const unsigned long past = __ballot(id < (long)upto * tiles_n);
             if (past) {
                 const int at = __builtin_ctzl(past);
                 const int count = __builtin_amdgcn_readlane(mine, at);
@@ -97,7 +101,7 @@ __device__ __forceinline__ void group_tile(const GroupArgs &p, char *lds, int g,
 template <class T, bool F16, bool TB, bool OUT16>
 __global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const TileList<T::BM> list(p, T::BN);
+    const TileList<T::BM> list(p, T::BN, gridDim.x);
     if ((int)blockIdx.x >= list.total) return;
     int g = 0, lo = 0, rows = 0, tm = 0, tn = 0;
     list.find(xcd_run(blockIdx.x, list.total), g, lo, rows, tm, tn);
@@ -120,7 +124,7 @@ struct GroupBody {
 template <bool F16, bool TB, bool OUT16>
 __global__ void __launch_bounds__(512) group_mixed_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[Mixed<TB>::LDS];
-    const GroupBody<F16, TB, OUT16> body{TileList<256>(p, 256)};
+    const GroupBody<F16, TB, OUT16> body{TileList<256>(p, 256, gridDim.x - mixed_grid(0))};
     Mixed<TB>::run(body, lds, body.list.total);
 }
 

@@ -96,7 +96,7 @@ struct Mixed {
     }
 };
 
-inline long mixed_grid(long total) { return total + 256; }   // (whole rounds, and 256 at most behind them)
+constexpr long mixed_grid(long total) { return total + 256; }   // (whole rounds, and 256 at most behind them)
 
 // Corner of part `sub` of the 256 x 256 tile (tm, tn) for tile T.
 template <class T>

@@ -4,7 +4,7 @@ import pytest
 
 import fp32_sgemm_tuning_amd as lib
 from gpu_util import torch_cuda
-from products_util import assert_equal
+from products_util import assert_equal, padded
 from test_gpu_w4 import weight
 from test_gpu_w4_forms import product
 from test_gpu_xent import check, problem
@@ -47,3 +47,25 @@ def test_4bit_product_rows():
 def test_vocabulary_rows(T):
     torch = torch_cuda()
     check(torch, *problem(torch, T, ROWS, 3, torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,N", [(65536, 8192), (65536, 4097), (9_000_000, 40)])
+def test_offsets_that_decrease_stay_within_their_operands(T, N):
+    """Groups that all overlap have more tiles than 32 bits count; the call
+    leaves what lies around C alone, and the next call is right."""
+    torch = torch_cuda()
+    e, G, K = torch.bfloat16, 65535, 8
+    A = small(torch, (T, K), 1, e)
+    B = small(torch, (1, K, N), 2, e).expand(G, K, N)
+    C = padded(torch, torch.zeros(T, N, dtype=e, device="cuda"), 8, 8, fill=99.0)
+    off = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = T                                   # 0, T, 0, T, ...
+    lib.sgemm_grouped(A, B, off, C=C)
+    around = torch.as_strided(C, (T, N + 8), (N + 8, 1))
+    assert (around[:, N:] == 99.0).all()
+    assert (torch.as_strided(C, (8,), (1,), C.storage_offset() - 8) == 99.0).all()
+    off.fill_(T)
+    off[:2] = torch.tensor([0, T // 2], dtype=torch.int32)
+    lib.sgemm_grouped(A, B, off, C=C)
+    ref = A.float() @ B[0].float()                  # (exact: integers)
+    assert torch.equal(C, ref.to(e)) and (around[:, N:] == 99.0).all()
