@@ -1657,11 +1657,16 @@ const char *sgemm_strerror(int status) {
         case SGEMM_STATUS_NULL_POINTER: return "NULL pointer with a non-empty extent";
         case SGEMM_STATUS_HIP_ERROR: return "HIP runtime error";
         case SGEMM_STATUS_INVALID_VARIANT: return "unknown kernel variant";
-        case SGEMM_STATUS_UNSUPPORTED: return "variant needs 16-byte aligned pointers and leading dimensions";
+        case SGEMM_STATUS_UNSUPPORTED:
+            return "variant needs 16-byte aligned pointers and leading dimensions; 4-bit weights need packed 16-byte, "
+                   "scales 8-byte and zeros 4-byte aligned";
         case SGEMM_STATUS_INVALID_OP: return "operation code is neither SGEMM_OP_N nor SGEMM_OP_T";
-        case SGEMM_STATUS_INVALID_DTYPE: return "element type not taken here";
+        case SGEMM_STATUS_INVALID_DTYPE:
+            return "input type is neither SGEMM_DTYPE_BF16 nor SGEMM_DTYPE_F16, or the result's neither the inputs' nor "
+                   "SGEMM_DTYPE_F32";
         case SGEMM_STATUS_SCRATCH_TOO_SMALL:
-            return "scratch or workspace missing, unaligned or smaller than the call needs";
+            return "sgemm_noalloc: the split of K needs more scratch than SGEMM_NOALLOC_SCRATCH_BYTES; other calls: the "
+                   "workspace is missing, not 16-byte aligned or too small";
         default: return "unknown status";
     }
 }

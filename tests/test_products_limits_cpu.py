@@ -55,3 +55,13 @@ def test_results_of_more_tiles_than_a_launch_covers(call, good, fits, over):
     check (a missing result)."""
     assert call(**{**good, **fits}) == NULL
     assert call(**{**good, **over}) == DIM
+
+
+@pytest.mark.parametrize("status,names", [
+    (capi.SGEMM_STATUS_UNSUPPORTED, ["variant", "16-byte aligned pointers and leading dimensions", "packed 16-byte", "scales 8-byte", "zeros 4-byte"]),
+    (capi.SGEMM_STATUS_INVALID_DTYPE, ["SGEMM_DTYPE_BF16", "SGEMM_DTYPE_F16", "SGEMM_DTYPE_F32"]),
+    (capi.SGEMM_STATUS_SCRATCH_TOO_SMALL, ["sgemm_noalloc", "SGEMM_NOALLOC_SCRATCH_BYTES", "workspace", "16-byte aligned"])])
+def test_error_texts_name_what_is_wrong(status, names):
+    """A status that several calls share says for each what it stands for."""
+    text = capi.sgemm_strerror(status)
+    assert all(n in text for n in names), text
