@@ -232,6 +232,13 @@ def _codes():
     return _CODES
 
 
+_INT = 2 ** 31 - 1   # sizes and leading dimensions are C ints; ctypes would drop higher bits unseen
+
+
+def _too_large(name):
+    raise ValueError(f"{name}: sizes and row strides must be below 2^31")
+
+
 def _rows16(t, name):
     """(type code, rows, columns, leading dimension) of a 16-bit row-major matrix view."""
     code = _codes().get(t.dtype, 0)
@@ -244,7 +251,10 @@ def _rows16(t, name):
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
     # (a single row, or none, has no meaningful row stride)
-    return code, rows, cols, step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    ld = step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    if rows | cols | ld > _INT:
+        _too_large(name)
+    return code, rows, cols, ld
 
 
 def _same_type(a, a_name, b, b_name):
@@ -333,7 +343,10 @@ def _result(C, shape, out_dtype, operand):
         dtype = out_dtype or torch.float32
         return operand.new_empty(shape, dtype=dtype), _CODES[dtype], max(cols, 1)
     step = C.stride(-2)
-    return C, _CODES[C.dtype], step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    ld = step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    if ld > _INT:
+        _too_large("C")
+    return C, _CODES[C.dtype], ld
 
 
 def _offsets(offsets):
@@ -367,6 +380,8 @@ def sgemm_grouped(A, B, offsets, C=None, alpha=1.0, beta=0.0, trans_b=False, out
     if unit != 1 and cb > 1:
         raise ValueError("B must have unit column stride (row-major)")
     ldb = ldb if rb > 1 or ldb >= cb > 0 else max(cb, 1)
+    if held | rb | cb | ldb > _INT:
+        _too_large("B")
     K2, N = (cb, rb) if trans_b else (rb, cb)
     if K2 != K:
         raise ValueError(f"inner dimensions differ: A is {M}x{K}, op(B[g]) is {K2}x{N}")
@@ -471,6 +486,8 @@ def sgemm_xent_grad(X, W, target, lse, dloss, alpha=1.0, ignore_index=-100, need
         step = 0
     elif dloss.dim() == 1 and dloss.shape[0] == M:
         step = dloss.stride(0)
+        if step > _INT:
+            _too_large("dloss")
     else:
         raise ValueError(f"dloss has shape {tuple(dloss.shape)}, expected {(M,)} or one value")
     device = _one_device(X, ("W", W), ("target", target), ("lse", lse), ("dloss", dloss))
@@ -517,6 +534,8 @@ def _w4(W):
     if zeros is not None and zeros.dtype != torch.uint8:
         raise TypeError("zeros must be uint8")
     N, Kp = packed.shape[0], (K + 127) // 128 * 128
+    if N | K > _INT:
+        _too_large("weight")
     if packed.shape[1] != Kp // 2 or not packed.is_contiguous():
         raise ValueError(f"packed has shape {tuple(packed.shape)}, expected contiguous {(N, Kp // 2)}")
     for t, name in ((scales, "scales"), (zeros, "zeros")):

@@ -65,3 +65,34 @@ def test_error_texts_name_what_is_wrong(status, names):
     """A status that several calls share says for each what it stands for."""
     text = capi.sgemm_strerror(status)
     assert all(n in text for n in names), text
+
+
+def test_sizes_past_an_int_are_refused():
+    """ctypes keeps the low 32 bits of an int argument: a row stride of 2^32 + 64
+    would be read as 64."""
+    import torch
+
+    import fp32_sgemm_tuning_amd as lib
+    e = torch.bfloat16
+
+    def far(rows, cols, step, dtype=e):                 # (no memory behind it)
+        return torch.empty(0, dtype=dtype, device="meta").as_strided((rows, cols), (step, 1))
+
+    x, off = far(4, 64, 64), torch.empty(3, dtype=torch.int32, device="meta")
+    t, v = torch.empty(4, dtype=torch.int64, device="meta"), torch.empty(4, device="meta")
+    bad, tall = far(4, 64, 2 ** 32 + 64), far(2 ** 32 + 4, 64, 64)
+    big = torch.empty(0, dtype=e, device="meta").as_strided((2, 64, 8), (0, 2 ** 32 + 8, 1))
+    w4 = lib.W4Weight(torch.empty(2 ** 32 + 8, 64, dtype=torch.uint8, device="meta"),
+                      torch.empty(2 ** 32 + 8, 1, dtype=e, device="meta"), None, 64, 128)
+    calls = [lambda: lib.sgemm_grouped(bad, torch.empty(2, 64, 8, dtype=e, device="meta"), off),
+             lambda: lib.sgemm_grouped(tall, torch.empty(2, 64, 8, dtype=e, device="meta"), off),
+             lambda: lib.sgemm_grouped(x, big, off),
+             lambda: lib.sgemm_grouped_wgrad(x, bad, off), lambda: lib.sgemm_xent(x, bad, t),
+             lambda: lib.sgemm_xent(x, tall, t),
+             lambda: lib.sgemm_xent_grad(x, x, t, v, torch.empty(0, device="meta").as_strided((4,), (2 ** 32 + 1,))),
+             lambda: lib.sgemm_w4(x, w4), lambda: lib.sgemm_w4_dequantize(w4), lambda: lib.sgemm_w4_quantize(bad),
+             lambda: lib._result(far(4, 8, 2 ** 32 + 8, torch.float32), (4, 8), None, x)]
+    lib._codes()
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            call()
