@@ -1,11 +1,12 @@
 """Every launch form of the products with 4-bit weights: groups, zero points,
-types, tails of K, strides, alpha and beta, infinities, and the race check."""
+types, tails of K, strides, alpha and beta, infinities, rounding, and the race
+check."""
 import pytest
 
 import fp32_sgemm_tuning_amd as lib
 from fp32_sgemm_tuning_amd import capi
 from gpu_util import torch_cuda
-from products_util import assert_equal, ints, padded
+from products_util import assert_equal, assert_within, ints, normal, padded
 from test_gpu_w4 import FORMS as KINDS, weight
 from w4_forms import SHAPES
 
@@ -111,6 +112,23 @@ def test_what_lies_behind_K_is_not_used(form, M, N, group, zeros, dtype):
         X[0, 0] = float("inf")
         want, got = product(torch, X, W)[0], lib.sgemm_w4(X, W)[0]
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~want.isnan()].double(), want[~want.isnan()])
+
+
+@pytest.mark.parametrize("group,zeros,dtype", KINDS)
+@pytest.mark.parametrize("form,M,N", SHAPES)
+def test_inputs_of_one_sign(form, M, N, group, zeros, dtype):
+    """Sums of x * (16 + q) and 16 + z times the sum of x, which grow with K where
+    X has one sign, cancel: their FP32 steps remain (31 times |x| each, `group`
+    sums; then one per scaled group).  The tiles sum x * (q - z), 15 times |x| at
+    most."""
+    torch = torch_cuda()
+    dtype = getattr(torch, dtype)
+    K = 1096
+    W = weight(torch, N, K, group, zeros, dtype, seed=N)
+    X = normal(torch, (M, K), dtype, 6).abs()
+    q, s = values(torch, W)
+    tol = (15 if form >= 6 else 62) * (group + K / group + 4) * 2.0 ** -23 * (X.double() @ s.T.contiguous())
+    assert_within(torch, lib.sgemm_w4(X, W), X.double() @ (q * s).T.contiguous(), tol)
 
 
 def test_race_check_build(monkeypatch):
