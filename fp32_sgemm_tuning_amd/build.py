@@ -3,8 +3,8 @@ twin libsgemm_poison.so.
 
     python -m fp32_sgemm_tuning_amd.build [--isa]
 
-libsgemm_poison.so is the same library with the lean FP32 and the 16-bit
-kernel units compiled with SGEMM_LDS_POISON=1: every LDS stage is filled
+libsgemm_poison.so is the same library with the lean FP32, the 16-bit and the
+4-bit kernel units compiled with SGEMM_LDS_POISON=1: every LDS stage is filled
 with NaN bits as soon as its last reader has passed its barrier, so a
 missing barrier gives a wrong result (tests only; the units without such
 kernels are the normal build's).

@@ -66,10 +66,11 @@ __device__ __forceinline__ void raster(int id, int tiles_m, int tiles_n, int &tm
 // workgroup each: whole rounds run on Tile256, and a last round that fills at
 // most half of the chip is cut finer, in two (TileWide, or with B transposed
 // TileTall) or, below a quarter, in four, so that its tiles take 0.57 or 0.39
-// of a round instead of a whole one.  16384 rows in 16 groups, BF16: 4096
+// of a round instead of a whole one.  16384 rows in 16 even groups, BF16: 4096
 // columns by 2048 k 282 us on Tile256 alone, 288 on TileWide alone, 259 so; B
-// transposed, 2048 by 4096, 295, 280 (TileTall) and 250; but 3001 rows in 5
-// groups by 5000 by 2048, just over one round, 89, 63 and 72.
+// transposed, 2048 by 4096, 295, 280 (TileTall) and 250 (uneven groups, as a
+// router fills them, take 297 and 300: more partly filled tiles); but 3001 rows in
+// 5 groups by 5000 by 2048, just over one round, 89, 63 and 72.
 // body.tile<T>(lds, id, sub) does part `sub` of tile number `id`; the number of
 // tiles need only be known here.  Launched with mixed_grid(largest total)
 // workgroups of 512 threads.

@@ -61,7 +61,8 @@ __device__ __forceinline__ int q_pair(unsigned w) {
     return (int)((v & (F16 ? 0x03C003C0u : 0x00780078u)) | (F16 ? 0x4C004C00u : 0x41804180u));
 }
 
-// sum x * (q - z) * s for one output, a multiplication at a time.
+// sum x * (q - z) * s for one output, a multiplication at a time (for all
+// outputs of 64 rows of NaN by 8192 x 4096 1.05 ms in place of 19 us).
 template <int GROUP, bool ZEROS, bool F16>
 __device__ __forceinline__ float w4_output(const W4Args &p, int row, int col) {
     const unsigned short *x = reinterpret_cast<const unsigned short *>(p.X) + row * p.ldx;
@@ -258,8 +259,8 @@ __device__ __forceinline__ i32x4 centred(unsigned w, unsigned zs) {
 
 // Many rows of X: a workgroup of WM x WN waves takes 16*MI*WM rows of X by
 // 16*NB*WN rows of W.  X comes through LDS (direct loads of one 128-k chunk,
-// two stages, rows of 256 bytes, 16-byte chunk c of row m at c ^ (m % 16): free
-// of bank conflicts); the weights go from memory straight into the registers
+// two stages, rows of 256 bytes, 16-byte chunk c of row m at c ^ (m % 16): no
+// bank conflicts counted); the weights go from memory straight into the registers
 // of the one wave that multiplies them, so each is unpacked once per tile and
 // only X loads the LDS.  q - z is exact in 16 bits; two k steps of a group
 // (one for groups of 32) are summed by the matrix instructions and then added
@@ -267,9 +268,11 @@ __device__ __forceinline__ i32x4 centred(unsigned w, unsigned zs) {
 // unpacking take about as many cycles as the matrix instructions, so every
 // matrix instruction is followed by its share of them: left to itself the
 // compiler gathers each kind, and the same tile took a ninth longer.  2048 x
-// 8192 x 4096, groups of 64 with zero points, FP16: 165 us, 833 TFLOP/s; two
-// workgroups of four waves share a compute unit (one of eight, in step at every
-// barrier, takes 170 us).  The product is formed transposed, as in
+// 8192 x 4096, groups of 64 with zero points, FP16: 169 us in a row of calls (813
+// TFLOP/s; 183 to 190 us under a kernel trace, matrix instructions 34% of the
+// time under counters); two workgroups of four waves share a compute unit (one
+// of eight, in step at every barrier, took 170 us where these took 165).  The
+// product is formed transposed, as in
 // sgemm_lowp.hpp: lane l holds row l%16 and columns 4*(l/16) .. +3.
 template <int MI, int NB, int WM, int WN, int GROUP, bool ZEROS, bool F16, bool OUT16>
 __global__ void __launch_bounds__(64 * WM * WN, 2) w4_tile_kernel(W4Args p) {
@@ -635,7 +638,8 @@ hipError_t launch_tile(const W4Args &p, int group, bool f16, bool out16, hipStre
 // kernel 19.6 us, 64 x 128 tiles 27 us (41 at least), 128 x 128 tiles 41 us (51
 // at least); measured on N = 8192 for 128 rows 37.7 / 42.3 / 51.6 us, for 256
 // rows 73.9 / 43.9 / 51.7, for 512 rows - / 59.0 / 53.3, for 2048 rows
-// - / 220 / 165.
+// - / 220 / 165 (groups of 64 with zero points; groups of 128 take 36 us for 128
+// rows, groups of 32 with zero points 45).
 // The forms as sgemm_w4_select_form() numbers them.
 enum Form { kRows16x16, kRows16x32, kRows16x64, kRows32x16, kRows32x32, kRows32x64, kTile64x128, kTile128x128 };
 

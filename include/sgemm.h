@@ -386,9 +386,9 @@ int sgemm_lowp_strided_batched(int dtype, int op_a, int op_b, int M, int N, int 
  * SGEMM_STATUS_SCRATCH_TOO_SMALL: the workspace is missing, unaligned or too
  * small.  SGEMM_STATUS_INVALID_DIM also where a result has more tiles than one
  * launch covers (2^32 threads): 8.3 million of 256 x 256 outputs in the grouped
- * products and the logits, 8.3 million of 128 x 128 in the weight gradient, 16.7
- * million of 64 x 128 in the product with 4-bit weights, whose weight may have up
- * to 2^29 - 64 rows.
+ * products (for small groups 16.7 million of 128 x 128 or 32 x 128) and the logits,
+ * 8.3 million of 128 x 128 in the weight gradient, 16.7 million of 64 x 128 in the
+ * product with 4-bit weights, whose weight may have up to 2^29 - 64 rows.
  *
  * sgemm_lowp_grouped: rows offsets[g] .. offsets[g+1] - 1 of A [M,K] and of
  * C [M,N] belong to group g, whose matrix is op(B) with B at
