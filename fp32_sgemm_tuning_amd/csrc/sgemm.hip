@@ -24,7 +24,7 @@
 #include "sgemm.h"
 #include "sgemm_kernels.hpp"
 
-#define SGEMM_LIB_VERSION 2
+#define SGEMM_LIB_VERSION 3
 
 namespace sgemm_mi355x {
 // Lean direct-to-LDS kernels (sgemm_lean.hip, built with MFMA results in
