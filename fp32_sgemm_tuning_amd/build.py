@@ -50,7 +50,7 @@ SOURCES = [os.path.join(CSRC, u) for u, _ in UNITS]
 PLAIN_UNITS = ("sgemm.hip",)
 POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u not in PLAIN_UNITS]
 DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp", "sgemm_lowp.hpp",
-                                                     "sgemm_tile16.hpp")] + \
+                                                     "sgemm_tile16.hpp", "sgemm_rows.hpp")] + \
     [os.path.join(INCLUDE, "sgemm.h")]
 
 ARCH = "gfx950"

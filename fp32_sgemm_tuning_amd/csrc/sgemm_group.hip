@@ -14,7 +14,7 @@
 // past the last tile end at once.
 #include <algorithm>
 
-#include "sgemm_tile16.hpp"
+#include "sgemm_rows.hpp"
 
 namespace sgemm_mi355x {
 
@@ -25,68 +25,7 @@ struct GroupArgs {
     const int *offsets;
     int groups, M, N, K;                    // M: rows of A
     float alpha, beta;
-};
-
-// Rows of group g, clamped to 0 .. M whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const int *offsets, int g, int M, int &lo, int &rows) {
-    lo = min(max(offsets[g], 0), M);
-    rows = min(max(offsets[g + 1], lo), M) - lo;
-}
-
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
-// The groups' tiles of BM rows one after another: how many there are, at most
-// `most`, and the group and the tile of number `id`.  Wave-uniform.  (Groups that
-// overlap, in offsets that decrease, can have more tiles than the grid covers and
-// than 32 bits count: products with the number of tile columns are formed in 64.
-// The tile rows of 64 groups fit 32 bits: 64 * 2^31 / 256, and M is at most 65535
-// times 32 or 128 where BM is less.)
-template <int BM>
-struct TileList {
-    const GroupArgs &p;
-    int tiles_n, first, total;                  // first: tile rows of group `lane`
-    __device__ __forceinline__ int tile_rows(int g) const {
-        int l = 0, r = 0;
-        if (g < p.groups) group_rows(p.offsets, g, p.M, l, r);
-        return (r + BM - 1) / BM;
-    }
-    __device__ __forceinline__ TileList(const GroupArgs &args, int bn, int most) : p(args), tiles_n((args.N + bn - 1) / bn) {
-        const int lane = threadIdx.x & 63;
-        first = tile_rows(lane);
-        long sum = __builtin_amdgcn_readfirstlane(wave_sum(first));
-        for (int base = 64; base < p.groups; base += 64) sum += __builtin_amdgcn_readfirstlane(wave_sum(tile_rows(base + lane)));
-        total = (int)min(sum * tiles_n, (long)most);
-    }
-    // (id < total)
-    __device__ __forceinline__ void find(int id, int &g, int &lo, int &rows, int &tm, int &tn) const {
-        const int lane = threadIdx.x & 63;
-        for (int base = 0; base < p.groups; base += 64) {
-            const int mine = base ? tile_rows(base + lane) : first;
-            int upto = mine;                                    // tile rows up to this lane's group
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int below = __shfl_up(upto, d);
-                if (lane >= d) upto += below;
-            }
-            const unsigned long past = __ballot(id < (long)upto * tiles_n);
-            if (past) {
-                const int at = __builtin_ctzl(past);
-                const int count = __builtin_amdgcn_readlane(mine, at);
-                id -= (__builtin_amdgcn_readlane(upto, at) - count) * tiles_n;
-                group_rows(p.offsets, base + at, p.M, lo, rows);
-                g = __builtin_amdgcn_readfirstlane(base + at);
-                lo = __builtin_amdgcn_readfirstlane(lo);
-                rows = __builtin_amdgcn_readfirstlane(rows);
-                raster(id, count, tiles_n, tm, tn);
-                return;
-            }
-            id -= __builtin_amdgcn_readlane(upto, 63) * tiles_n;
-        }
-    }
+    __device__ __forceinline__ void rows_of(int g, int &lo, int &rows) const { group_rows(offsets, g, M, lo, rows); }
 };
 
 template <class T, bool F16, bool TB, bool OUT16>
@@ -101,7 +40,7 @@ __device__ __forceinline__ void group_tile(const GroupArgs &p, char *lds, int g,
 template <class T, bool F16, bool TB, bool OUT16>
 __global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-    const TileList<T::BM> list(p, T::BN, gridDim.x);
+    const TileList<T::BM, GroupArgs> list(p, T::BN, gridDim.x);
     if ((int)blockIdx.x >= list.total) return;
     int g = 0, lo = 0, rows = 0, tm = 0, tn = 0;
     list.find(xcd_run(blockIdx.x, list.total), g, lo, rows, tm, tn);
@@ -111,7 +50,7 @@ __global__ void __launch_bounds__(T::NT) group_rows_kernel(GroupArgs p) {
 // Tiles of 256 x 256 with a finer last round.
 template <bool F16, bool TB, bool OUT16>
 struct GroupBody {
-    const TileList<256> list;
+    const TileList<256, GroupArgs> list;
     template <class T>
     __device__ __forceinline__ void tile(char *lds, int id, int sub) const {
         int g = 0, lo = 0, rows = 0, tm = 0, tn = 0, m0, n0;
@@ -124,7 +63,7 @@ struct GroupBody {
 template <bool F16, bool TB, bool OUT16>
 __global__ void __launch_bounds__(512) group_mixed_kernel(GroupArgs p) {
     __shared__ __attribute__((aligned(16))) char lds[Mixed<TB>::LDS];
-    const GroupBody<F16, TB, OUT16> body{TileList<256>(p, 256, gridDim.x - mixed_grid(0))};
+    const GroupBody<F16, TB, OUT16> body{TileList<256, GroupArgs>(p, 256, gridDim.x - mixed_grid(0))};
     Mixed<TB>::run(body, lds, body.list.total);
 }
 
@@ -223,21 +162,15 @@ constexpr int kMaxGroups = 65535;   // launch grid extent of the padded copies
                   : launch_k(KERNEL<BEFORE false, AFTER false>, grid, dim3(NT), s, p)))
 #define COMMA ,
 
-// The most tiles of bm x bn that any split of the rows into groups can have.
-long most_tiles(const GroupArgs &p, int bm, int bn) {
-    const long groups = std::min(p.groups, p.M);
-    return (p.M + groups * (bm - 1)) / bm * ((p.N + bn - 1) / bn);
-}
-
 template <class T, bool TB>
 hipError_t launch_rows(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
-    const dim3 grid((unsigned)most_tiles(p, T::BM, T::BN));
+    const dim3 grid((unsigned)most_tiles(p.groups, p.M, p.N, T::BM, T::BN));
     return GROUP_FORMS(group_rows_kernel, T::NT, T COMMA, TB COMMA);
 }
 
 template <bool TB>
 hipError_t launch_mixed(const GroupArgs &p, bool f16, bool out16, hipStream_t s) {
-    const dim3 grid((unsigned)mixed_grid(most_tiles(p, 256, 256)));
+    const dim3 grid((unsigned)mixed_grid(most_tiles(p.groups, p.M, p.N, 256, 256)));
     return GROUP_FORMS(group_mixed_kernel, 512, , TB COMMA);
 }
 
@@ -250,14 +183,10 @@ hipError_t launch_wgrad(const GroupArgs &p, int shares, bool f16, bool out16, hi
 
 // Whether launch_rows() can cover M rows.
 bool rows_fit(int groups, int M, int N) {
-    GroupArgs p = {};
-    p.groups = groups;
-    p.M = M;
-    p.N = N;
     const int rows = groups > 0 && M > 0 ? M / std::min(groups, M) : 0;
-    return rows <= 32    ? launch_fits(most_tiles(p, 32, 128), Tile32::NT)
-           : rows <= 128 ? launch_fits(most_tiles(p, 128, 128), Tile128::NT)
-                         : launch_fits(mixed_grid(most_tiles(p, 256, 256)), 512);
+    return rows <= 32    ? launch_fits(most_tiles(groups, M, N, 32, 128), Tile32::NT)
+           : rows <= 128 ? launch_fits(most_tiles(groups, M, N, 128, 128), Tile128::NT)
+                         : launch_fits(mixed_grid(most_tiles(groups, M, N, 256, 256)), 512);
 }
 
 // By the rows of an average group: tiles of 32 rows are bound by the weights'

@@ -72,6 +72,35 @@ __device__ __forceinline__ f32x4 mfma_16x16x32(i32x4 a, i32x4 b, f32x4 c) {
                                                        c, 0, 0, 0);
 }
 
+// What the K loop multiplies: 16-bit elements, or (kMulI8) pairs of 8-bit integers,
+// which fill the same 16 bits; v_mfma_i32_16x16x64_i8 takes the 16 bytes that a
+// lane supplies as 16 k in place of 8, in as many cycles, and sums in 32-bit
+// integers.  Operands that both have k along their rows only.
+constexpr int kMulBf16 = 0, kMulF16 = 1, kMulI8 = 2;
+
+template <int KIND>
+struct Product {
+    using Acc = f32x4;
+    static __device__ __forceinline__ f32x4 mfma(i32x4 a, i32x4 b, f32x4 c) { return mfma_16x16x32<KIND == kMulF16>(a, b, c); }
+};
+template <>
+struct Product<kMulI8> {
+    using Acc = i32x4;
+    static __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    }
+};
+
+// The first `bytes` (1 .. 15) of a chunk, the others 0.
+__device__ __forceinline__ i32x4 first_bytes(i32x4 v, int bytes) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = bytes - 4 * i;
+        v[i] = n >= 4 ? v[i] : n <= 0 ? 0 : v[i] & ((1 << (8 * n)) - 1);
+    }
+    return v;
+}
+
 // Slot of 16-byte chunk c in row k of a [k][x] stage (B, or A stored
 // transposed): the 32-byte units of a row are XORed with (k % 4) +
 // 4 * ((k / 8) % 2).  A transposed read takes
@@ -130,12 +159,17 @@ __device__ __forceinline__ void wait_vm_lgkm0() {
 // m- or n-contiguous (B, or A^T) sits in the swizzled [k][x] layout and is
 // read with the transpose read.
 // P: M, N, K, lda, ldb and the operands A and B (16-bit elements behind them).
+// KIND kMulI8: two 8-bit integers to an element, M, K, lda and so on counted in
+// elements; K is whole chunks, and p.cut the bytes of the last one that count
+// (0: all of them): what A's rows hold behind those is taken as 0, so that what
+// B's hold there does not matter.
 // m0, n0: the tile's corner; lds: NSTAGE stages; S, y: the split and this
 // block's share (SPLIT); acc: the tile's accumulators, zeroed here.
-template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NSTAGE, bool PP, bool EDGE, bool F16, bool SPLIT,
+template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int NSTAGE, bool PP, bool EDGE, int KIND, bool SPLIT,
           bool TA, bool TB, class P>
 __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char *lds, int S, int y,
-                                                f32x4 (&acc)[BM / WAVES_M / 16][BN / WAVES_N / 16]) {
+                                                typename Product<KIND>::Acc (&acc)[BM / WAVES_M / 16][BN / WAVES_N / 16]) {
+    static_assert(KIND != kMulI8 || (EDGE && !TA && TB), "pairs of 8-bit integers lie along k");
     static_assert(BK == 32 || BK == 64, "K tile");
     static_assert(!PP || WAVES_M * WAVES_N == 8, "the alternating schedule runs 8 waves");
     using AL = ALayout<BK / 2>;                             // A stage layout (its unit is 4 bytes)
@@ -198,12 +232,14 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
 
     // K remainder: k in [K - kr, K), taken first; full tiles from k = 0, on
     // the operands' own alignment (as in the lean FP32 kernel)
-    const int kr = EDGE ? p.K % BK : 0;
+    int kr = EDGE ? p.K % BK : 0;
+    if constexpr (KIND == kMulI8)
+        if (p.cut && kr == 0) kr = BK;      // the cut chunk is one of the remainder's
     const int tail = kr != 0;
     const long kfull = (long)p.K - kr;
     // K tiles of this block: all of them, or this split's share; ntiles
     // counts this block's tiles, t_first is the first one's index
-    int t_first = 0, ntiles = p.K / BK + tail;
+    int t_first = 0, ntiles = (KIND == kMulI8 ? (int)(kfull / BK) : p.K / BK) + tail;
     if constexpr (SPLIT) {
         const int total = ntiles;
         t_first = (int)((long)total * y / S);
@@ -311,7 +347,7 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mi][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int nb = 0; nb < NB; ++nb) acc[mi][nb] = typename Product<KIND>::Acc{0, 0, 0, 0};
 
     // One k step: MFMA q = (slab q / NB, block q % NB) from fa and fb[BC].
     // After MFMA QB-1 (QB a multiple of NB; before MFMA 0 when QB is 0) the
@@ -333,7 +369,7 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
         }
         static_for<0, NM>([&](auto qc) {
             constexpr int q = decltype(qc)::value;
-            acc[q / NB][q % NB] = mfma_16x16x32<F16>(fb[BC][q % NB], fa[q / NB], acc[q / NB][q % NB]);
+            acc[q / NB][q % NB] = Product<KIND>::mfma(fb[BC][q % NB], fa[q / NB], acc[q / NB][q % NB]);
             if constexpr (q == QB - 1) {
                 __builtin_amdgcn_sched_barrier(0);
                 sync();
@@ -367,6 +403,22 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
 #pragma unroll
             for (int g = 0; g < L; ++g)
                 *reinterpret_cast<i32x4 *>(lds + (dst(st, g) - lds0) + 16 * lane) = i32x4{-1, -1, -1, -1};
+            wait_lgkmcnt0();
+        }
+    };
+    // The cut chunk of A, landed in stage 0 by this lane's own load, without the
+    // bytes that do not count.
+    auto cut_remainder = [&]() {
+        if constexpr (KIND == kMulI8) {
+            if (!remainder_first || !p.cut) return;
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                int x, c, k;
+                coords(true, ACH, i, x, c, k);
+                if (k + 8 != kr) continue;
+                i32x4 *chunk = reinterpret_cast<i32x4 *>(lds + (dst(0, i) - lds0) + 16 * lane);
+                *chunk = first_bytes(*chunk, p.cut);
+            }
             wait_lgkmcnt0();
         }
     };
@@ -424,6 +476,7 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
                 for (int g = 0; g < L; ++g) issue_one(decltype(sc)::value, decltype(sc)::value, g);
             });
             wait_vm_lgkm0<(NSTAGE - 2) * L>();
+            cut_remainder();
             __builtin_amdgcn_s_barrier();
             if (group) __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
@@ -455,7 +508,7 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
                 // compute phase
                 static_for<0, KS * NM>([&](auto qc) {
                     constexpr int ks = decltype(qc)::value / NM, q = decltype(qc)::value % NM;
-                    acc[q / NB][q % NB] = mfma_16x16x32<F16>(pb[ks][q % NB], pa[ks][q / NB], acc[q / NB][q % NB]);
+                    acc[q / NB][q % NB] = Product<KIND>::mfma(pb[ks][q % NB], pa[ks][q / NB], acc[q / NB][q % NB]);
                 });
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vm_lgkm0<(NSTAGE - 2) * L>();
@@ -484,6 +537,7 @@ __device__ __forceinline__ void lowp_accumulate(const P &p, int m0, int n0, char
             for (int g = 0; g < L; ++g) issue_one(decltype(sc)::value, decltype(sc)::value, g);
         });
         wait_vm_lgkm0<(NSTAGE - 1) * L>();
+        cut_remainder();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
