@@ -11,7 +11,9 @@ from typing import NamedTuple, Optional
 from . import capi
 
 __all__ = ["sgemm", "sgemm_op", "sgemm_lowp", "sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_xent", "sgemm_xent_grad",
-           "sgemm_w4", "sgemm_w4_quantize", "sgemm_w4_dequantize", "W4Weight", "SgemmError", "capi", "variant_names"]
+           "sgemm_w4", "sgemm_w4_quantize", "sgemm_w4_dequantize", "W4Weight", "sgemm_i8", "sgemm_i8_grouped",
+           "sgemm_i8_quantize", "sgemm_i8_dequantize", "I8Matrix", "sgemm_grouped_sort", "sgemm_grouped_combine",
+           "sgemm_grouped_combine_grad", "GroupOrder", "SgemmError", "capi", "variant_names"]
 
 
 class SgemmError(RuntimeError):
@@ -609,3 +611,344 @@ def sgemm_w4_dequantize(W, stream=None):
                                         _address(zeros), group, out.data_ptr(), max(K, 1), h))
         return out
     return _run(device, stream, call, packed, scales, zeros)
+
+
+# ---------------------------------------------------------------------------
+# Products of 8-bit integers; tokens sorted by expert and back.
+# ---------------------------------------------------------------------------
+class I8Matrix(NamedTuple):
+    """A matrix [rows,K] (or [G,rows,K], one per group) in 8-bit integers with
+    a scale for each row: values int8 with unit column stride, scales float32
+    [rows] (or [G,rows]).  Products take it as it is where its rows start at
+    multiples of 16 bytes, as sgemm_i8_quantize() lays them out, and copy it
+    otherwise."""
+    values: "torch.Tensor"              # noqa: F821
+    scales: "torch.Tensor"              # noqa: F821
+
+
+def _ld_of(t, name):
+    """Leading dimension of (each matrix of) t [..., rows, columns]."""
+    rows, cols = t.shape[-2:]
+    step, unit = t.stride()[-2:]
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    ld = step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    if rows | cols | ld > _INT:
+        _too_large(name)
+    return ld
+
+
+def _i8(Q, name, dims):
+    """(rows, K, leading dimension) of an I8Matrix of 2 or 3 dimensions, its parts checked."""
+    import torch
+    values, scales = Q
+    if values.dtype != torch.int8:
+        raise TypeError(f"{name}'s values must be int8, got {values.dtype}")
+    if scales.dtype != torch.float32:
+        raise TypeError(f"{name}'s scales must be float32, got {scales.dtype}")
+    if values.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D")
+    if scales.shape != values.shape[:-1]:
+        raise ValueError(f"{name}'s scales have shape {tuple(scales.shape)}, expected {tuple(values.shape[:-1])}")
+    if scales.shape[-1] > 1 and scales.stride(-1) != 1:
+        raise ValueError(f"{name}'s scales must be contiguous")
+    return values.shape[-2], values.shape[-1], _ld_of(values, name)
+
+
+def _float_code(dtype, name):
+    code = _codes().get(dtype)
+    if code is None:
+        raise TypeError(f"{name} is {dtype}, expected bfloat16, float16 or float32")
+    return code
+
+
+def _check_float_result(C, shape, out_dtype, beta):
+    """Before anything is allocated: beta, a given C's shape and type, the wanted type (any float)."""
+    if C is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs C")
+        if out_dtype is not None:
+            _float_code(out_dtype, "out_dtype")
+        return
+    if out_dtype is not None and C.dtype != out_dtype:
+        raise TypeError(f"C is {C.dtype} but out_dtype is {out_dtype}")
+    _float_code(C.dtype, "C")
+    if tuple(C.shape) != shape:
+        raise ValueError(f"C has shape {tuple(C.shape)}, expected {shape}")
+    if shape[-1] > 1 and C.stride(-1) != 1:
+        raise ValueError("C must have unit column stride (row-major)")
+
+
+def sgemm_i8(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
+    """C = alpha * X @ W.T + beta * C for X [M,K] and W [N,K] in 8-bit
+    integers (I8Matrix: a scale for each token and each output channel);
+    returns C.
+
+    Any M from a single token to a prompt, K up to 131071.  The sums are
+    exact; C [M,N] is float32 (the default), bfloat16 or float16."""
+    import torch
+    M, K, ldx = _i8(X, "X", 2)
+    N, K2, ldw = _i8(W, "W", 2)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W is {N}x{K2}")
+    x, sx = X
+    w, sw = W
+    device = _one_device(x, ("X's scales", sx), ("W", w), ("W's scales", sw), ("C", C))
+    _check_float_result(C, (M, N), out_dtype, beta)
+    operands = (x.data_ptr(), ldx, sx.data_ptr(), w.data_ptr(), ldw, sw.data_ptr())
+
+    def call(h):
+        out, code_c, ldc = _result(C, (M, N), out_dtype, x)
+        args = (M, N, K, float(alpha), *operands, float(beta), out.data_ptr(), ldc, code_c)
+        product = capi.load().sgemm_i8
+        status = product(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: product(*args, ws, size, h),
+                    lambda: capi.sgemm_i8_workspace(M, N, K, operands[0], ldx, operands[3], ldw), x)
+        return out
+    return _run(device, stream, call, x, sx, w, sw, C)
+
+
+def sgemm_i8_grouped(X, W, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
+    """C[r] = alpha * X[r] @ W[g].T + beta * C[r] for the rows r of each group
+    g, offsets[g] <= r < offsets[g+1], in 8-bit integers; returns C.
+
+    X [T,K] and W [G,N,K] are I8Matrix; offsets, empty groups and rows of no
+    group as in sgemm_grouped, the result as in sgemm_i8."""
+    import torch
+    groups = _offsets(offsets)
+    M, K, ldx = _i8(X, "X", 2)
+    N, K2, ldw = _i8(W, "W", 3)
+    x, sx = X
+    w, sw = W
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: X is {M}x{K}, W[g] is {N}x{K2}")
+    if w.shape[0] != groups:
+        raise ValueError(f"W holds {w.shape[0]} matrices, offsets bound {groups} groups")
+    device = _one_device(x, ("X's scales", sx), ("W", w), ("W's scales", sw), ("offsets", offsets), ("C", C))
+    _check_float_result(C, (M, N), out_dtype, beta)
+    sizes = (x.data_ptr(), ldx, sx.data_ptr(), w.data_ptr(), ldw, w.stride(0) if groups > 1 else 0, sw.data_ptr(),
+             sw.stride(0) if groups > 1 else 0)
+
+    def call(h):
+        out, code_c, ldc = _result(C, (M, N), out_dtype, x)
+        args = (groups, M, N, K, float(alpha), *sizes, offsets.data_ptr(), float(beta), out.data_ptr(), ldc, code_c)
+        product = capi.load().sgemm_i8_grouped
+        status = product(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: product(*args, ws, size, h),
+                    lambda: capi.sgemm_i8_grouped_workspace(groups, M, N, K, sizes[0], ldx, sizes[3], ldw, sizes[5]), x)
+        return out
+    return _run(device, stream, call, x, sx, w, sw, offsets, C)
+
+
+def sgemm_i8_quantize(X, stream=None):
+    """X [M,K] or [G,M,K] (bfloat16, float16 or float32) as an I8Matrix: for
+    each row a scale max(max|x| / 127, 2^-126) and the values x / scale rounded
+    to the nearest integer, halves to even.  A row that holds a NaN or an
+    infinity gets a NaN scale (and values 0)."""
+    import torch
+    code = _float_code(X.dtype, "X")
+    if X.dim() not in (2, 3):
+        raise ValueError("X must be 2-D or 3-D")
+    ldx = _ld_of(X, "X")
+    M, K = X.shape[-2:]
+    if X.dim() == 3 and X.shape[0] > 1 and X.stride(0) != M * ldx:
+        raise ValueError("the matrices of a 3-D X must follow each other")
+    M = M * X.shape[0] if X.dim() == 3 else M
+    if M > _INT:
+        _too_large("X")
+    device = _one_device(X)
+    ldv = (K + 15) // 16 * 16
+
+    def call(h):
+        values = X.new_empty((*X.shape[:-1], ldv), dtype=torch.int8)[..., :K]
+        scales = X.new_empty(X.shape[:-1], dtype=torch.float32)
+        _check(capi.sgemm_i8_quantize(code, M, K, X.data_ptr(), ldx, values.data_ptr(), max(ldv, 1), scales.data_ptr(), h))
+        return I8Matrix(values, scales)
+    return _run(device, stream, call, X)
+
+
+def sgemm_i8_dequantize(Q, dtype=None, stream=None):
+    """The values an I8Matrix [M,K] or [G,M,K] stands for, rounded to `dtype`
+    (default: float32)."""
+    import torch
+    dtype = dtype or torch.float32
+    code = _float_code(dtype, "dtype")
+    values, scales = Q
+    if values.dim() not in (2, 3):
+        raise ValueError("Q must be 2-D or 3-D")
+    M, K, ldv = _i8(Q, "Q", values.dim())
+    if values.dim() == 3:
+        if values.shape[0] > 1 and (values.stride(0) != M * ldv or scales.stride(0) != M):
+            raise ValueError("the matrices of a 3-D Q must follow each other")
+        M *= values.shape[0]
+        if M > _INT:
+            _too_large("Q")
+    device = _one_device(values, ("scales", scales))
+
+    def call(h):
+        out = values.new_empty(values.shape, dtype=dtype)
+        _check(capi.sgemm_i8_dequantize(code, M, K, values.data_ptr(), ldv, scales.data_ptr(), out.data_ptr(), max(K, 1), h))
+        return out
+    return _run(device, stream, call, values, scales)
+
+
+class GroupOrder(NamedTuple):
+    """The order sgemm_grouped_sort gives T tokens of `picks` experts each, all
+    int32: offsets [groups + 1], rows offsets[g] .. offsets[g+1] - 1 being group
+    g's; position [T,picks], the row of each token and pick, -1 for those of no
+    group; source [T*picks], token * picks + pick of each row, -1 behind
+    offsets[groups]."""
+    offsets: "torch.Tensor"             # noqa: F821
+    position: "torch.Tensor"            # noqa: F821
+    source: "torch.Tensor"              # noqa: F821
+
+
+def sgemm_grouped_sort(X, experts, groups, stream=None):
+    """(rows, order): the rows of X [T,H] sorted by expert, as the grouped
+    products take them, and the GroupOrder.
+
+    experts int32 or int64 [T,picks] (or [T]: one each); any value outside
+    0..groups-1 stands for no group (a padded token, an expert held
+    elsewhere).  A group's rows are in the order of the tokens, then of the
+    picks.  rows [T*picks,H]: rows of no group, at the end, are zeros.  X is
+    bfloat16, float16, float32 or an I8Matrix (then so are the rows), or None
+    for the order alone.  The gradient with respect to X is
+    sgemm_grouped_combine(drows, order)."""
+    import torch
+    if experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"experts is {experts.dtype}, expected int32 or int64")
+    if experts.dim() not in (1, 2):
+        raise ValueError("experts must be 1-D or 2-D")
+    if experts.dim() == 1:
+        experts = experts[:, None]
+    T, picks = experts.shape
+    if picks > 1 and experts.stride(1) != 1:
+        raise ValueError("experts must have unit column stride (row-major)")
+    lde = _ld_of(experts, "experts")
+    n = T * picks
+    if not 0 <= groups <= _INT or n >= _INT:
+        _too_large("experts")
+    scaled = isinstance(X, I8Matrix)
+    x, sx = X if scaled else (X, None)
+    H = ldx = 0
+    code = capi.SGEMM_DTYPE_F32
+    if x is not None:
+        if scaled:
+            _, H, ldx = _i8(X, "X", 2)
+            code = capi.SGEMM_DTYPE_I8
+        else:
+            code = _float_code(x.dtype, "X")
+            if x.dim() != 2:
+                raise ValueError("X must be 2-D")
+            H, ldx = x.shape[1], _ld_of(x, "X")
+        if x.shape[0] != T:
+            raise ValueError(f"X has {x.shape[0]} rows, experts {T}")
+    device = _one_device(experts, ("X", x), ("X's scales", sx))
+    size = _check(capi.sgemm_grouped_sort_workspace(T, picks, groups))
+
+    def call(h):
+        empty = experts.new_empty
+        order = GroupOrder(empty(groups + 1, dtype=torch.int32), empty((T, picks), dtype=torch.int32), empty(n, dtype=torch.int32))
+        rows = row_scales = None
+        ldr = max(H, 1)
+        if scaled:
+            ldr = max((H + 15) // 16 * 16, 1)
+            rows, row_scales = x.new_empty((n, ldr))[:, :H], sx.new_empty(n)
+        elif x is not None:
+            rows = x.new_empty((n, H))
+        ws = empty(size, dtype=torch.uint8) if size else None
+        _check(capi.load().sgemm_grouped_sort(
+            code, T, picks, groups, H, _address(x), ldx, _address(sx), experts.data_ptr(), lde, experts.element_size(),
+            order.offsets.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
+            _address(row_scales), _address(ws), size, h))
+        return (I8Matrix(rows, row_scales) if scaled else rows), order
+    return _run(device, stream, call, experts, x, sx)
+
+
+def _order(order, Y, name):
+    """(T, picks, H, type code, leading dimension of Y), an order and the sorted rows Y checked."""
+    import torch
+    offsets, position, source = order
+    for t, part, dims in ((offsets, "offsets", 1), (position, "position", 2), (source, "source", 1)):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{part} must be int32")
+        if t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"{part} must be {dims}-D and contiguous")
+    T, picks = position.shape
+    if offsets.shape[0] < 1 or source.shape[0] != T * picks:
+        raise ValueError(f"the order's parts have shapes {tuple(offsets.shape)}, {tuple(position.shape)} and {tuple(source.shape)}")
+    code = _float_code(Y.dtype, name)
+    if Y.dim() != 2 or Y.shape[0] != T * picks:
+        raise ValueError(f"{name} has shape {tuple(Y.shape)}, expected {T * picks} rows")
+    return T, picks, Y.shape[1], code, _ld_of(Y, name)
+
+
+def _pick_weights(weights, T, picks):
+    """(type code, leading dimension) of the picks' weights."""
+    if weights is None:
+        return capi.SGEMM_DTYPE_F32, max(picks, 1)
+    code = _float_code(weights.dtype, "weights")
+    if tuple(weights.shape) != (T, picks):
+        raise ValueError(f"weights has shape {tuple(weights.shape)}, expected {(T, picks)}")
+    return code, _ld_of(weights, "weights")
+
+
+def _mixed(a, a_name, b, b_name):
+    """Two types of which both are one, or one is float32."""
+    import torch
+    if a != b and torch.float32 not in (a, b):
+        raise TypeError(f"{a_name} is {a} but {b_name} is {b}")
+
+
+def sgemm_grouped_combine(Y, order, weights=None, out_dtype=None, stream=None):
+    """out [T,H]: out[t] = sum over t's picks j of weights[t,j] * Y[order.position[t,j]],
+    in float32; picks of no group are left out.
+
+    Y [T*picks,H] bfloat16, float16 or float32, the rows in sgemm_grouped_sort's
+    order; weights [T,picks] of any of these types (None: 1); out is of Y's
+    type unless out_dtype names float32, or for a float32 Y any of the three.
+    Gradients: sgemm_grouped_combine_grad."""
+    T, picks, H, code, ldy = _order(order, Y, "Y")
+    code_w, ldw = _pick_weights(weights, T, picks)
+    out_dtype = out_dtype or Y.dtype
+    code_out = _float_code(out_dtype, "out_dtype")
+    _mixed(Y.dtype, "Y", out_dtype, "out_dtype")
+    position = order.position
+    device = _one_device(Y, ("position", position), ("weights", weights))
+
+    def call(h):
+        out = Y.new_empty((T, H), dtype=out_dtype)
+        _check(capi.load().sgemm_grouped_combine(code, code_out, T, picks, H, Y.data_ptr(), ldy, position.data_ptr(),
+                                                 _address(weights), ldw, code_w, out.data_ptr(), max(H, 1), h))
+        return out
+    return _run(device, stream, call, Y, position, weights)
+
+
+def sgemm_grouped_combine_grad(D, Y, order, weights=None, need_dy=True, need_dweights=True, stream=None):
+    """(dY, dweights), the gradients of sum(D * out) for the out of
+    sgemm_grouped_combine(Y, order, weights); of Y's and of the weights' type.
+
+    D [T,H] is of Y's type, or one of them is float32.  dY's rows of no group
+    are zeros, as are the weights' gradients of picks of no group.  need_dy /
+    need_dweights False (or weights None): None in that place, and no work for
+    it."""
+    T, picks, H, code, ldy = _order(order, Y, "Y")
+    code_w, ldw = _pick_weights(weights, T, picks)
+    code_d = _float_code(D.dtype, "D")
+    _mixed(Y.dtype, "Y", D.dtype, "D")
+    if tuple(D.shape) != (T, H):
+        raise ValueError(f"D has shape {tuple(D.shape)}, expected {(T, H)}")
+    ldd = _ld_of(D, "D")
+    offsets, position, _ = order
+    device = _one_device(D, ("Y", Y), ("offsets", offsets), ("position", position), ("weights", weights))
+
+    def call(h):
+        dY = Y.new_empty((T * picks, H)) if need_dy else None
+        dweights = weights.new_empty((T, picks)) if need_dweights and weights is not None else None
+        _check(capi.load().sgemm_grouped_combine_grad(
+            code, code_d, T, picks, offsets.shape[0] - 1, H, D.data_ptr(), ldd, Y.data_ptr(), ldy, offsets.data_ptr(),
+            position.data_ptr(), _address(weights), ldw, code_w, _address(dY), max(H, 1), _address(dweights), h))
+        return dY, dweights
+    return _run(device, stream, call, D, Y, offsets, position, weights)

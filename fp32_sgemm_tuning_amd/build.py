@@ -3,8 +3,8 @@ twin libsgemm_poison.so.
 
     python -m fp32_sgemm_tuning_amd.build [--isa]
 
-libsgemm_poison.so is the same library with the lean FP32, the 16-bit and the
-4-bit kernel units compiled with SGEMM_LDS_POISON=1: every LDS stage is filled
+libsgemm_poison.so is the same library with the lean FP32, the 16-bit, the
+4-bit and the 8-bit kernel units compiled with SGEMM_LDS_POISON=1: every LDS stage is filled
 with NaN bits as soon as its last reader has passed its barrier, so a
 missing barrier gives a wrong result (tests only; the units without such
 kernels are the normal build's).
@@ -43,11 +43,13 @@ UNITS = [
     ("sgemm_group.hip", VGPR_FORM),
     ("sgemm_xent.hip", VGPR_FORM),
     ("sgemm_w4.hip", VGPR_FORM),
+    ("sgemm_i8.hip", VGPR_FORM),
+    ("sgemm_route.hip", []),
 ]
 SOURCES = [os.path.join(CSRC, u) for u, _ in UNITS]
 # units rebuilt with the LDS poison for the race-check library; the others,
 # which hold no kernel whose LDS stages are poisoned, are linked as they are
-PLAIN_UNITS = ("sgemm.hip",)
+PLAIN_UNITS = ("sgemm.hip", "sgemm_route.hip")
 POISON_UNITS = [(u, extra + ["-DSGEMM_LDS_POISON=1"]) for u, extra in UNITS if u not in PLAIN_UNITS]
 DEPS = SOURCES + [os.path.join(CSRC, h) for h in ("sgemm_kernels.hpp", "sgemm_lean.hpp", "sgemm_lowp.hpp",
                                                      "sgemm_tile16.hpp", "sgemm_rows.hpp")] + \

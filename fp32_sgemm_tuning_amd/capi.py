@@ -31,6 +31,7 @@ SGEMM_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024 + 16 * 1024
 SGEMM_DTYPE_BF16 = 1
 SGEMM_DTYPE_F16 = 2
 SGEMM_DTYPE_F32 = 3
+SGEMM_DTYPE_I8 = 4
 
 SGEMM_OP_N = 0
 SGEMM_OP_T = 1
@@ -50,7 +51,9 @@ EXPORTS = ("sgemm", "sgemm_ex", "sgemm_select_variant", "sgemm_num_variants",
            "sgemm_noalloc", "sgemm_lowp_grouped", "sgemm_lowp_grouped_workspace", "sgemm_lowp_grouped_wgrad",
            "sgemm_lowp_grouped_wgrad_workspace", "sgemm_lowp_xent", "sgemm_lowp_xent_grad",
            "sgemm_lowp_xent_workspace", "sgemm_w4", "sgemm_w4_workspace", "sgemm_w4_quantize", "sgemm_w4_dequantize",
-           "sgemm_w4_select_form")
+           "sgemm_w4_select_form", "sgemm_i8", "sgemm_i8_workspace", "sgemm_i8_grouped", "sgemm_i8_grouped_workspace",
+           "sgemm_i8_quantize", "sgemm_i8_dequantize", "sgemm_grouped_sort", "sgemm_grouped_sort_workspace",
+           "sgemm_grouped_combine", "sgemm_grouped_combine_grad")
 
 _lib = None
 
@@ -139,7 +142,18 @@ def open_library(path: str) -> ctypes.CDLL:
             ("sgemm_w4_workspace", [i, i, vp, i], ll),
             ("sgemm_w4_select_form", [i, i], i),
             ("sgemm_w4_quantize", [i, i, i, vp, i, i, vp, vp, vp, vp], i),
-            ("sgemm_w4_dequantize", [i, i, i, vp, vp, vp, i, vp, i, vp], i)):
+            ("sgemm_w4_dequantize", [i, i, i, vp, vp, vp, i, vp, i, vp], i),
+            ("sgemm_i8", [i, i, i, f, vp, i, vp, vp, i, vp, f, vp, i, i, vp, ll, vp], i),
+            ("sgemm_i8_workspace", [i, i, i, vp, i, vp, i], ll),
+            ("sgemm_i8_grouped", [i, i, i, i, f, vp, i, vp, vp, i, ll, vp, ll, vp, f, vp, i, i, vp, ll, vp], i),
+            ("sgemm_i8_grouped_workspace", [i, i, i, i, vp, i, vp, i, ll], ll),
+            ("sgemm_i8_quantize", [i, i, i, vp, i, vp, i, vp, vp], i),
+            ("sgemm_i8_dequantize", [i, i, i, vp, i, vp, vp, i, vp], i),
+            ("sgemm_grouped_sort", [i, i, i, i, i, vp, i, vp, vp, i, i, vp, vp, vp, vp, i, vp, vp, ll, vp], i),
+            ("sgemm_grouped_sort_workspace", [i, i, i], ll),
+            ("sgemm_grouped_combine", [i, i, i, i, i, vp, i, vp, vp, i, i, vp, i, vp], i),
+            ("sgemm_grouped_combine_grad",
+             [i, i, i, i, i, i, vp, i, vp, i, vp, vp, vp, i, i, vp, i, vp, vp], i)):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = res
     lib.sgemm_strerror.argtypes = [i]
@@ -285,6 +299,55 @@ def sgemm_w4_quantize(dtype, N, K, W, ldw, group, packed, scales, zeros, stream)
 
 def sgemm_w4_dequantize(dtype, N, K, packed, scales, zeros, group, W, ldw, stream):
     return load().sgemm_w4_dequantize(dtype, N, K, packed, scales, zeros, group, W, ldw, stream)
+
+
+def sgemm_i8(M, N, K, alpha, X, ldx, x_scales, W, ldw, w_scales, beta, C, ldc, dtype_c, workspace, workspace_bytes,
+             stream):
+    return load().sgemm_i8(M, N, K, alpha, X, ldx, x_scales, W, ldw, w_scales, beta, C, ldc, dtype_c, workspace,
+                           workspace_bytes, stream)
+
+
+def sgemm_i8_workspace(M, N, K, X, ldx, W, ldw):
+    return load().sgemm_i8_workspace(M, N, K, X, ldx, W, ldw)
+
+
+def sgemm_i8_grouped(groups, M, N, K, alpha, X, ldx, x_scales, W, ldw, stride_w, w_scales, stride_s, offsets, beta, C,
+                     ldc, dtype_c, workspace, workspace_bytes, stream):
+    return load().sgemm_i8_grouped(groups, M, N, K, alpha, X, ldx, x_scales, W, ldw, stride_w, w_scales, stride_s,
+                                   offsets, beta, C, ldc, dtype_c, workspace, workspace_bytes, stream)
+
+
+def sgemm_i8_grouped_workspace(groups, M, N, K, X, ldx, W, ldw, stride_w):
+    return load().sgemm_i8_grouped_workspace(groups, M, N, K, X, ldx, W, ldw, stride_w)
+
+
+def sgemm_i8_quantize(dtype, M, K, X, ldx, values, ldv, scales, stream):
+    return load().sgemm_i8_quantize(dtype, M, K, X, ldx, values, ldv, scales, stream)
+
+
+def sgemm_i8_dequantize(dtype, M, K, values, ldv, scales, X, ldx, stream):
+    return load().sgemm_i8_dequantize(dtype, M, K, values, ldv, scales, X, ldx, stream)
+
+
+def sgemm_grouped_sort(dtype, T, picks, groups, H, X, ldx, x_scales, experts, lde, expert_bytes, offsets, position,
+                       source, rows, ldr, row_scales, workspace, workspace_bytes, stream):
+    return load().sgemm_grouped_sort(dtype, T, picks, groups, H, X, ldx, x_scales, experts, lde, expert_bytes, offsets,
+                                     position, source, rows, ldr, row_scales, workspace, workspace_bytes, stream)
+
+
+def sgemm_grouped_sort_workspace(T, picks, groups):
+    return load().sgemm_grouped_sort_workspace(T, picks, groups)
+
+
+def sgemm_grouped_combine(dtype, dtype_out, T, picks, H, Y, ldy, position, weights, ldw, dtype_w, out, ldo, stream):
+    return load().sgemm_grouped_combine(dtype, dtype_out, T, picks, H, Y, ldy, position, weights, ldw, dtype_w, out,
+                                        ldo, stream)
+
+
+def sgemm_grouped_combine_grad(dtype, dtype_d, T, picks, groups, H, D, ldd, Y, ldy, offsets, position, weights, ldw,
+                               dtype_w, dY, lddy, dweights, stream):
+    return load().sgemm_grouped_combine_grad(dtype, dtype_d, T, picks, groups, H, D, ldd, Y, ldy, offsets, position,
+                                             weights, ldw, dtype_w, dY, lddy, dweights, stream)
 
 
 def sgemm_lowp_variant_name(variant):

@@ -24,7 +24,7 @@
 #include "sgemm.h"
 #include "sgemm_kernels.hpp"
 
-#define SGEMM_LIB_VERSION 3
+#define SGEMM_LIB_VERSION 4
 
 namespace sgemm_mi355x {
 // Lean direct-to-LDS kernels (sgemm_lean.hip, built with MFMA results in
@@ -1663,7 +1663,8 @@ const char *sgemm_strerror(int status) {
         case SGEMM_STATUS_INVALID_OP: return "operation code is neither SGEMM_OP_N nor SGEMM_OP_T";
         case SGEMM_STATUS_INVALID_DTYPE:
             return "input type is neither SGEMM_DTYPE_BF16 nor SGEMM_DTYPE_F16, or the result's neither the inputs' nor "
-                   "SGEMM_DTYPE_F32";
+                   "SGEMM_DTYPE_F32; 8-bit products, sorted and combined rows: none of those three (sorted rows also "
+                   "SGEMM_DTYPE_I8), or one side BF16 and the other FP16; experts in neither 4 nor 8 bytes";
         case SGEMM_STATUS_SCRATCH_TOO_SMALL:
             return "sgemm_noalloc: the split of K needs more scratch than SGEMM_NOALLOC_SCRATCH_BYTES; other calls: the "
                    "workspace is missing, not 16-byte aligned or too small";

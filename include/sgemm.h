@@ -96,7 +96,8 @@ extern "C" {
 /* Element types of sgemm_lowp and the calls below it. */
 #define SGEMM_DTYPE_BF16 1                  /* bfloat16: 1 sign, 8 exponent, 7 fraction bits */
 #define SGEMM_DTYPE_F16 2                   /* IEEE binary16 */
-#define SGEMM_DTYPE_F32 3                   /* IEEE binary32: result type of the grouped and 4-bit products */
+#define SGEMM_DTYPE_F32 3                   /* IEEE binary32: result type of the grouped, 4-bit and 8-bit products */
+#define SGEMM_DTYPE_I8 4                    /* 8-bit integers with a scale for each row: rows that sgemm_grouped_sort takes */
 
 /* Operation codes of the sgemm_op family. */
 #define SGEMM_OP_N 0                        /* use the stored matrix as is */
@@ -518,6 +519,98 @@ int sgemm_w4_quantize(int dtype, int N, int K, const void *W, int ldw, int group
 int sgemm_w4_dequantize(int dtype, int N, int K,
                         const void *packed, const void *scales, const void *zeros, int group,
                         void *W, int ldw, void *stream);
+
+/*
+ * sgemm_i8: products of 8-bit integers with a scale for each row of X (a
+ * token) and each row of W (an output channel),
+ *   C[m][n] = alpha * x_scales[m] * w_scales[n] * sum_k X[m][k] * W[n][k]
+ *             + beta * C[m][n],
+ * X [M,K] and W [N,K] of values -128 .. 127, FP32 scales, C [M,N] of dtype_c:
+ * BF16, FP16 or FP32.  The sums are exact (32-bit integers; K up to 131071) and
+ * scaled in FP32, (sum * (alpha * x_scales[m])) * w_scales[n], so a result is
+ * the same however K is split.  Operands whose rows do not start at multiples of
+ * 16 bytes (pointer and leading dimension) are first copied into the workspace,
+ * which also takes the sums of a split K.  An operand's memory is read in whole
+ * aligned 16-byte chunks, up to 15 bytes behind the last k of a row; what they
+ * hold is not used.  M up to 2^24, N up to 2^30.
+ *
+ * sgemm_i8_grouped: the same for rows offsets[g] .. offsets[g+1] - 1 of X and of
+ * C with the weight at W + g*stride_w and scales at w_scales + g*stride_s;
+ * offsets, groups and rows of no group as in sgemm_lowp_grouped().
+ */
+int sgemm_i8(int M, int N, int K, float alpha,
+             const void *X, int ldx, const float *x_scales,
+             const void *W, int ldw, const float *w_scales,
+             float beta, void *C, int ldc, int dtype_c,
+             void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_i8_workspace(int M, int N, int K, const void *X, int ldx, const void *W, int ldw);
+int sgemm_i8_grouped(int groups, int M, int N, int K, float alpha,
+                     const void *X, int ldx, const float *x_scales,
+                     const void *W, int ldw, long long stride_w,
+                     const float *w_scales, long long stride_s,
+                     const int *offsets, float beta, void *C, int ldc, int dtype_c,
+                     void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_i8_grouped_workspace(int groups, int M, int N, int K, const void *X, int ldx,
+                                     const void *W, int ldw, long long stride_w);
+
+/*
+ * sgemm_i8_quantize: X [M,K] of BF16, FP16 or FP32 into 8-bit integers with a
+ * scale for each row, s = max(max|x| / 127, 2^-126) in FP32 and
+ * values = x / s rounded to the nearest integer, halves to even (-127 .. 127).  A
+ * row that holds a NaN or an infinity gets s NaN and values 0, so that what is
+ * made of it is NaN.  sgemm_i8_dequantize: X = values * s, rounded to `dtype`.
+ */
+int sgemm_i8_quantize(int dtype, int M, int K, const void *X, int ldx,
+                      void *values, int ldv, float *scales, void *stream);
+int sgemm_i8_dequantize(int dtype, int M, int K, const void *values, int ldv, const float *scales,
+                        void *X, int ldx, void *stream);
+
+/*
+ * sgemm_grouped_sort: T tokens, each with `picks` experts, sorted by expert into
+ * n = T * picks rows for the grouped products.  experts[t * lde + j], of
+ * expert_bytes (4 or 8) bytes, is the expert of token t's pick j; any value
+ * outside 0 .. groups - 1 stands for no group (a padded token, another rank's
+ * expert).  Written are
+ *   offsets   [groups + 1]  rows offsets[g] .. offsets[g+1] - 1 are group g's, by
+ *                           token, then by pick
+ *   position  [T][picks]    the row of (t, j), or -1 for no group
+ *   source    [n]           t * picks + j of each row, -1 behind offsets[groups]
+ *   rows      [n,H]         row position[t][j] is X[t]; zeros behind
+ *                           offsets[groups].  NULL: not wanted
+ * X [T,H] of BF16, FP16, FP32 or SGEMM_DTYPE_I8; with the last x_scales [T] are
+ * brought to row_scales [n] in the same way.  groups up to 4096, n below
+ * 2^31 - 1, H up to 2^28.  The gradient with respect to X is
+ * sgemm_grouped_combine() without weights.
+ *
+ * sgemm_grouped_combine: the way back,
+ *   out[t] = sum_j weights[t * ldw + j] * Y[position[t][j]],
+ * summed in FP32 in the order of j, picks of no group left out; weights of
+ * dtype_w (BF16, FP16 or FP32), NULL: 1.  Y [n,H], out [T,H]: of one type, or
+ * one of them FP32.
+ *
+ * sgemm_grouped_combine_grad: for D, the gradient with respect to out,
+ *   dY[position[t][j]] = weights[t * ldw + j] * D[t],
+ *   dweights[t][j] = sum_h D[t][h] * Y[position[t][j]][h],
+ * dY [n,H] of Y's type, zeros behind offsets[groups], dweights [T][picks] of
+ * dtype_w, 0 for picks of no group; either may be NULL if it is not wanted (Y
+ * is read for dweights only).  D and Y: of one type, or one of them FP32.
+ */
+int sgemm_grouped_sort(int dtype, int T, int picks, int groups, int H,
+                       const void *X, int ldx, const float *x_scales,
+                       const void *experts, int lde, int expert_bytes,
+                       int *offsets, int *position, int *source,
+                       void *rows, int ldr, float *row_scales,
+                       void *workspace, long long workspace_bytes, void *stream);
+long long sgemm_grouped_sort_workspace(int T, int picks, int groups);
+int sgemm_grouped_combine(int dtype, int dtype_out, int T, int picks, int H,
+                          const void *Y, int ldy, const int *position,
+                          const void *weights, int ldw, int dtype_w,
+                          void *out, int ldo, void *stream);
+int sgemm_grouped_combine_grad(int dtype, int dtype_d, int T, int picks, int groups, int H,
+                               const void *D, int ldd, const void *Y, int ldy,
+                               const int *offsets, const int *position,
+                               const void *weights, int ldw, int dtype_w,
+                               void *dY, int lddy, void *dweights, void *stream);
 
 /* The variant sgemm_lowp() would run for these arguments (no launch; the
  * pointers are only inspected for alignment), or SGEMM_STATUS_INVALID_DIM.
