@@ -9,11 +9,13 @@
 // ((float)sum * (alpha * sx)) * sw, in FP32, then to C's type.
 //
 //   i8_rows_kernel   few rows of X: bound by W's bytes
-//   i8_tile_kernel,
-//   i8_mixed_kernel  tiles through LDS, on the K loop of sgemm_lowp.hpp
-//   i8_join_kernel   adds the shares of a split K
+//   i8_tile_kernel   tiles through LDS, on the K loop of sgemm_lowp.hpp
+//   i8_wide_kernel   many tiles of 256 x 256, on a K loop of their own
+//   i8_share_kernel,
+//   i8_join_kernel   tiles of a share of K, and the shares added
 //   i8_quantize_kernel, i8_dequantize_kernel
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "sgemm_rows.hpp"
@@ -21,6 +23,11 @@
 namespace sgemm_mi355x {
 
 namespace {
+
+using Tile32x32 = TileShape<32, 32, 64, 1, 2, 8, false>;
+using Tile64 = TileShape<64, 64, 64, 2, 2, 4, false>;
+using Tile128x64 = TileShape<128, 64, 64, 4, 2, 4, false>;
+using TileFourth = TileShape<128, 128, 64, 4, 2, 3, false>;
 
 struct I8Args {
     const char *X, *W;                      // 8-bit integers, rows of whole aligned 16-byte chunks
@@ -32,6 +39,7 @@ struct I8Args {
     float alpha, beta;
     int dtype_c;
     int *parts;                             // the shares' sums [shares][M][ceil_to(N, 4)]
+    int most;                               // tiles of 256 x 256 at most
     __device__ __forceinline__ void rows_of(int g, int &lo, int &rows) const {
         if (offsets) group_rows(offsets, g, M, lo, rows);
         else lo = 0, rows = M;
@@ -118,22 +126,297 @@ __global__ void __launch_bounds__(T::NT) i8_tile_kernel(I8Args p) {
     if (tm * T::BM < rows) i8_tile<T>(p, lds, g, lo, rows, tm * T::BM, tn * T::BN);
 }
 
-// Tiles of 256 x 256 with a finer last round.
-struct I8Body {
-    const TileList<256, I8Args> list;
-    template <class T>
-    __device__ __forceinline__ void tile(char *lds, int id, int sub) const {
-        int g = 0, lo = 0, rows = 0, tm = 0, tn = 0, m0, n0;
-        list.find(id, g, lo, rows, tm, tn);
-        part_corner<T>(tm, tn, sub, m0, n0);
-        if (m0 < rows && n0 < list.p.N) i8_tile<T>(list.p, lds, g, lo, rows, m0, n0);
+// ---------------------------------------------------------------------------
+// Many tiles: 256 x 256, on a K loop of their own.
+//
+// What a compute unit loads bounds such tiles: 64 KiB per 128 k, for 2048 cycles
+// of matrix instructions.  Its first-level cache, 32 KiB of 128-byte lines, also
+// holds what is in flight, so a load that takes half of each line it touches (a K
+// tile of 64 bytes) leaves half as much in flight and fetches every line twice.
+// Here a unit of K is 128 bytes, whole lines of each row (8192 x 14336 x 4096 to
+// BF16: 58 -> 29 million reads of the second-level cache, 445 -> 397 us; with all
+// that follows 373, 2580 TOPS, of which storing 235 MB is about 45).
+//
+// Five LDS slots of 32 KiB hold the units of A and of B in turn, A_u in slot 2u
+// mod 5 and B_u in the next.  Eight waves in two groups, one wave of each on a
+// SIMD, read fragments and multiply in turn, half a unit (64 k) at a time, one
+// group a phase behind the other; every phase ends with a barrier.  In unit u's
+// first read phase the loads of B_{u+1} are issued, in its second those of
+// A_{u+2}, into the slots of unit u - 1, which all waves have read by then; the
+// wait for unit u + 1 is at the end of the last phase before it is read, and
+// leaves A_{u+2} in flight.
+//
+// A lane holds 16 consecutive columns of a row of C (two 16-byte stores in 16
+// bits): the rows of B enter the matrix instruction so that its column j of block
+// nb is the wave's column 16 * (j / 4) + 4 * nb + j % 4.  A chunk c of row r lies
+// at c ^ (r / 2 % 8) in A's slots and at c ^ key_b(r) in B's, whose 16 rows to a
+// read differ in bits 0, 1, 4 and 5: no bank conflicts counted in either.
+//
+// A workgroup per compute unit takes tiles one after another.  The loads of the
+// next tile's first units are issued before a tile is stored, and nothing waits
+// for the stores until the second unit is read (381 -> 373 us).
+struct Wide {
+    static constexpr int SLOT = 32768, LDS = 5 * SLOT, NT = 512, WORKGROUPS = 256;
+    using Acc = i32x4[8][4];
+    struct Tile {
+        int g, lo, rows, m0, n0;
+        const char *A, *B;                  // the tile's corner in each operand
+    };
+    const I8Args &p;
+    char *lds;
+    int lane, wave, units, kr;              // kr: bytes of the remainder unit, which comes first (0: none)
+    unsigned to;                            // LDS address of this wave's part of slot 0
+
+    static __device__ __forceinline__ int key_b(int r) { return ((r >> 4) & 3) << 1 | ((r >> 1) & 1); }
+    __device__ __forceinline__ Wide(const I8Args &args, char *l) : p(args), lds(l), lane(threadIdx.x & 63) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int K = (p.K + 15) & ~15;
+        kr = K % 128;
+        if ((p.K & 15) && kr == 0) kr = 128;    // the cut chunk is one of the remainder's
+        units = (K - kr) / 128 + (kr != 0);
+        to = (unsigned)reinterpret_cast<uintptr_t>((lds_addr_t)lds) + wave * 1024;
+    }
+    __device__ __forceinline__ void place(Tile &t) const {
+        t.A = p.X + (t.lo + (long)t.m0) * p.ldx;
+        t.B = p.W + t.g * p.strideW + t.n0 * p.ldw;
+    }
+    // This lane's row of the first 64 of a slot, and the chunk of it that it loads.
+    __device__ __forceinline__ int row_of() const { return wave * 8 + (lane >> 3); }
+    template <bool B>
+    __device__ __forceinline__ int chunk_of() const { return (lane & 7) ^ (B ? key_b(row_of()) : (row_of() >> 1) & 7); }
+    // Race-check build: what this lane's loads of a slot fill, before they are issued.
+    __device__ __forceinline__ void poison(int slot) const {
+        if constexpr (SGEMM_LDS_POISON) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<i32x4 *>(lds + slot * SLOT + wave * 1024 + i * 8192 + 16 * lane) = i32x4{-1, -1, -1, -1};
+            wait_lgkmcnt0();
+        }
+    }
+    // `bytes` of each row from `from` on into a slot.  Rows past the operand's last
+    // lie behind the descriptor's range, which ends with that row's bytes (a row is
+    // as long as the leading dimension at most).
+    template <bool B>
+    __device__ __forceinline__ void load_rows(const Tile &t, const char *from, int bytes, bool in, int slot) const {
+        poison(slot);
+        const int ld = (int)(B ? p.ldw : p.ldx), rows = B ? min(256, p.N - t.n0) : min(256, t.rows - t.m0);
+        const int off = row_of() * ld + 16 * chunk_of<B>();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dma16_lowp(from, (rows - 1) * ld + bytes, to + slot * SLOT + i * 8192, in ? off + i * 64 * ld : (int)kOutOfRange);
+    }
+    // Unit u of A or (B) of B into a slot.
+    template <bool B>
+    __device__ __forceinline__ void load(const Tile &t, int u, int slot) const {
+        load_rows<B>(t, (B ? t.B : t.A) + (kr ? u - 1 : u) * 128l, 128, true, slot);
+    }
+    template <bool B>
+    __device__ __forceinline__ void load_first(const Tile &t, int slot) const {
+        if (!kr) load<B>(t, 0, slot);
+        else load_rows<B>(t, (B ? t.B : t.A) + (((p.K + 15) & ~15) - kr), kr, 16 * chunk_of<B>() < kr, slot);
+    }
+    // The loads of a tile's first units, into all five slots: no wave reads any.
+    __device__ __forceinline__ void begin(const Tile &t) const {
+        if (units == 0) return;
+        load_first<false>(t, 0);
+        load_first<true>(t, 1);
+        if (units < 2) return;
+        load<false>(t, 1, 2);
+        load<true>(t, 1, 3);
+        if (units > 2) load<false>(t, 2, 4);
+    }
+    // acc = the product of a tile that begin() was called for; `landed`: its loads
+    // have, and stores may be in flight.  Behind it no wave reads LDS.
+    __device__ __forceinline__ void multiply(const Tile &t, Acc &acc, bool landed) const {
+#pragma unroll
+        for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) acc[mi][nb] = i32x4{0, 0, 0, 0};
+        if (units == 0) return;
+        using AL = ALayout<32>;
+        const int group = wave >> 2, lr = lane & 15, lg = lane >> 4;
+        if (!landed) {                      // unit 0 has landed
+            if (units > 2) wait_vm_lgkm0<12>();
+            else if (units == 2) wait_vm_lgkm0<8>();
+            else wait_vm_lgkm0<0>();
+        }
+        if (p.K & 15) {                     // what A's rows hold behind K does not count
+            if (16 * chunk_of<false>() + 16 == kr) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    i32x4 *chunk = reinterpret_cast<i32x4 *>(lds + wave * 1024 + i * 8192 + 16 * lane);
+                    *chunk = first_bytes(*chunk, p.K & 15);
+                }
+            }
+            wait_lgkmcnt0();
+        }
+        __builtin_amdgcn_s_barrier();
+        if (group) __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const int rowb = (wave & 3) * 64 + 16 * (lr >> 2) + (lr & 3);
+        // (the second half of a unit: chunks 4 .. 7, bit 6 of the address)
+        const int fromA = 4 * AL::offset(group * 128 + lr, lg), fromB = 128 * rowb + 16 * (lg ^ key_b(rowb));
+        int sa = 0, u = 0;                  // A_u's slot
+        asm volatile("" : "+s"(u));         // (no copy of the loop for its first turn, which would take registers of its own)
+        for (; u < units; ++u) {
+            const int sb = sa == 4 ? 0 : sa + 1, next = sb == 4 ? 0 : sb + 1, free0 = next == 4 ? 0 : next + 1, free1 = free0 == 4 ? 0 : free0 + 1;
+            // the loads of unit u + 1 have landed, those of A_{u+2} may be in flight
+            auto next_landed = [&]() {
+                if (u == 0 && landed) return;
+                if (u + 2 < units) wait_vm_lgkm0<4>();
+                else wait_vm_lgkm0<0>();
+            };
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const char *A = lds + sa * SLOT + (fromA ^ (64 * ks)), *B = lds + sb * SLOT + (fromB ^ (64 * ks));
+                i32x4 fa[8], fb[4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) fb[nb] = *reinterpret_cast<const i32x4 *>(B + nb * 512);
+#pragma unroll
+                for (int mi = 0; mi < 8; ++mi) fa[mi] = *reinterpret_cast<const i32x4 *>(A + mi * 2048);
+                if (ks == 0) {
+                    if (u > 0 && u + 1 < units) load<true>(t, u + 1, free0);
+                } else {
+                    if (u > 0 && u + 2 < units) load<false>(t, u + 2, free1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                wait_lgkmcnt0();
+                if (ks == 1 && group) next_landed();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) acc[mi][nb] = Product<kMulI8>::mfma(fb[nb], fa[mi], acc[mi][nb]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (ks == 1 && !group) next_landed();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            sa = next;
+        }
+        if (!group) __builtin_amdgcn_s_barrier();
+    }
+    // C of a tile.  All loads before it have landed before its first store.
+    __device__ __forceinline__ void store(const Tile &t, const Acc &acc) const {
+        int l = threadIdx.x & 63;
+        asm volatile("" : "+v"(l));         // (what follows from it is not kept in registers from tile to tile)
+        const int row0 = t.m0 + (wave >> 2) * 128 + (l & 15), col = t.n0 + (wave & 3) * 64 + 16 * (l >> 4);
+        float sx[8];
+        f32x4 sw[4];
+#pragma unroll
+        for (int mi = 0; mi < 8; ++mi) sx[mi] = p.alpha * p.sx[t.lo + min(row0 + mi * 16, t.rows - 1)];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) sw[nb] = scales4(p.sw + t.g * p.strideS, col + 4 * nb, p.N);
+        wait_vmcnt0();
+        by_result(p.dtype_c, [&](auto f16, auto out16) {
+            constexpr bool F16 = decltype(f16)::value, OUT16 = decltype(out16)::value;
+#pragma unroll
+            for (int mi = 0; mi < 8; ++mi) {
+                __builtin_amdgcn_sched_barrier(0);      // (eight rows at once need more registers than there are)
+                const int row = row0 + mi * 16;
+                char *at = p.C + (t.lo + (long)row) * p.ldc * (OUT16 ? 2 : 4);
+                f32x4 v[4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) v[nb] = to_float(acc[mi][nb]) * sx[mi] * sw[nb];
+                if constexpr (!OUT16) turn(v);
+                if (row >= t.rows) continue;
+                if (OUT16 && p.beta == 0.f && col + 16 <= p.N) {
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        const i32x2 x = round16<F16>(v[h]), y = round16<F16>(v[h + 1]);
+                        const i32x4 o = {x[0], x[1], y[0], y[1]};
+                        __builtin_memcpy(at + 2l * (col + 4 * h), &o, 16);
+                    }
+                } else if (OUT16) {
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) store4<F16, OUT16>(at, col + 4 * nb, p.N, p.beta, v[nb]);
+                } else {                    // the four lanes of a row side by side in every store
+                    const int first = t.n0 + (wave & 3) * 64 + 4 * (l >> 4);
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) store4<F16, OUT16>(at, first + 16 * nb, p.N, p.beta, v[nb]);
+                }
+            }
+        });
+    }
+    // Lane group l/16 = j gets of lane group i (block j) as its block i.
+    static __device__ __forceinline__ void turn(f32x4 (&v)[4]) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            unsigned x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(v[i][r]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const auto y = __builtin_amdgcn_permlane32_swap(x[i], x[i + 2], false, false);
+                x[i] = y[0];
+                x[i + 2] = y[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const auto y = __builtin_amdgcn_permlane16_swap(x[i], x[i + 1], false, false);
+                x[i] = y[0];
+                x[i + 1] = y[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i][r] = __uint_as_float(x[i]);
+        }
     }
 };
 
-__global__ void __launch_bounds__(512) i8_mixed_kernel(I8Args p) {
-    __shared__ __attribute__((aligned(16))) char lds[Mixed<true>::LDS];
-    const I8Body body{TileList<256, I8Args>(p, 256, gridDim.x - mixed_grid(0))};
-    Mixed<true>::run(body, lds, body.list.total);
+// Tiles of 256 x 256, in rounds of one per compute unit; the tiles of a last round
+// that fills at most half of the chip are cut in two or four, a part for each
+// workgroup, as in Mixed.  One workgroup per compute unit does it all: more would
+// wait for LDS and cost 3 us at the end.
+template <class T>
+__device__ __forceinline__ void i8_part(const TileList<256, I8Args> &list, char *lds, int id, int sub) {
+    int g = 0, lo = 0, rows = 0, tm = 0, tn = 0, m0, n0;
+    list.find(id, g, lo, rows, tm, tn);
+    part_corner<T>(tm, tn, sub, m0, n0);
+    if (m0 < rows && n0 < list.p.N) i8_tile<T>(list.p, lds, g, lo, rows, m0, n0);
+}
+
+__global__ void __launch_bounds__(Wide::NT) i8_wide_kernel(I8Args p) {
+    __shared__ __attribute__((aligned(16))) char lds[Wide::LDS];
+    constexpr int W = Wide::WORKGROUPS;
+    const TileList<256, I8Args> list(p, 256, p.most);
+    const int whole = list.total & ~(W - 1), rest = list.total - whole, upto = rest > W / 2 ? list.total : whole;
+    int id = blockIdx.x;
+    if (id < upto) {
+        const Wide wide(p, lds);
+        Wide::Tile t;
+        auto find = [&](int n) {
+            int tm = 0, tn = 0;
+            list.find(n < whole ? xcd_run(n, whole) : whole + xcd_run(n - whole, rest), t.g, t.lo, t.rows, tm, tn);
+            t.m0 = tm * 256;
+            t.n0 = tn * 256;
+            wide.place(t);
+        };
+        Wide::Acc acc;
+        find(id);
+        wide.begin(t);
+        for (bool landed = false;; landed = true) {
+            wide.multiply(t, acc, landed);
+            const Wide::Tile done = t;
+            id += W;
+            if (id < upto) {
+                find(id);
+                wide.begin(t);
+            }
+            wide.store(done, acc);
+            if (id >= upto) break;
+        }
+    }
+    if (upto == list.total) return;
+    const int k = blockIdx.x;
+    if (rest > W / 4) {
+        if (k >= 2 * rest) return;
+        const int at = xcd_run(k, 2 * rest);
+        i8_part<TileTall>(list, lds, whole + (at >> 1), at & 1);
+    } else if (k < 4 * rest) {
+        const int at = xcd_run(k, 4 * rest);
+        i8_part<TileFourth>(list, lds, whole + (at >> 2), at & 3);
+    }
 }
 
 // One weight, share blockIdx.y of gridDim.y of K: its sums, for i8_join_kernel.
@@ -176,96 +459,63 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args p, int shares) {
     });
 }
 
-// Few rows: MB blocks of 16 rows of X by NB blocks of 16 rows of W per
-// workgroup, whose eight waves take shares of K of their own (so no wave waits
-// for another's loads, and nothing passes through LDS but the sums at the end).
-// A lane's 16 bytes of a row are its operand of one v_mfma_i32_16x16x64_i8 as
-// they lie in memory; two steps read a row's 128-byte line, and AHEAD lines of
-// every row are in flight.
-template <int MB, int NB>
+// Up to 16 rows and few columns: a block of 16 rows of W per workgroup, whose eight
+// waves take shares of K of their own, so that no wave waits for another's loads
+// and nothing passes through LDS but the sums at the end.  A lane's 16 bytes of a
+// row are its operand of one v_mfma_i32_16x16x64_i8 as they lie in memory; two
+// steps read a row's 128-byte line, and four lines of every row are in flight.
+// 1 x 4096 x 4096: 5.7 us, where tiles of 32 x 32 take 7.2; from two blocks per
+// compute unit on those are faster (16 x 8192 x 4096: 11.3 and 9.5).
 __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args p) {
-    constexpr int NW = 8, AHEAD = MB + NB <= 3 ? 4 : 2;
-    __shared__ i32x4 part[NW][MB * NB][64];
+    constexpr int NW = 8, AHEAD = 4;
+    __shared__ i32x4 part[NW][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lr = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16 * NB, m0 = blockIdx.y * 16 * MB;
-    const char *x[MB], *w[NB];              // (rows past the last: that one again, for outputs that are not stored)
-#pragma unroll
-    for (int m = 0; m < MB; ++m) x[m] = p.X + min(m0 + 16 * m + lr, p.M - 1) * p.ldx + 16 * lg;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) w[b] = p.W + min(n0 + 16 * b + lr, p.N - 1) * p.ldw + 16 * lg;
-    i32x4 acc[MB][NB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[m][b] = i32x4{0, 0, 0, 0};
-    const int lines = (p.K + 127) / 128, last = (int)((long)lines * (wave + 1) / NW);
+    const int lr = lane & 15, lg = lane >> 4, n0 = blockIdx.x * 16;
+    // (rows past the last: that one again, for outputs that are not stored)
+    const char *x = p.X + min(lr, p.M - 1) * p.ldx + 16 * lg, *w = p.W + min(n0 + lr, p.N - 1) * p.ldw + 16 * lg;
     const i32x4 none = {0, 0, 0, 0};
-    for (int c0 = (int)((long)lines * wave / NW); c0 < last; c0 += AHEAD) {
-        i32x4 fx[AHEAD][2][MB], fw[AHEAD][2][NB];
-        if ((min(c0 + AHEAD, last)) * 128 <= p.K) {
+    i32x4 acc = none;
+    const int lines = (p.K + 127) / 128, last = lines * (wave + 1) / NW;
+    for (int c0 = lines * wave / NW; c0 < last; c0 += AHEAD) {
+        i32x4 fx[AHEAD][2], fw[AHEAD][2];
+        const bool whole = min(c0 + AHEAD, last) * 128 <= p.K;
 #pragma unroll
-            for (int t = 0; t < AHEAD; ++t) {
-                if (t && c0 + t >= last) break;
+        for (int t = 0; t < AHEAD; ++t) {
+            if (c0 + t >= last) break;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = (c0 + t) * 128 + 64 * s;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) fw[t][s][b] = *reinterpret_cast<const i32x4 *>(w[b] + k);
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) fx[t][s][m] = *reinterpret_cast<const i32x4 *>(x[m] + k);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < AHEAD; ++t) {
-                if (t && c0 + t >= last) break;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = (c0 + t) * 128 + 64 * s, left = p.K - k - 16 * lg;     // integers from this lane's chunk on
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        fw[t][s][b] = none;
-                        if (left > 0) fw[t][s][b] = *reinterpret_cast<const i32x4 *>(w[b] + k);
+            for (int s = 0; s < 2; ++s) {
+                const int k = (c0 + t) * 128 + 64 * s, left = p.K - k - 16 * lg;    // integers from this lane's chunk on
+                if (whole) {
+                    fw[t][s] = *reinterpret_cast<const i32x4 *>(w + k);
+                    fx[t][s] = *reinterpret_cast<const i32x4 *>(x + k);
+                } else {
+                    fw[t][s] = fx[t][s] = none;
+                    if (left > 0) {
+                        fw[t][s] = *reinterpret_cast<const i32x4 *>(w + k);
+                        fx[t][s] = *reinterpret_cast<const i32x4 *>(x + k);
                     }
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        fx[t][s][m] = none;
-                        if (left > 0) fx[t][s][m] = *reinterpret_cast<const i32x4 *>(x[m] + k);
-                        if (left < 16) fx[t][s][m] = first_bytes(fx[t][s][m], left);
-                    }
+                    if (left < 16) fx[t][s] = first_bytes(fx[t][s], left);
                 }
             }
         }
 #pragma unroll
         for (int t = 0; t < AHEAD; ++t) {
-            if (t && c0 + t >= last) break;
+            if (c0 + t >= last) break;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) acc[m][b] = Product<kMulI8>::mfma(fw[t][s][b], fx[t][s][m], acc[m][b]);
+            for (int s = 0; s < 2; ++s) acc = Product<kMulI8>::mfma(fw[t][s], fx[t][s], acc);
         }
     }
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) part[wave][m * NB + b][lane] = acc[m][b];
+    part[wave][lane] = acc;
     __syncthreads();
-    // block (m, b)'s lane l holds columns 4*(l/16) .. +3 of row l%16
-    for (int t = threadIdx.x; t < MB * NB * 64; t += 64 * NW) {
-        const int b = t >> 6, l = t & 63;
-        i32x4 v = part[0][b][l];
+    if (wave) return;
 #pragma unroll
-        for (int i = 1; i < NW; ++i) v += part[i][b][l];
-        const int row = m0 + 16 * (b / NB) + (l & 15), col = n0 + 16 * (b % NB) + 4 * (l >> 4);
-        if (row >= p.M || col >= p.N) continue;
-        const f32x4 c = to_float(v) * (p.alpha * p.sx[row]) * scales4(p.sw, col, p.N);
-        by_result(p.dtype_c, [&](auto f16, auto out16) {
-            store4<decltype(f16)::value, decltype(out16)::value>(p.C + row * p.ldc * (decltype(out16)::value ? 2 : 4), col, p.N, p.beta, c);
-        });
-    }
+    for (int i = 1; i < NW; ++i) acc += part[i][lane];
+    const int col = n0 + 4 * lg;            // columns .. +3 of row lr
+    if (lr >= p.M || col >= p.N) return;
+    const f32x4 c = to_float(acc) * (p.alpha * p.sx[lr]) * scales4(p.sw, col, p.N);
+    by_result(p.dtype_c, [&](auto f16, auto out16) {
+        store4<decltype(f16)::value, decltype(out16)::value>(p.C + lr * p.ldc * (decltype(out16)::value ? 2 : 4), col, p.N, p.beta, c);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -419,76 +669,99 @@ hipError_t by_dtype(int dtype, F &&f) {
 // ---------------------------------------------------------------------------
 // Which kernel.
 
-using Tile64 = TileShape<64, 64, 64, 2, 2, 4, false>;
+// The forms of one weight's product.  Each but the first is priced as
+//   3.5 us + rounds over the compute units * K / 128 * its time for 128 k of a tile,
+// and the cheapest taken.  Those times (the tile alone on its compute unit, and
+// two of them at once where LDS has room) are from shapes that fill one round or
+// more at K = 4096, BF16 results, in us:
+//   32 x 32     64 x 4096     7.8    64 x 64    200 x 4096  10.6,  256 x 8192  22.8
+//   128 x 64   512 x 4096    15.0    256 x 256, whole rounds: 4096 x 4096  58;
+//   in halves 1024 x 8192    40      in quarters  1024 x 4096  22.5
+// (64 x 64 at the last two takes 67 and 30, 128 x 64 56 and 25).  A grid of 64 x 64
+// tiles that leaves most of the chip idle splits K: 100 x 1000 x 8192 15.3 -> 10.3.
+enum Form { kRows, kTile32, kTile64, kTile128x64, kWide };
 
-enum Form { kRows16x16, kRows16x32, kRows32x32, kRows48x32, kRows64x16, kRows64x32, kTile64, kTile128, kTileMixed, kForms };
+struct Plan {
+    Form form;
+    int shares;
+};
 
-Form select_form(int M, int N, int K) {
-    (void)K;
-    const long n32 = (N + 31L) / 32;
-    if (M <= 16) return n32 >= 200 ? kRows16x32 : kRows16x16;
-    if (M <= 32) return kRows32x32;
-    if (M <= 48) return kRows48x32;
-    if (M <= 64) return n32 >= 200 ? kRows64x32 : kRows64x16;
-    const long t64 = (M + 63L) / 64 * ((N + 63L) / 64), t128 = (M + 127L) / 128 * ((N + 127L) / 128);
-    return t64 <= 512 ? kTile64 : t128 <= 512 ? kTile128 : kTileMixed;
-}
-
-int select_shares(int, int, int) { return 1; }
-
-template <int MB, int NB>
-hipError_t launch_rows8(const I8Args &p, hipStream_t s) {
-    return launch_k(i8_rows_kernel<MB, NB>, dim3((unsigned)((p.N + 16 * NB - 1L) / (16 * NB)), (unsigned)((p.M + 16 * MB - 1) / (16 * MB))), dim3(512), s, p);
+Plan select_plan(int M, int N, int K) {
+    auto tiles = [&](int bm, int bn) { return (M + bm - 1L) / bm * ((N + bn - 1L) / bn); };
+    const double steps = (K + 127) / 128;
+    if (M <= 16 && N <= 16 * 256) return {kRows, 1};
+    Plan best = {kTile32, 1};
+    double least = 1e30;
+    auto offer = [&](Form form, int shares, double us) {
+        if (us < least) least = us, best = {form, shares};
+    };
+    auto paired = [](double load, double one, double two) {
+        const double full = std::floor(load / 512), rest = load - 512 * full;
+        return full * two + (rest > 256 ? two : rest > 0 ? one : 0);
+    };
+    const long t64 = tiles(64, 64), t256 = tiles(256, 256);
+    offer(kTile32, 1, 3.5 + steps * paired(tiles(32, 32), 0.134, 0.21));
+    offer(kTile64, 1, 3.5 + steps * paired(t64, 0.22, 0.58));
+    for (int s = 2; s <= 8 && t64 * s <= 256; s *= 2)
+        offer(kTile64, s, 6.5 + std::ceil(steps / s) * 0.22 + s * 8e-6 * M * N / 3.5);
+    offer(kTile128x64, 1, 3.5 + steps * 0.43 * std::ceil(tiles(128, 64) / 256.0));
+    const double whole = std::floor(t256 / 256.0), rest = t256 - 256 * whole;
+    offer(kWide, 1, 3.5 + steps * (1.65 * (whole + (rest > 128)) + (rest > 128 || rest == 0 ? 0 : rest > 64 ? 1.13 : 0.6)));
+    return best;
 }
 
 template <class T>
-hipError_t launch_tiles(const I8Args &p, int shares, hipStream_t s) {
-    const dim3 grid((unsigned)most_tiles(p.groups, p.M, p.N, T::BM, T::BN), (unsigned)shares), block(T::NT);
-    if (shares == 1) return launch_k(i8_tile_kernel<T>, grid, block, s, p);
-    const hipError_t e = launch_k(i8_share_kernel<T>, grid, block, s, p);
+hipError_t launch_tiles(const I8Args &p, hipStream_t s) {
+    return launch_k(i8_tile_kernel<T>, dim3((unsigned)most_tiles(p.groups, p.M, p.N, T::BM, T::BN)), dim3(T::NT), s, p);
+}
+
+template <class T>
+hipError_t launch_shares(const I8Args &p, int shares, hipStream_t s) {
+    const hipError_t e = launch_k(i8_share_kernel<T>, dim3((unsigned)most_tiles(1, p.M, p.N, T::BM, T::BN), (unsigned)shares), dim3(T::NT), s, p);
     if (e != hipSuccess) return e;
     return launch_k(i8_join_kernel, dim3((unsigned)(((p.N + 3L) / 4 * p.M + 255) / 256)), dim3(256), s, p, shares);
 }
 
-hipError_t launch_mixed(const I8Args &p, hipStream_t s) {
-    return launch_k(i8_mixed_kernel, dim3((unsigned)mixed_grid(most_tiles(p.groups, p.M, p.N, 256, 256))), dim3(512), s, p);
+hipError_t launch_wide(I8Args p, hipStream_t s) {
+    p.most = (int)most_tiles(p.groups, p.M, p.N, 256, 256);
+    return launch_k(i8_wide_kernel, dim3(Wide::WORKGROUPS), dim3(Wide::NT), s, p);
 }
 
-hipError_t launch_dense(const I8Args &p, int shares, hipStream_t s) {
-    switch (select_form(p.M, p.N, p.K)) {
-        case kRows16x16: return launch_rows8<1, 1>(p, s);
-        case kRows16x32: return launch_rows8<1, 2>(p, s);
-        case kRows32x32: return launch_rows8<2, 2>(p, s);
-        case kRows48x32: return launch_rows8<3, 2>(p, s);
-        case kRows64x16: return launch_rows8<4, 1>(p, s);
-        case kRows64x32: return launch_rows8<4, 2>(p, s);
-        case kTile64: return launch_tiles<Tile64>(p, shares, s);
-        case kTile128: return launch_tiles<Tile128>(p, shares, s);
-        default: return launch_mixed(p, s);
+// (what the counts of tiles stay below)
+bool wide_fits(int groups, int M, int N) { return launch_fits(most_tiles(groups, M, N, 256, 256), Wide::NT); }
+
+hipError_t launch_dense(const I8Args &p, Plan plan, hipStream_t s) {
+    switch (plan.form) {
+        case kRows: return launch_k(i8_rows_kernel, dim3((unsigned)((p.N + 15) / 16)), dim3(512), s, p);
+        case kTile32: return launch_tiles<Tile32x32>(p, s);
+        case kTile64: return plan.shares > 1 ? launch_shares<Tile64>(p, plan.shares, s) : launch_tiles<Tile64>(p, s);
+        case kTile128x64: return launch_tiles<Tile128x64>(p, s);
+        default: return launch_wide(p, s);
     }
 }
 
 // Whether one launch can cover the outputs.
 bool dense_fits(int M, int N, int K) {
-    switch (select_form(M, N, K)) {
+    switch (select_plan(M, N, K).form) {
+        case kRows: return true;
+        case kTile32: return launch_fits(most_tiles(1, M, N, 32, 32), Tile32x32::NT);
         case kTile64: return launch_fits(most_tiles(1, M, N, 64, 64), Tile64::NT);
-        case kTile128: return launch_fits(most_tiles(1, M, N, 128, 128), Tile128::NT);
-        case kTileMixed: return launch_fits(mixed_grid(most_tiles(1, M, N, 256, 256)), 512);
-        default: return launch_fits((N + 15L) / 16, 512);
+        case kTile128x64: return launch_fits(most_tiles(1, M, N, 128, 64), Tile128x64::NT);
+        default: return wide_fits(1, M, N);
     }
 }
 
 // By the rows of an average group, as the 16-bit products.
 hipError_t launch_grouped(const I8Args &p, hipStream_t s) {
     const int rows = p.M / std::min(p.groups, p.M);
-    return rows <= 32 ? launch_tiles<Tile32>(p, 1, s) : rows <= 128 ? launch_tiles<Tile128>(p, 1, s) : launch_mixed(p, s);
+    return rows <= 32 ? launch_tiles<Tile32>(p, s) : rows <= 128 ? launch_tiles<Tile128>(p, s) : launch_wide(p, s);
 }
 
 bool grouped_fits(int groups, int M, int N) {
     const int rows = groups > 0 && M > 0 ? M / std::min(groups, M) : 0;
     return rows <= 32    ? launch_fits(most_tiles(groups, M, N, 32, 128), Tile32::NT)
            : rows <= 128 ? launch_fits(most_tiles(groups, M, N, 128, 128), Tile128::NT)
-                         : launch_fits(mixed_grid(most_tiles(groups, M, N, 256, 256)), 512);
+                         : wide_fits(groups, M, N);
 }
 
 constexpr int kMaxK8 = (1 << 17) - 1;       // sums of products of -128 fit 32 bits
@@ -579,7 +852,7 @@ extern "C" {
 
 long long sgemm_i8_workspace(int M, int N, int K, const void *X, int ldx, const void *W, int ldw) {
     if (M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
-    return i8_needs(1, M, N, K, X, ldx, W, ldw, 0, select_shares(M, N, K)).all();
+    return i8_needs(1, M, N, K, X, ldx, W, ldw, 0, select_plan(M, N, K).shares).all();
 }
 
 int sgemm_i8(int M, int N, int K, float alpha, const void *X, int ldx, const float *x_scales, const void *W, int ldw,
@@ -592,14 +865,14 @@ int sgemm_i8(int M, int N, int K, float alpha, const void *X, int ldx, const flo
     if (M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || x_scales == nullptr || w_scales == nullptr || (K > 0 && (X == nullptr || W == nullptr)))
         return SGEMM_STATUS_NULL_POINTER;
-    const int shares = select_shares(M, N, K);
-    const Needs need = i8_needs(1, M, N, K, X, ldx, W, ldw, 0, shares);
+    const Plan plan = select_plan(M, N, K);
+    const Needs need = i8_needs(1, M, N, K, X, ldx, W, ldw, 0, plan.shares);
     if (!workspace_ok(need.all(), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     I8Args p = {static_cast<const char *>(X), static_cast<const char *>(W), x_scales, w_scales, static_cast<char *>(C),
-                ldx, ldw, ldc, 0, 0, nullptr, 1, M, N, K, alpha, beta, dtype_c, nullptr};
+                ldx, ldw, ldc, 0, 0, nullptr, 1, M, N, K, alpha, beta, dtype_c, nullptr, 0};
     hipError_t e = take_operands(p, need, static_cast<char *>(workspace), s);
-    if (e == hipSuccess) e = launch_dense(p, shares, s);
+    if (e == hipSuccess) e = launch_dense(p, plan, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 
@@ -624,7 +897,7 @@ int sgemm_i8_grouped(int groups, int M, int N, int K, float alpha, const void *X
     if (!workspace_ok(need.all(), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     I8Args p = {static_cast<const char *>(X), static_cast<const char *>(W), x_scales, w_scales, static_cast<char *>(C),
-                ldx, ldw, ldc, stride_w, stride_s, offsets, groups, M, N, K, alpha, beta, dtype_c, nullptr};
+                ldx, ldw, ldc, stride_w, stride_s, offsets, groups, M, N, K, alpha, beta, dtype_c, nullptr, 0};
     hipError_t e = take_operands(p, need, static_cast<char *>(workspace), s);
     if (e == hipSuccess) e = launch_grouped(p, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");

@@ -6,7 +6,7 @@ from test_kernel_asm import _device_asm, _kernels, _waits_after_direct_loads, _w
 
 UNIT = "sgemm_i8.hip"
 # kernels that stream tiles with direct-to-LDS loads, and how many of them there are
-STREAMED = {"i8_tile_kernel": 3, "i8_mixed_kernel": 1, "i8_share_kernel": 3}
+STREAMED = {"i8_tile_kernel": 5, "i8_wide_kernel": 1, "i8_share_kernel": 1}
 
 
 @pytest.fixture(scope="module")
