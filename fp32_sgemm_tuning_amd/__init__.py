@@ -759,12 +759,13 @@ def sgemm_i8_quantize(X, stream=None):
     if M > _INT:
         _too_large("X")
     device = _one_device(X)
-    ldv = (K + 15) // 16 * 16
+    ldv = max((K + 15) // 16, 1) * 16
 
     def call(h):
-        values = X.new_empty((*X.shape[:-1], ldv), dtype=torch.int8)[..., :K]
+        strides = (ldv, 1) if X.dim() == 2 else (X.shape[1] * ldv, ldv, 1)
+        values = X.new_empty_strided(X.shape, strides, dtype=torch.int8)
         scales = X.new_empty(X.shape[:-1], dtype=torch.float32)
-        _check(capi.sgemm_i8_quantize(code, M, K, X.data_ptr(), ldx, values.data_ptr(), max(ldv, 1), scales.data_ptr(), h))
+        _check(capi.load().sgemm_i8_quantize(code, M, K, X.data_ptr(), ldx, values.data_ptr(), ldv, scales.data_ptr(), h))
         return I8Matrix(values, scales)
     return _run(device, stream, call, X)
 
@@ -789,7 +790,7 @@ def sgemm_i8_dequantize(Q, dtype=None, stream=None):
 
     def call(h):
         out = values.new_empty(values.shape, dtype=dtype)
-        _check(capi.sgemm_i8_dequantize(code, M, K, values.data_ptr(), ldv, scales.data_ptr(), out.data_ptr(), max(K, 1), h))
+        _check(capi.load().sgemm_i8_dequantize(code, M, K, values.data_ptr(), ldv, scales.data_ptr(), out.data_ptr(), max(K, 1), h))
         return out
     return _run(device, stream, call, values, scales)
 
@@ -846,7 +847,6 @@ def sgemm_grouped_sort(X, experts, groups, stream=None):
         if x.shape[0] != T:
             raise ValueError(f"X has {x.shape[0]} rows, experts {T}")
     device = _one_device(experts, ("X", x), ("X's scales", sx))
-    size = _check(capi.sgemm_grouped_sort_workspace(T, picks, groups))
 
     def call(h):
         empty = experts.new_empty
@@ -854,15 +854,18 @@ def sgemm_grouped_sort(X, experts, groups, stream=None):
         rows = row_scales = None
         ldr = max(H, 1)
         if scaled:
-            ldr = max((H + 15) // 16 * 16, 1)
-            rows, row_scales = x.new_empty((n, ldr))[:, :H], sx.new_empty(n)
+            ldr = max((H + 15) // 16, 1) * 16
+            rows, row_scales = x.new_empty_strided((n, H), (ldr, 1)), sx.new_empty(n)
         elif x is not None:
             rows = x.new_empty((n, H))
-        ws = empty(size, dtype=torch.uint8) if size else None
-        _check(capi.load().sgemm_grouped_sort(
-            code, T, picks, groups, H, _address(x), ldx, _address(sx), experts.data_ptr(), lde, experts.element_size(),
-            order.offsets.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
-            _address(row_scales), _address(ws), size, h))
+        args = (code, T, picks, groups, H, _address(x), ldx, _address(sx), experts.data_ptr(), lde, experts.element_size(),
+                order.offsets.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
+                _address(row_scales))
+        sort = capi.load().sgemm_grouped_sort
+        status = sort(*args, None, 0, h)
+        if status:
+            _finish(status, lambda ws, size: sort(*args, ws, size, h),
+                    lambda: capi.sgemm_grouped_sort_workspace(T, picks, groups), experts)
         return (I8Matrix(rows, row_scales) if scaled else rows), order
     return _run(device, stream, call, experts, x, sx)
 
@@ -871,11 +874,12 @@ def _order(order, Y, name):
     """(T, picks, H, type code, leading dimension of Y), an order and the sorted rows Y checked."""
     import torch
     offsets, position, source = order
-    for t, part, dims in ((offsets, "offsets", 1), (position, "position", 2), (source, "source", 1)):
-        if t.dtype != torch.int32:
-            raise TypeError(f"{part} must be int32")
-        if t.dim() != dims or not t.is_contiguous():
-            raise ValueError(f"{part} must be {dims}-D and contiguous")
+    if not offsets.dtype == position.dtype == source.dtype == torch.int32:
+        raise TypeError("offsets, position and source must be int32")
+    if offsets.dim() != 1 or position.dim() != 2 or source.dim() != 1:
+        raise ValueError("offsets and source must be 1-D, position 2-D")
+    if not (offsets.is_contiguous() and position.is_contiguous()):
+        raise ValueError("offsets and position must be contiguous")
     T, picks = position.shape
     if offsets.shape[0] < 1 or source.shape[0] != T * picks:
         raise ValueError(f"the order's parts have shapes {tuple(offsets.shape)}, {tuple(position.shape)} and {tuple(source.shape)}")

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(256) i8_quantize_kernel(QuantArgs p) {
         larger(u);
     }
 #pragma unroll
-    for (int d = 32; d; d >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, d));
+    for (int d = NT < 64 ? NT / 2 : 32; d; d >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, d));
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
         __syncthreads();
@@ -835,7 +835,7 @@ bool workspace_ok(long need, const void *workspace, long long bytes) {
     return need == 0 || (workspace != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(workspace) & 15) == 0);
 }
 
-constexpr int kWaveRow = 1024;              // longest row that a wave quantises (in registers; a workgroup holds 4096)
+constexpr int kShortRow = 256, kWaveRow = 1024;    // longest rows that 16 lanes and a wave quantise (in registers; a workgroup holds 4096)
 constexpr int kMaxRows8 = 1 << 24;          // launch grid extents
 
 int check_quant(int dtype, int M, int K, int ldv, int ldx) {
@@ -906,14 +906,15 @@ int sgemm_i8_grouped(int groups, int M, int N, int K, float alpha, const void *X
 int sgemm_i8_quantize(int dtype, int M, int K, const void *X, int ldx, void *values, int ldv, float *scales, void *stream) {
     const int st = check_quant(dtype, M, K, ldv, ldx);
     if (st != SGEMM_STATUS_OK) return st;
-    if (!launch_fits(K <= kWaveRow ? (M + 3L) / 4 : M, 256)) return SGEMM_STATUS_INVALID_DIM;
+    if (!launch_fits(K <= kShortRow ? (M + 15L) / 16 : K <= kWaveRow ? (M + 3L) / 4 : M, 256)) return SGEMM_STATUS_INVALID_DIM;
     if (M == 0) return SGEMM_STATUS_OK;
     if (scales == nullptr || (K > 0 && (X == nullptr || values == nullptr))) return SGEMM_STATUS_NULL_POINTER;
     const QuantArgs p = {static_cast<const char *>(X), static_cast<signed char *>(values), scales, nullptr, ldx, ldv, M, K};
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const hipError_t e = by_dtype(dtype, [&](auto d) {
         constexpr int D = decltype(d)::value;
-        return p.K <= kWaveRow ? launch_k(i8_quantize_kernel<D, 64>, dim3((unsigned)((p.M + 3L) / 4)), dim3(256), s, p)
+        return p.K <= kShortRow ? launch_k(i8_quantize_kernel<D, 16>, dim3((unsigned)((p.M + 15L) / 16)), dim3(256), s, p)
+               : p.K <= kWaveRow ? launch_k(i8_quantize_kernel<D, 64>, dim3((unsigned)((p.M + 3L) / 4)), dim3(256), s, p)
                            : launch_k(i8_quantize_kernel<D, 256>, dim3((unsigned)p.M), dim3(256), s, p);
     });
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");

@@ -39,8 +39,11 @@ struct SortArgs {
     int chunk;                              // assignments per workgroup of the counting kernels
     int lanes;                              // per token in the copies
     __device__ __forceinline__ int key(int i) const {
-        const int t = (unsigned)i / (unsigned)picks;
-        const long at = t * lde + (i - t * picks);
+        long at = i;
+        if (lde != picks) {
+            const int t = (unsigned)i / (unsigned)picks;
+            at = t * lde + (i - t * picks);
+        }
         const long e = wide ? static_cast<const long long *>(experts)[at] : static_cast<const int *>(experts)[at];
         return (unsigned long)e < (unsigned long)groups ? (int)e : groups;
     }
@@ -84,17 +87,24 @@ __device__ __forceinline__ void copy_token(const SortArgs &p, int t, const int *
 
 // Up to kFew assignments, in one launch: each workgroup holds all keys in LDS
 // and counts for itself the places of its tokens' assignments (a wave each)
-// and the bounds of some groups, then copies its tokens' rows.
+// and the bounds of some groups, then copies its tokens' rows.  1024 assignments
+// 5.3 us where the three kernels below take 6.9, but 4096 11 to 18.
 constexpr int kFew = 2048;
 
 __global__ void __launch_bounds__(256) sort_few_kernel(SortArgs p) {
-    __shared__ int keys[kFew], places[kFew], kept;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < p.n; i += 256) keys[i] = p.key(i);
+    __shared__ __attribute__((aligned(16))) int keys[kFew + 256];
+    __shared__ int places[kFew], kept;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, upto = (p.n + 255) & ~255;
+    for (int i = threadIdx.x; i < upto; i += 256) keys[i] = i < p.n ? p.key(i) : 0x7fffffff;   // (neither below a key nor one)
     __syncthreads();
     auto below = [&](int key, int self) {   // keys below `key`, and equal ones before assignment `self`
         int count = 0;
-        for (int i = lane; i < p.n; i += 64) count += keys[i] < key || (keys[i] == key && i < self);
+#pragma unroll 4
+        for (int i = 4 * lane; i < upto; i += 256) {
+            const i32x4 k = *reinterpret_cast<const i32x4 *>(keys + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) count += k[e] < key || (k[e] == key && i + e < self);
+        }
         return wave_sum(count);
     };
     // the bounds: a thread each where a thread's count is short, else a wave each
@@ -302,32 +312,40 @@ __device__ __forceinline__ void store8(char *base, long row, long ld, int c, int
     if (c + 4 < H) store4<DTYPE == kF16Row, E == 2>(at, c + 4, H, 0.f, f32x4{v[4], v[5], v[6], v[7]});
 }
 
-// PICKS rows of Y in flight.
+// A piece of a token's row per `lanes` lanes and turn, with PICKS rows of Y in
+// flight.  8192 x 8 rows of 4096 in BF16 122 us, 4.9 TB/s (with four rows in flight
+// and a token's pieces one after another 141; 512 x 8 rows of 7168 23 and 34).
 template <int YT, int OT>
 __global__ void __launch_bounds__(256) combine_kernel(CombineArgs p) {
-    constexpr int PICKS = 4;
-    const int lane = threadIdx.x & (p.lanes - 1), per = 256 / p.lanes;
-    for (long t = (long)blockIdx.x * per + threadIdx.x / p.lanes; t < p.T; t += (long)gridDim.x * per) {
-        for (int c = 8 * lane; c < p.H; c += 8 * p.lanes) {
-            float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int j0 = 0; j0 < p.picks; j0 += PICKS) {
-                Row8<YT> y[PICKS];
-                int at[PICKS];
+    constexpr int PICKS = YT == kF32Row ? 4 : 8;
+    const int lane = threadIdx.x & (p.lanes - 1), per = 256 / p.lanes, cuts = (p.H + 8 * p.lanes - 1) / (8 * p.lanes);
+    for (long u = (long)blockIdx.x * per + threadIdx.x / p.lanes; u < (long)p.T * cuts; u += (long)gridDim.x * per) {
+        const int t = (int)(u / cuts), c = 8 * (lane + (int)(u - (long)t * cuts) * p.lanes);
+        if (c >= p.H) continue;
+        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int j0 = 0; j0 < p.picks; j0 += PICKS) {
+            Row8<YT> y[PICKS];
+            int at[PICKS];
+            float w[PICKS];
 #pragma unroll
-                for (int j = 0; j < PICKS; ++j) {
-                    at[j] = j0 + j < p.picks ? p.place((int)t, j0 + j) : -1;
-                    if (at[j] >= 0) y[j].load(p.Y, at[j], p.ldy, c, p.H);
-                }
-#pragma unroll
-                for (int j = 0; j < PICKS; ++j) {
-                    if (at[j] < 0) continue;
-                    const float w = p.weight((int)t, j0 + j);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[e] += w * y[j].at(e);
+            for (int j = 0; j < PICKS; ++j) {
+                at[j] = -1;
+                if (j0 + j < p.picks) {
+                    at[j] = p.place(t, j0 + j);
+                    w[j] = p.weight(t, j0 + j);
                 }
             }
-            store8<OT>(p.out, t, p.ldo, c, p.H, sum);
+#pragma unroll
+            for (int j = 0; j < PICKS; ++j)
+                if (at[j] >= 0) y[j].load(p.Y, at[j], p.ldy, c, p.H);
+#pragma unroll
+            for (int j = 0; j < PICKS; ++j) {
+                if (at[j] < 0) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += w[j] * y[j].at(e);
+            }
         }
+        store8<OT>(p.out, t, p.ldo, c, p.H, sum);
     }
 }
 
@@ -473,7 +491,7 @@ int sgemm_grouped_sort(int dtype, int T, int picks, int groups, int H, const voi
                   offsets, position, source, static_cast<int *>(workspace), (long)ldx * size, (long)ldr * size, lde, T, picks, groups, n,
                   H * size, expert_bytes == 8, 0, lanes_for((H * (long)size + 15) / 16)};
     if (n <= kFew) {
-        const hipError_t e = launch_k(sort_few_kernel, dim3((unsigned)std::min(std::max(T, 1), kFew)), dim3(256), s, p);
+        const hipError_t e = launch_k(sort_few_kernel, dim3((unsigned)std::min(std::max(T, 1), 512)), dim3(256), s, p);
         return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
     }
     const int blocks = sort_blocks(n, groups);

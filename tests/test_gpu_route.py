@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 # (T, picks, groups): one launch, several, many groups; sizes around their borders
 ORDERS = [(1, 1, 1), (1, 8, 256), (4, 2, 8), (7, 3, 5), (33, 1, 4), (64, 1, 64), (65, 1, 3), (100, 6, 60), (2048, 1, 16), (256, 8, 300),
-          (2049, 1, 16), (683, 3, 4096), (1000, 7, 1), (3001, 6, 60), (5000, 2, 2047), (4000, 3, 2048), (16384, 8, 128), (40000, 4, 4096), (70001, 2, 7)]
+          (2049, 1, 16), (4096, 1, 5), (512, 8, 64), (4097, 1, 16), (1366, 3, 4096), (1000, 7, 1), (3001, 6, 60), (5000, 2, 2047), (4000, 3, 2048), (16384, 8, 128), (40000, 4, 4096), (70001, 2, 7)]
 
 
 def experts_of(torch, T, picks, groups, seed, dtype=None, drop=0.2):

@@ -39,7 +39,7 @@ REFUSED = [
         (SMALL, dict(ldw=65, stride_w=2080, workspace=AL, workspace_bytes=2 * 32 * 64 - 1))]),
     (capi.sgemm_i8_quantize, QUANT, [
         (TYPE, dict(dtype=0)), (TYPE, dict(dtype=4)), (DIM, dict(M=-1)), (DIM, dict(K=-1)), (DIM, dict(ldx=39)), (DIM, dict(ldv=39)),
-        (DIM, dict(M=1 << 24, K=2000, ldx=2000, ldv=2000)), (DIM, dict(M=1 << 26)), (NULL, dict(X=None)), (NULL, dict(values=None)), (NULL, dict(scales=None))]),
+        (DIM, dict(M=1 << 24, K=2000, ldx=2000, ldv=2000)), (DIM, dict(M=1 << 28)), (NULL, dict(X=None)), (NULL, dict(values=None)), (NULL, dict(scales=None))]),
     (capi.sgemm_i8_dequantize, DEQUANT, [
         (TYPE, dict(dtype=4)), (DIM, dict(M=-1)), (DIM, dict(K=-1)), (DIM, dict(ldx=39)), (DIM, dict(ldv=39)), (NULL, dict(X=None)),
         (NULL, dict(values=None)), (NULL, dict(scales=None))]),
@@ -49,7 +49,7 @@ REFUSED = [
         (DIM, dict(H=(1 << 28) + 1, ldx=1 << 29, ldr=1 << 29)),
         (NULL, dict(X=None)), (NULL, dict(experts=None)), (NULL, dict(offsets=None)), (NULL, dict(position=None)), (NULL, dict(source=None)),
         (NULL, dict(dtype=4)), (NULL, dict(dtype=4, x_scales=AL)), (NULL, dict(T=0, offsets=None)),
-        (SMALL, dict(T=2000)), (SMALL, dict(T=2000, workspace=AL, workspace_bytes=8 * 5 * 4 - 1)), (SMALL, dict(T=2000, workspace=MIS, workspace_bytes=1 << 30))]),
+        (SMALL, dict(T=3000)), (SMALL, dict(T=3000, workspace=AL, workspace_bytes=12 * 5 * 4 - 1)), (SMALL, dict(T=3000, workspace=MIS, workspace_bytes=1 << 30))]),
     (capi.sgemm_grouped_combine, COMBINE, [
         (TYPE, dict(dtype=4)), (TYPE, dict(dtype_out=2)), (TYPE, dict(dtype_w=4)), (DIM, dict(T=-1)), (DIM, dict(picks=-1)), (DIM, dict(H=-1)),
         (DIM, dict(ldy=15)), (DIM, dict(ldo=15)), (DIM, dict(ldw=1)), (DIM, dict(T=1 << 30)), (NULL, dict(Y=None)), (NULL, dict(position=None)),
