@@ -27,6 +27,8 @@ namespace {
 using Tile32x32 = TileShape<32, 32, 64, 1, 2, 8, false>;
 using Tile64 = TileShape<64, 64, 64, 2, 2, 4, false>;
 using Tile128x64 = TileShape<128, 64, 64, 4, 2, 4, false>;
+using Tile32x64 = TileShape<32, 64, 64, 1, 4, 4, false>;
+using Tile64x128 = TileShape<64, 128, 64, 2, 2, 3, false>;
 using TileFourth = TileShape<128, 128, 64, 4, 2, 3, false>;
 
 struct I8Args {
@@ -751,16 +753,18 @@ bool dense_fits(int M, int N, int K) {
     }
 }
 
-// By the rows of an average group, as the 16-bit products.
+// By the rows of an average group.  In us: 512 rows in 16 groups of 2048 x 4096
+// 33 on tiles of 32 x 64, 39 on 64 x 64; 1024 rows 43 and on 64 x 128 40; 4096 rows
+// 75 on 64 x 128, 60 on 256 x 256.
 hipError_t launch_grouped(const I8Args &p, hipStream_t s) {
     const int rows = p.M / std::min(p.groups, p.M);
-    return rows <= 32 ? launch_tiles<Tile32>(p, s) : rows <= 128 ? launch_tiles<Tile128>(p, s) : launch_wide(p, s);
+    return rows <= 32 ? launch_tiles<Tile32x64>(p, s) : rows <= 128 ? launch_tiles<Tile64x128>(p, s) : launch_wide(p, s);
 }
 
 bool grouped_fits(int groups, int M, int N) {
     const int rows = groups > 0 && M > 0 ? M / std::min(groups, M) : 0;
-    return rows <= 32    ? launch_fits(most_tiles(groups, M, N, 32, 128), Tile32::NT)
-           : rows <= 128 ? launch_fits(most_tiles(groups, M, N, 128, 128), Tile128::NT)
+    return rows <= 32    ? launch_fits(most_tiles(groups, M, N, 32, 64), Tile32x64::NT)
+           : rows <= 128 ? launch_fits(most_tiles(groups, M, N, 64, 128), Tile64x128::NT)
                          : wide_fits(groups, M, N);
 }
 
