@@ -646,13 +646,22 @@ def _i8(Q, name, dims):
         raise TypeError(f"{name}'s values must be int8, got {values.dtype}")
     if scales.dtype != torch.float32:
         raise TypeError(f"{name}'s scales must be float32, got {scales.dtype}")
-    if values.dim() != dims:
+    shape, steps = values.shape, values.stride()
+    if len(shape) != dims:
         raise ValueError(f"{name} must be {dims}-D")
-    if scales.shape != values.shape[:-1]:
-        raise ValueError(f"{name}'s scales have shape {tuple(scales.shape)}, expected {tuple(values.shape[:-1])}")
-    if scales.shape[-1] > 1 and scales.stride(-1) != 1:
-        raise ValueError(f"{name}'s scales must be contiguous")
-    return values.shape[-2], values.shape[-1], _ld_of(values, name)
+    if scales.shape != shape[:-1]:
+        raise ValueError(f"{name}'s scales have shape {tuple(scales.shape)}, expected {tuple(shape[:-1])}")
+    rows, K, ld = shape[-2], shape[-1], steps[-2]
+    if steps[-1] != 1 and K > 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    if rows > 1:
+        if scales.stride(-1) != 1:
+            raise ValueError(f"{name}'s scales must be contiguous")
+    elif not ld >= K > 0:
+        ld = max(K, 1)
+    if rows | K | ld > _INT:
+        _too_large(name)
+    return rows, K, ld
 
 
 def _float_code(dtype, name):
@@ -686,7 +695,6 @@ def sgemm_i8(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
 
     Any M from a single token to a prompt, K up to 131071.  The sums are
     exact; C [M,N] is float32 (the default), bfloat16 or float16."""
-    import torch
     M, K, ldx = _i8(X, "X", 2)
     N, K2, ldw = _i8(W, "W", 2)
     if K2 != K:
@@ -715,7 +723,6 @@ def sgemm_i8_grouped(X, W, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None,
 
     X [T,K] and W [G,N,K] are I8Matrix; offsets, empty groups and rows of no
     group as in sgemm_grouped, the result as in sgemm_i8."""
-    import torch
     groups = _offsets(offsets)
     M, K, ldx = _i8(X, "X", 2)
     N, K2, ldw = _i8(W, "W", 3)

@@ -690,7 +690,7 @@ struct Plan {
 
 Plan select_plan(int M, int N, int K) {
     auto tiles = [&](int bm, int bn) { return (M + bm - 1L) / bm * ((N + bn - 1L) / bn); };
-    const double steps = (K + 127) / 128;
+    const double steps = std::max(1, (K + 127) / 128);
     if (M <= 16 && N <= 16 * 256) return {kRows, 1};
     Plan best = {kTile32, 1};
     double least = 1e30;

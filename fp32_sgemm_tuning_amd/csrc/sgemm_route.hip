@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(64 * W) sort_place_kernel(SortArgs p) {
     volatile int *mine = table[wave];
     const int bits = 32 - __builtin_clz(p.groups | 1);
     for (long i0 = from; i0 < to; i0 += 64) {
-        const int i = (int)i0 + lane;
-        const bool live = i < to;
+        const bool live = i0 + lane < to;
+        const int i = live ? (int)i0 + lane : 0;
         const int key = live ? p.key(i) : 0;
         unsigned long same = __ballot(live);
         for (int b = 0; b < bits; ++b) {
