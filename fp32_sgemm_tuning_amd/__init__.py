@@ -343,12 +343,12 @@ def _result(C, shape, out_dtype, operand):
     rows, cols = shape[-2:]
     if C is None:
         dtype = out_dtype or torch.float32
-        return operand.new_empty(shape, dtype=dtype), _CODES[dtype], max(cols, 1)
+        return operand.new_empty(shape, dtype=dtype), _codes()[dtype], max(cols, 1)
     step = C.stride(-2)
     ld = step if rows > 1 or step >= cols > 0 else max(cols, 1)
     if ld > _INT:
         _too_large("C")
-    return C, _CODES[C.dtype], ld
+    return C, _codes()[C.dtype], ld
 
 
 def _offsets(offsets):

@@ -164,3 +164,14 @@ def test_sizes_past_an_int_are_refused():
         with pytest.raises(ValueError, match="below 2\\^31"):
             call()
             pytest.fail(str(i))
+
+
+def test_first_call_of_a_process(monkeypatch):
+    """A result's type code is known before any call has looked one up."""
+    import torch
+
+    import fp32_sgemm_tuning_amd as lib
+    monkeypatch.setattr(lib, "_CODES", {})
+    assert lib._result(None, (2, 3), None, torch.zeros(1))[1:] == (capi.SGEMM_DTYPE_F32, 3)
+    monkeypatch.setattr(lib, "_CODES", {})
+    assert lib._result(torch.zeros(2, 3, dtype=torch.bfloat16), (2, 3), None, None)[1:] == (capi.SGEMM_DTYPE_BF16, 3)
