@@ -461,13 +461,39 @@ __global__ void __launch_bounds__(256) i8_join_kernel(I8Args p, int shares) {
     });
 }
 
+// One lane's 16 integers of a row from k on, of which `left` are left: those from
+// there on 0 (CUT), or whatever lies in an aligned chunk.
+template <bool ANY, bool CUT>
+__device__ __forceinline__ i32x4 row_chunk(const char *at, int left) {
+    i32x4 v = {0, 0, 0, 0};
+    if constexpr (!ANY) {
+        if (left > 0) v = *reinterpret_cast<const i32x4 *>(at);
+        return CUT && left < 16 ? first_bytes(v, left) : v;
+    }
+    if (left >= 16) {                       // from whole words: those at odd bytes load far slower
+        const unsigned past = reinterpret_cast<uintptr_t>(at) & 3;
+        const int *word = reinterpret_cast<const int *>(at - past);
+        __builtin_memcpy(&v, word, 16);
+        const int fifth = word[past ? 4 : 3];                   // (holds the 16th byte, or is one that was loaded)
+        const i32x4 up = {v[1], v[2], v[3], fifth};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (int)__builtin_amdgcn_alignbyte((unsigned)up[i], (unsigned)v[i], past);
+        return v;
+    }
+    for (int e = 0; e < left; ++e) v[e >> 2] |= (int)((unsigned)(unsigned char)at[e] << (8 * (e & 3)));
+    return v;
+}
+
 // Up to 16 rows and few columns: a block of 16 rows of W per workgroup, whose eight
 // waves take shares of K of their own, so that no wave waits for another's loads
 // and nothing passes through LDS but the sums at the end.  A lane's 16 bytes of a
 // row are its operand of one v_mfma_i32_16x16x64_i8 as they lie in memory; two
 // steps read a row's 128-byte line, and four lines of every row are in flight.
 // 1 x 4096 x 4096: 5.7 us, where tiles of 32 x 32 take 7.2; from two blocks per
-// compute unit on those are faster (16 x 8192 x 4096: 11.3 and 9.5).
+// compute unit on those are faster (16 x 8192 x 4096: 11.3 and 9.5).  ANY: rows of
+// any alignment, which the tiles would have to copy first (8 x 4096 x 4095 18.1 ->
+// 12.8 us, 16 x 14336 x 4095 41.4 -> 40.2).
+template <bool ANY>
 __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args p) {
     constexpr int NW = 8, AHEAD = 4;
     __shared__ i32x4 part[NW][64];
@@ -475,8 +501,7 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args p) {
     const int lr = lane & 15, lg = lane >> 4, n0 = blockIdx.x * 16;
     // (rows past the last: that one again, for outputs that are not stored)
     const char *x = p.X + min(lr, p.M - 1) * p.ldx + 16 * lg, *w = p.W + min(n0 + lr, p.N - 1) * p.ldw + 16 * lg;
-    const i32x4 none = {0, 0, 0, 0};
-    i32x4 acc = none;
+    i32x4 acc = {0, 0, 0, 0};
     const int lines = (p.K + 127) / 128, last = lines * (wave + 1) / NW;
     for (int c0 = lines * wave / NW; c0 < last; c0 += AHEAD) {
         i32x4 fx[AHEAD][2], fw[AHEAD][2];
@@ -486,17 +511,13 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args p) {
             if (c0 + t >= last) break;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k = (c0 + t) * 128 + 64 * s, left = p.K - k - 16 * lg;    // integers from this lane's chunk on
+                const int k = (c0 + t) * 128 + 64 * s, left = whole ? 16 : p.K - k - 16 * lg;    // integers from this lane's chunk on
                 if (whole) {
-                    fw[t][s] = *reinterpret_cast<const i32x4 *>(w + k);
-                    fx[t][s] = *reinterpret_cast<const i32x4 *>(x + k);
+                    fw[t][s] = row_chunk<ANY, false>(w + k, 16);
+                    fx[t][s] = row_chunk<ANY, false>(x + k, 16);
                 } else {
-                    fw[t][s] = fx[t][s] = none;
-                    if (left > 0) {
-                        fw[t][s] = *reinterpret_cast<const i32x4 *>(w + k);
-                        fx[t][s] = *reinterpret_cast<const i32x4 *>(x + k);
-                    }
-                    if (left < 16) fx[t][s] = first_bytes(fx[t][s], left);
+                    fw[t][s] = row_chunk<ANY, false>(w + k, left);
+                    fx[t][s] = row_chunk<ANY, true>(x + k, left);
                 }
             }
         }
@@ -688,10 +709,11 @@ struct Plan {
     int shares;
 };
 
-Plan select_plan(int M, int N, int K) {
+// `copies`: whether an operand would be copied for all forms but kRows.
+Plan select_plan(int M, int N, int K, bool copies) {
     auto tiles = [&](int bm, int bn) { return (M + bm - 1L) / bm * ((N + bn - 1L) / bn); };
     const double steps = std::max(1, (K + 127) / 128);
-    if (M <= 16 && N <= 16 * 256) return {kRows, 1};
+    if (M <= 16 && (N <= 16 * 256 || (copies && launch_fits((N + 15L) / 16, 512)))) return {kRows, 1};
     Plan best = {kTile32, 1};
     double least = 1e30;
     auto offer = [&](Form form, int shares, double us) {
@@ -732,9 +754,9 @@ hipError_t launch_wide(I8Args p, hipStream_t s) {
 // (what the counts of tiles stay below)
 bool wide_fits(int groups, int M, int N) { return launch_fits(most_tiles(groups, M, N, 256, 256), Wide::NT); }
 
-hipError_t launch_dense(const I8Args &p, Plan plan, hipStream_t s) {
+hipError_t launch_dense(const I8Args &p, Plan plan, bool copies, hipStream_t s) {
     switch (plan.form) {
-        case kRows: return launch_k(i8_rows_kernel, dim3((unsigned)((p.N + 15) / 16)), dim3(512), s, p);
+        case kRows: return launch_k(copies ? i8_rows_kernel<true> : i8_rows_kernel<false>, dim3((unsigned)((p.N + 15) / 16)), dim3(512), s, p);
         case kTile32: return launch_tiles<Tile32x32>(p, s);
         case kTile64: return plan.shares > 1 ? launch_shares<Tile64>(p, plan.shares, s) : launch_tiles<Tile64>(p, s);
         case kTile128x64: return launch_tiles<Tile128x64>(p, s);
@@ -743,8 +765,8 @@ hipError_t launch_dense(const I8Args &p, Plan plan, hipStream_t s) {
 }
 
 // Whether one launch can cover the outputs.
-bool dense_fits(int M, int N, int K) {
-    switch (select_plan(M, N, K).form) {
+bool dense_fits(Plan plan, int M, int N) {
+    switch (plan.form) {
         case kRows: return true;
         case kTile32: return launch_fits(most_tiles(1, M, N, 32, 32), Tile32x32::NT);
         case kTile64: return launch_fits(most_tiles(1, M, N, 64, 64), Tile64::NT);
@@ -770,7 +792,7 @@ bool grouped_fits(int groups, int M, int N) {
 
 constexpr int kMaxK8 = (1 << 17) - 1;       // sums of products of -128 fit 32 bits
 constexpr long kMaxLd8 = 2L * kMaxLd16;
-constexpr int kMaxGroups8 = 65535;          // launch grid extent of the padded copies
+constexpr int kMaxGroups8 = 65534;          // launch grid extent of the padded copies, X's among them
 
 // Rows of whole aligned chunks; what lies behind K in the last is not used.
 bool chunk_rows8(const void *p, long ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0 && ld <= kMaxLd8; }
@@ -792,46 +814,57 @@ Needs i8_needs(int groups, int M, int N, int K, const void *X, int ldx, const vo
             shares > 1 ? 4L * shares * M * ceil_to(N, 4) : 0};
 }
 
-// One 16-byte chunk of dst per thread and step, from rows of any alignment.
-__global__ void __launch_bounds__(256) pad_bytes_kernel(const char *src, long ld, long stride, int rows, int cols, char *dst, int chunks) {
-    src += blockIdx.y * stride;
-    dst += (long)blockIdx.y * rows * chunks * 16;
-    const long all = (long)rows * chunks;
-    for (long t = blockIdx.x * 256L + threadIdx.x; t < all; t += gridDim.x * 256L) {
-        const long r = t / chunks;
-        const int c = 16 * (int)(t - r * chunks);
-        const char *from = src + r * ld + c;
-        i32x4 v = {0, 0, 0, 0};
-        if (c + 16 <= cols) {
-            __builtin_memcpy(&v, from, 16);
-        } else {
-            for (int e = 0; c + e < cols; ++e) v[e >> 2] |= (int)((unsigned)(unsigned char)from[e] << (8 * (e & 3)));
+Needs dense_needs(Plan plan, int M, int N, int K, const void *X, int ldx, const void *W, int ldw) {
+    return plan.form == kRows ? Needs{0, 0, 0} : i8_needs(1, M, N, K, X, ldx, W, ldw, 0, plan.shares);
+}
+
+// Rows of any alignment into rows of whole aligned chunks, zeros behind them.
+struct PadJob {
+    const char *src;
+    char *dst;
+    long ld, stride;                        // bytes; from matrix to matrix
+    int rows;                               // of each matrix
+};
+
+// Matrix 0 of blockIdx.y is X, the others W's (or all W's: first 0).  A row per
+// wave and turn, a 16-byte chunk per lane.
+__global__ void __launch_bounds__(256) pad_bytes_kernel(PadJob x, PadJob w, int first, int K) {
+    const bool is_w = (int)blockIdx.y >= first;
+    const PadJob &j = is_w ? w : x;
+    const long at = is_w ? blockIdx.y - first : 0, ld = ((long)K + 15) & ~15l;
+    const char *src = j.src + at * j.stride;
+    char *dst = j.dst + at * j.rows * ld;
+    for (long r = blockIdx.x * 4l + (threadIdx.x >> 6); r < j.rows; r += gridDim.x * 4l) {
+        const char *from = src + r * j.ld;
+        for (int c = 16 * (threadIdx.x & 63); c < K; c += 1024) {
+            i32x4 v = {0, 0, 0, 0};
+            if (c + 16 <= K) {
+                __builtin_memcpy(&v, from + c, 16);     // (bound by memory; whole words and a shift are no faster here)
+            } else {
+                for (int e = 0; c + e < K; ++e) v[e >> 2] |= (int)((unsigned)(unsigned char)from[c + e] << (8 * (e & 3)));
+            }
+            *reinterpret_cast<i32x4 *>(dst + r * ld + c) = v;
         }
-        reinterpret_cast<i32x4 *>(dst)[t] = v;
     }
 }
 
-hipError_t pad_bytes(const void *src, long ld, long stride, int copies, int rows, int cols, void *dst, hipStream_t s) {
-    const int chunks = (cols + 15) / 16;
-    return launch_k(pad_bytes_kernel, dim3((unsigned)std::min(((long)rows * chunks + 255) / 256, 1L << 16), (unsigned)copies), dim3(256), s,
-                    static_cast<const char *>(src), ld, stride, rows, cols, static_cast<char *>(dst), chunks);
-}
-
-// The copies that the operands need, made in the workspace.
+// The copies that the operands need, made in the workspace by one launch.
 hipError_t take_operands(I8Args &p, const Needs &need, char *w, hipStream_t s) {
-    hipError_t e = hipSuccess;
+    p.parts = reinterpret_cast<int *>(w + need.x + need.w);
+    if (need.x + need.w == 0) return hipSuccess;
+    const PadJob jx = {p.X, w, p.ldx, 0, p.M}, jw = {p.W, w + need.x, p.ldw, p.strideW, p.N};
+    const int first = need.x ? 1 : 0, rows = std::max(need.x ? p.M : 0, need.w ? p.N : 0);
+    const hipError_t e = launch_k(pad_bytes_kernel, dim3((unsigned)std::min((rows + 3L) / 4, 1L << 20), (unsigned)(first + (need.w ? p.groups : 0))),
+                                  dim3(256), s, jx, jw, first, p.K);
     if (need.x) {
-        e = pad_bytes(p.X, p.ldx, 0, 1, p.M, p.K, w, s);
         p.X = w;
         p.ldx = ceil_to(p.K, 16);
     }
-    if (e == hipSuccess && need.w) {
-        e = pad_bytes(p.W, p.ldw, p.strideW, p.groups, p.N, p.K, w + need.x, s);
+    if (need.w) {
         p.W = w + need.x;
         p.ldw = ceil_to(p.K, 16);
         p.strideW = p.N * p.ldw;
     }
-    p.parts = reinterpret_cast<int *>(w + need.x + need.w);
     return e;
 }
 
@@ -856,7 +889,7 @@ extern "C" {
 
 long long sgemm_i8_workspace(int M, int N, int K, const void *X, int ldx, const void *W, int ldw) {
     if (M < 0 || N < 0 || K < 0) return SGEMM_STATUS_INVALID_DIM;
-    return i8_needs(1, M, N, K, X, ldx, W, ldw, 0, select_plan(M, N, K).shares).all();
+    return dense_needs(select_plan(M, N, K, !chunk_rows8(X, ldx) || !chunk_rows8(W, ldw)), M, N, K, X, ldx, W, ldw).all();
 }
 
 int sgemm_i8(int M, int N, int K, float alpha, const void *X, int ldx, const float *x_scales, const void *W, int ldw,
@@ -865,18 +898,19 @@ int sgemm_i8(int M, int N, int K, float alpha, const void *X, int ldx, const flo
     if (!dtype_ok(dtype_c)) return SGEMM_STATUS_INVALID_DTYPE;
     if (M < 0 || M > kMaxRows8 || N < 0 || N > (1 << 30) || K < 0 || K > kMaxK8) return SGEMM_STATUS_INVALID_DIM;
     if (ldx < std::max(K, 1) || ldw < std::max(K, 1) || ldc < std::max(N, 1)) return SGEMM_STATUS_INVALID_DIM;
-    if (!dense_fits(M, N, K)) return SGEMM_STATUS_INVALID_DIM;
+    const bool copies = !chunk_rows8(X, ldx) || !chunk_rows8(W, ldw);
+    const Plan plan = select_plan(M, N, K, copies);
+    if (!dense_fits(plan, M, N)) return SGEMM_STATUS_INVALID_DIM;
     if (M == 0 || N == 0) return SGEMM_STATUS_OK;
     if (C == nullptr || x_scales == nullptr || w_scales == nullptr || (K > 0 && (X == nullptr || W == nullptr)))
         return SGEMM_STATUS_NULL_POINTER;
-    const Plan plan = select_plan(M, N, K);
-    const Needs need = i8_needs(1, M, N, K, X, ldx, W, ldw, 0, plan.shares);
+    const Needs need = dense_needs(plan, M, N, K, X, ldx, W, ldw);
     if (!workspace_ok(need.all(), workspace, workspace_bytes)) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     I8Args p = {static_cast<const char *>(X), static_cast<const char *>(W), x_scales, w_scales, static_cast<char *>(C),
                 ldx, ldw, ldc, 0, 0, nullptr, 1, M, N, K, alpha, beta, dtype_c, nullptr, 0};
     hipError_t e = take_operands(p, need, static_cast<char *>(workspace), s);
-    if (e == hipSuccess) e = launch_dense(p, plan, s);
+    if (e == hipSuccess) e = launch_dense(p, plan, copies, s);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 

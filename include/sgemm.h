@@ -529,9 +529,9 @@ int sgemm_w4_dequantize(int dtype, int N, int K,
  * BF16, FP16 or FP32.  The sums are exact (32-bit integers; K up to 131071) and
  * scaled in FP32, (sum * (alpha * x_scales[m])) * w_scales[n], so a result is
  * the same however K is split.  Operands whose rows do not start at multiples of
- * 16 bytes (pointer and leading dimension) are first copied into the workspace,
- * which also takes the sums of a split K.  An operand's memory is read in whole
- * aligned 16-byte chunks, up to 15 bytes behind the last k of a row; what they
+ * 16 bytes (pointer and leading dimension) are first copied into the workspace
+ * (but not for M up to 16), which also takes the sums of a split K.  An aligned operand is read in whole
+ * 16-byte chunks, up to 15 bytes behind the last k of a row; what they
  * hold is not used.  M up to 2^24, N up to 2^30.
  *
  * sgemm_i8_grouped: the same for rows offsets[g] .. offsets[g+1] - 1 of X and of

@@ -337,6 +337,22 @@ def test_two_streams_and_a_given_one():
     assert all(torch.equal(g, want) for row in got for g in row)
 
 
+@pytest.mark.parametrize("offset", range(8))
+def test_few_rows_at_any_byte(offset):
+    """Rows of any alignment, the last ending with its allocation's last byte."""
+    torch = torch_cuda()
+    M, N, K = 3, 50, 143 + offset
+    x, w = ints8(torch, (M, K), 1), ints8(torch, (N, K), 2)
+    sx, sw = scales(torch, M, 3), scales(torch, N, 4)
+    far = torch.full((offset + N * K,), 99, dtype=torch.int8, device="cuda")
+    far[offset:].view(N, K).copy_(w)
+    got = lib.sgemm_i8(lib.I8Matrix(x, sx), lib.I8Matrix(far[offset:].view(N, K), sw))
+    check(torch, got, product_ref(x, sx, w, sw))
+    near = torch.full((offset + M * K,), 99, dtype=torch.int8, device="cuda")
+    near[offset:].view(M, K).copy_(x)
+    assert torch.equal(lib.sgemm_i8(lib.I8Matrix(near[offset:].view(M, K), sx), lib.I8Matrix(w, sw)), got)
+
+
 def test_past_32_bits():
     """Operands and results of more than 2^32 bytes; the last rows lie behind."""
     torch = torch_cuda()

@@ -6,7 +6,7 @@ from fp32_sgemm_tuning_amd import capi
 
 AL, MIS = 0x10000, 0x10002          # fake device addresses, aligned and not; never dereferenced
 
-I8 = dict(M=3, N=32, K=64, alpha=1.0, X=AL, ldx=64, x_scales=AL, W=AL, ldw=64, w_scales=AL, beta=0.0, C=AL, ldc=32, dtype_c=1,
+I8 = dict(M=17, N=32, K=64, alpha=1.0, X=AL, ldx=64, x_scales=AL, W=AL, ldw=64, w_scales=AL, beta=0.0, C=AL, ldc=32, dtype_c=1,
           workspace=None, workspace_bytes=0, stream=None)
 GROUPED = dict(groups=2, M=64, N=32, K=64, alpha=1.0, X=AL, ldx=64, x_scales=AL, W=AL, ldw=64, stride_w=2048, w_scales=AL, stride_s=32,
                offsets=AL, beta=0.0, C=AL, ldc=32, dtype_c=3, workspace=None, workspace_bytes=0, stream=None)
@@ -28,7 +28,7 @@ REFUSED = [
         (DIM, dict(N=(1 << 30) + 1, ldc=2 ** 31 - 1)), (DIM, dict(M=1 << 24, N=1 << 16, ldc=1 << 16)),
         (NULL, dict(X=None)), (NULL, dict(W=None)), (NULL, dict(C=None)), (NULL, dict(x_scales=None)), (NULL, dict(w_scales=None)),
         (SMALL, dict(X=MIS)), (SMALL, dict(W=AL + 8)), (SMALL, dict(ldx=65)), (SMALL, dict(ldw=72)),
-        (SMALL, dict(ldx=65, workspace=AL, workspace_bytes=3 * 64 - 1)), (SMALL, dict(X=MIS, workspace=MIS, workspace_bytes=1 << 30))]),
+        (SMALL, dict(ldx=65, workspace=AL, workspace_bytes=17 * 64 - 1)), (SMALL, dict(X=MIS, workspace=MIS, workspace_bytes=1 << 30))]),
     (capi.sgemm_i8_grouped, GROUPED, [
         (TYPE, dict(dtype_c=4)), (DIM, dict(groups=-1)), (DIM, dict(groups=65536)), (DIM, dict(M=-1)), (DIM, dict(N=-1)), (DIM, dict(K=-1)),
         (DIM, dict(ldx=63)), (DIM, dict(ldw=63)), (DIM, dict(ldc=31)), (DIM, dict(stride_w=-1)), (DIM, dict(stride_s=-1)),
@@ -81,8 +81,9 @@ def test_workspaces():
     ws = capi.sgemm_i8_workspace
     assert ws(3, 32, 64, AL, 64, AL, 64) == 0
     assert ws(3, 32, 61, AL, 64, AL, 64) == 0                   # what lies behind K is not used
-    assert ws(3, 32, 61, AL, 61, AL, 64) == 256                 # 3 rows of 64 bytes, whole 256s
-    assert ws(3, 32, 61, AL, 61, AL + 1, 64) == 256 + 2048
+    assert ws(20, 32, 61, AL, 61, AL, 64) == 1280               # 20 rows of 64 bytes, whole 256s
+    assert ws(20, 32, 61, AL, 61, AL + 1, 64) == 1280 + 2048
+    assert ws(16, 50000, 61, AL, 61, AL + 1, 61) == 0           # few rows are taken as they are
     assert ws(0, 32, 61, AL, 61, AL, 64) == 0
     ws = capi.sgemm_i8_grouped_workspace
     assert ws(2, 64, 32, 64, AL, 64, AL, 64, 2048) == 0
