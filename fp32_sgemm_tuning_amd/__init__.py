@@ -95,11 +95,16 @@ def _stream_handle(device, stream):
     if stream is not None:
         return stream.cuda_stream
     import torch
-    idx = device.index if device.index is not None else torch.cuda.current_device()
+    return _current_stream(device.index if device.index is not None else torch.cuda.current_device())
+
+
+def _current_stream(index):
+    """The HIP stream handle of the current stream of device `index`."""
+    import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is not None:
-        return raw(idx)
-    return torch.cuda.current_stream(idx).cuda_stream
+        return raw(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 def variant_names():
@@ -290,7 +295,7 @@ def _run(index, stream, call, *operands):
     the operands' memory is then kept until that stream has used it."""
     import torch
     if stream is None and index == torch.cuda.current_device():
-        return call(_stream_handle(operands[0].device, None))
+        return call(_current_stream(index))
     if stream is not None and stream.device.index != index:
         raise ValueError(f"stream belongs to {stream.device}, the operands to {operands[0].device}")
     with torch.cuda.device(index), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
@@ -856,8 +861,10 @@ def sgemm_grouped_sort(X, experts, groups, stream=None):
     device = _one_device(experts, ("X", x), ("X's scales", sx))
 
     def call(h):
-        empty = experts.new_empty
-        order = GroupOrder(empty(groups + 1, dtype=torch.int32), empty((T, picks), dtype=torch.int32), empty(n, dtype=torch.int32))
+        # (one allocation for the three: views are cheaper)
+        held = experts.new_empty(2 * n + groups + 1, dtype=torch.int32)
+        order = GroupOrder(held.as_strided((groups + 1,), (1,), 0), held.as_strided((T, picks), (max(picks, 1), 1), groups + 1),
+                           held.as_strided((n,), (1,), groups + 1 + n))
         rows = row_scales = None
         ldr = max(H, 1)
         if scaled:
@@ -866,7 +873,7 @@ def sgemm_grouped_sort(X, experts, groups, stream=None):
         elif x is not None:
             rows = x.new_empty((n, H))
         args = (code, T, picks, groups, H, _address(x), ldx, _address(sx), experts.data_ptr(), lde, experts.element_size(),
-                order.offsets.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
+                held.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
                 _address(row_scales))
         sort = capi.load().sgemm_grouped_sort
         status = sort(*args, None, 0, h)
