@@ -8,7 +8,7 @@
 // be split in any way and the result is rounded by the scales alone:
 // ((float)sum * (alpha * sx)) * sw, in FP32, then to C's type.
 //
-//   i8_rows_kernel   few rows of X: bound by W's bytes
+//   i8_rows_kernel   up to 16 rows of X: bound by W's bytes
 //   i8_tile_kernel   tiles through LDS, on the K loop of sgemm_lowp.hpp
 //   i8_wide_kernel   many tiles of 256 x 256, on a K loop of their own
 //   i8_share_kernel,
@@ -32,7 +32,7 @@ using Tile64x128 = TileShape<64, 128, 64, 2, 2, 3, false>;
 using TileFourth = TileShape<128, 128, 64, 4, 2, 3, false>;
 
 struct I8Args {
-    const char *X, *W;                      // 8-bit integers, rows of whole aligned 16-byte chunks
+    const char *X, *W;                      // 8-bit integers; rows at multiples of 16 bytes but for i8_rows_kernel<true>
     const float *sx, *sw;
     char *C;
     long ldx, ldw, ldc, strideW, strideS;   // elements; strides from group to group
@@ -163,6 +163,7 @@ struct Wide {
     struct Tile {
         int g, lo, rows, m0, n0;
         const char *A, *B;                  // the tile's corner in each operand
+        int endA, endB;                     // bytes from there to its last row
     };
     const I8Args &p;
     char *lds;
@@ -178,9 +179,12 @@ struct Wide {
         units = (K - kr) / 128 + (kr != 0);
         to = (unsigned)reinterpret_cast<uintptr_t>((lds_addr_t)lds) + wave * 1024;
     }
+    // (in range even if the offsets change while the kernel runs)
     __device__ __forceinline__ void place(Tile &t) const {
-        t.A = p.X + (t.lo + (long)t.m0) * p.ldx;
+        t.A = p.X + min(t.lo + t.m0, p.M - 1) * p.ldx;
         t.B = p.W + t.g * p.strideW + t.n0 * p.ldw;
+        t.endA = (min(max(t.rows - t.m0, 1), 256) - 1) * (int)p.ldx;
+        t.endB = (min(p.N - t.n0, 256) - 1) * (int)p.ldw;
     }
     // This lane's row of the first 64 of a slot, and the chunk of it that it loads.
     __device__ __forceinline__ int row_of() const { return wave * 8 + (lane >> 3); }
@@ -201,11 +205,11 @@ struct Wide {
     template <bool B>
     __device__ __forceinline__ void load_rows(const Tile &t, const char *from, int bytes, bool in, int slot) const {
         poison(slot);
-        const int ld = (int)(B ? p.ldw : p.ldx), rows = B ? min(256, p.N - t.n0) : min(256, t.rows - t.m0);
+        const int ld = (int)(B ? p.ldw : p.ldx);
         const int off = row_of() * ld + 16 * chunk_of<B>();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            dma16_lowp(from, (rows - 1) * ld + bytes, to + slot * SLOT + i * 8192, in ? off + i * 64 * ld : (int)kOutOfRange);
+            dma16_lowp(from, (B ? t.endB : t.endA) + bytes, to + slot * SLOT + i * 8192, in ? off + i * 64 * ld : (int)kOutOfRange);
     }
     // Unit u of A or (B) of B into a slot.
     template <bool B>
@@ -307,7 +311,7 @@ struct Wide {
         float sx[8];
         f32x4 sw[4];
 #pragma unroll
-        for (int mi = 0; mi < 8; ++mi) sx[mi] = p.alpha * p.sx[t.lo + min(row0 + mi * 16, t.rows - 1)];
+        for (int mi = 0; mi < 8; ++mi) sx[mi] = p.alpha * p.sx[t.lo + max(min(row0 + mi * 16, t.rows - 1), 0)];
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) sw[nb] = scales4(p.sw + t.g * p.strideS, col + 4 * nb, p.N);
         wait_vmcnt0();
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(Wide::NT) i8_wide_kernel(I8Args p) {
     int id = blockIdx.x;
     if (id < upto) {
         const Wide wide(p, lds);
-        Wide::Tile t;
+        Wide::Tile t = {};
         auto find = [&](int n) {
             int tm = 0, tn = 0;
             list.find(n < whole ? xcd_run(n, whole) : whole + xcd_run(n - whole, rest), t.g, t.lo, t.rows, tm, tn);

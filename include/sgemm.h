@@ -536,7 +536,8 @@ int sgemm_w4_dequantize(int dtype, int N, int K,
  *
  * sgemm_i8_grouped: the same for rows offsets[g] .. offsets[g+1] - 1 of X and of
  * C with the weight at W + g*stride_w and scales at w_scales + g*stride_s;
- * offsets, groups and rows of no group as in sgemm_lowp_grouped().
+ * offsets and rows of no group as in sgemm_lowp_grouped(), groups up to 65534,
+ * N below 2^22 - 64.
  */
 int sgemm_i8(int M, int N, int K, float alpha,
              const void *X, int ldx, const float *x_scales,

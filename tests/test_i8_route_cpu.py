@@ -30,7 +30,7 @@ REFUSED = [
         (SMALL, dict(X=MIS)), (SMALL, dict(W=AL + 8)), (SMALL, dict(ldx=65)), (SMALL, dict(ldw=72)),
         (SMALL, dict(ldx=65, workspace=AL, workspace_bytes=17 * 64 - 1)), (SMALL, dict(X=MIS, workspace=MIS, workspace_bytes=1 << 30))]),
     (capi.sgemm_i8_grouped, GROUPED, [
-        (TYPE, dict(dtype_c=4)), (DIM, dict(groups=-1)), (DIM, dict(groups=65536)), (DIM, dict(M=-1)), (DIM, dict(N=-1)), (DIM, dict(K=-1)),
+        (TYPE, dict(dtype_c=4)), (DIM, dict(groups=-1)), (DIM, dict(groups=65535)), (DIM, dict(M=-1)), (DIM, dict(N=-1)), (DIM, dict(K=-1)),
         (DIM, dict(ldx=63)), (DIM, dict(ldw=63)), (DIM, dict(ldc=31)), (DIM, dict(stride_w=-1)), (DIM, dict(stride_s=-1)),
         (DIM, dict(K=1 << 17, ldx=1 << 17, ldw=1 << 17)), (DIM, dict(M=2 ** 31 - 1, N=1 << 21, ldc=1 << 21)),
         (DIM, dict(M=60000, groups=60000, N=40000, ldc=40000)),
