@@ -599,7 +599,8 @@ __device__ __forceinline__ int nearest(float x, float s, float inverse) {
 // A row per NT threads, 8 values to a thread and step, PIECES steps of them in
 // registers; longer rows are read again (from the cache).  The largest
 // magnitude is taken as bits: NaN lies above infinity there, and either makes
-// the scale NaN.
+// the scale NaN.  16384 x 4096 in BF16: 45 us, 4.4 TB/s (four steps in registers,
+// which short rows leave empty, 52); back 34 us, 5.8 TB/s.
 template <int DTYPE, int NT>
 __global__ void __launch_bounds__(256) i8_quantize_kernel(QuantArgs p) {
     constexpr int PIECES = 2, ROWS = 256 / NT, E = DTYPE == SGEMM_DTYPE_F32 ? 4 : 2;

