@@ -633,11 +633,12 @@ class I8Matrix(NamedTuple):
 
 def _ld_of(t, name):
     """Leading dimension of (each matrix of) t [..., rows, columns]."""
-    rows, cols = t.shape[-2:]
-    step, unit = t.stride()[-2:]
-    if unit != 1 and cols > 1:
+    shape, steps = t.shape, t.stride()
+    rows, cols, ld = shape[-2], shape[-1], steps[-2]
+    if steps[-1] != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
-    ld = step if rows > 1 or step >= cols > 0 else max(cols, 1)
+    if rows <= 1 and not ld >= cols > 0:
+        ld = max(cols, 1)
     if rows | cols | ld > _INT:
         _too_large(name)
     return ld
@@ -693,6 +694,19 @@ def _check_float_result(C, shape, out_dtype, beta):
         raise ValueError("C must have unit column stride (row-major)")
 
 
+def _launch(product, args, size, operand, likely, h):
+    """product(*args, workspace, its bytes, h), with a workspace of size() bytes
+    if the call asks for one; at once where that is `likely`."""
+    import torch
+    if not likely:
+        status = product(*args, None, 0, h)
+        if status != capi.SGEMM_STATUS_SCRATCH_TOO_SMALL:
+            return _check(status)
+    n = _check(size())
+    ws = operand.new_empty(n, dtype=torch.uint8) if n else None
+    return _check(product(*args, _address(ws), n, h))
+
+
 def sgemm_i8(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     """C = alpha * X @ W.T + beta * C for X [M,K] and W [N,K] in 8-bit
     integers (I8Matrix: a scale for each token and each output channel);
@@ -713,11 +727,8 @@ def sgemm_i8(X, W, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     def call(h):
         out, code_c, ldc = _result(C, (M, N), out_dtype, x)
         args = (M, N, K, float(alpha), *operands, float(beta), out.data_ptr(), ldc, code_c)
-        product = capi.load().sgemm_i8
-        status = product(*args, None, 0, h)
-        if status:
-            _finish(status, lambda ws, size: product(*args, ws, size, h),
-                    lambda: capi.sgemm_i8_workspace(M, N, K, operands[0], ldx, operands[3], ldw), x)
+        _launch(capi.load().sgemm_i8, args, lambda: capi.sgemm_i8_workspace(M, N, K, operands[0], ldx, operands[3], ldw), x,
+                (operands[0] | ldx | operands[3] | ldw) & 15, h)
         return out
     return _run(device, stream, call, x, sx, w, sw, C)
 
@@ -745,11 +756,9 @@ def sgemm_i8_grouped(X, W, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None,
     def call(h):
         out, code_c, ldc = _result(C, (M, N), out_dtype, x)
         args = (groups, M, N, K, float(alpha), *sizes, offsets.data_ptr(), float(beta), out.data_ptr(), ldc, code_c)
-        product = capi.load().sgemm_i8_grouped
-        status = product(*args, None, 0, h)
-        if status:
-            _finish(status, lambda ws, size: product(*args, ws, size, h),
-                    lambda: capi.sgemm_i8_grouped_workspace(groups, M, N, K, sizes[0], ldx, sizes[3], ldw, sizes[5]), x)
+        _launch(capi.load().sgemm_i8_grouped, args,
+                lambda: capi.sgemm_i8_grouped_workspace(groups, M, N, K, sizes[0], ldx, sizes[3], ldw, sizes[5]), x,
+                (sizes[0] | ldx | sizes[3] | ldw | sizes[5]) & 15, h)
         return out
     return _run(device, stream, call, x, sx, w, sw, offsets, C)
 
@@ -761,22 +770,24 @@ def sgemm_i8_quantize(X, stream=None):
     infinity gets a NaN scale (and values 0)."""
     import torch
     code = _float_code(X.dtype, "X")
-    if X.dim() not in (2, 3):
+    shape = X.shape
+    if len(shape) not in (2, 3):
         raise ValueError("X must be 2-D or 3-D")
     ldx = _ld_of(X, "X")
-    M, K = X.shape[-2:]
-    if X.dim() == 3 and X.shape[0] > 1 and X.stride(0) != M * ldx:
-        raise ValueError("the matrices of a 3-D X must follow each other")
-    M = M * X.shape[0] if X.dim() == 3 else M
-    if M > _INT:
-        _too_large("X")
-    device = _one_device(X)
+    M, K = shape[-2], shape[-1]
     ldv = max((K + 15) // 16, 1) * 16
+    strides = (ldv, 1)
+    if len(shape) == 3:
+        if shape[0] > 1 and X.stride(0) != M * ldx:
+            raise ValueError("the matrices of a 3-D X must follow each other")
+        strides = (M * ldv, ldv, 1)
+        M *= shape[0]
+        if M > _INT:
+            _too_large("X")
+    device = _one_device(X)
 
     def call(h):
-        strides = (ldv, 1) if X.dim() == 2 else (X.shape[1] * ldv, ldv, 1)
-        values = X.new_empty_strided(X.shape, strides, dtype=torch.int8)
-        scales = X.new_empty(X.shape[:-1], dtype=torch.float32)
+        values, scales = X.new_empty_strided(shape, strides, dtype=torch.int8), X.new_empty(shape[:-1], dtype=torch.float32)
         _check(capi.load().sgemm_i8_quantize(code, M, K, X.data_ptr(), ldx, values.data_ptr(), ldv, scales.data_ptr(), h))
         return I8Matrix(values, scales)
     return _run(device, stream, call, X)
@@ -875,11 +886,8 @@ def sgemm_grouped_sort(X, experts, groups, stream=None):
         args = (code, T, picks, groups, H, _address(x), ldx, _address(sx), experts.data_ptr(), lde, experts.element_size(),
                 held.data_ptr(), order.position.data_ptr(), order.source.data_ptr(), _address(rows), ldr,
                 _address(row_scales))
-        sort = capi.load().sgemm_grouped_sort
-        status = sort(*args, None, 0, h)
-        if status:
-            _finish(status, lambda ws, size: sort(*args, ws, size, h),
-                    lambda: capi.sgemm_grouped_sort_workspace(T, picks, groups), experts)
+        _launch(capi.load().sgemm_grouped_sort, args, lambda: capi.sgemm_grouped_sort_workspace(T, picks, groups), experts,
+                n > 2048, h)
         return (I8Matrix(rows, row_scales) if scaled else rows), order
     return _run(device, stream, call, experts, x, sx)
 
