@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(T::NT) i8_tile_kernel(I8Args p) {
 // tile of 64 bytes) leaves half as much in flight and fetches every line twice.
 // Here a unit of K is 128 bytes, whole lines of each row (8192 x 14336 x 4096 to
 // BF16: 58 -> 29 million reads of the second-level cache, 445 -> 397 us; with all
-// that follows 373, 2580 TOPS, of which storing 235 MB is about 45).
+// that follows 372, 2590 TOPS, of which storing 235 MB is about 34).
 //
 // Five LDS slots of 32 KiB hold the units of A and of B in turn, A_u in slot 2u
 // mod 5 and B_u in the next.  Eight waves in two groups, one wave of each on a
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(T::NT) i8_tile_kernel(I8Args p) {
 // wait for unit u + 1 is at the end of the last phase before it is read, and
 // leaves A_{u+2} in flight.
 //
-// A lane holds 16 consecutive columns of a row of C (two 16-byte stores in 16
-// bits): the rows of B enter the matrix instruction so that its column j of block
+// A lane holds 16 consecutive columns of a row of C (two pieces of 16 bytes in 16
+// bits, see exchange): the rows of B enter the matrix instruction so that its column j of block
 // nb is the wave's column 16 * (j / 4) + 4 * nb + j % 4.  A chunk c of row r lies
 // at c ^ (r / 2 % 8) in A's slots and at c ^ key_b(r) in B's, whose 16 rows to a
 // read differ in bits 0, 1, 4 and 5: no bank conflicts counted in either.
@@ -303,47 +303,99 @@ struct Wide {
         }
         if (!group) __builtin_amdgcn_s_barrier();
     }
-    // C of a tile.  All loads before it have landed before its first store.
-    __device__ __forceinline__ void store(const Tile &t, const Acc &acc) const {
+    // The scales of a tile's rows (times alpha) and columns, arrived: all loads before them have landed too.
+    struct Scales {
+        float x[8];
+        f32x4 w[4];
+    };
+    __device__ __forceinline__ void load(const Tile &t, Scales &s) const {
+        const int row0 = t.m0 + (wave >> 2) * 128 + (lane & 15), col = t.n0 + (wave & 3) * 64 + 16 * (lane >> 4);
+#pragma unroll
+        for (int mi = 0; mi < 8; ++mi) s.x[mi] = p.sx[t.lo + max(min(row0 + mi * 16, t.rows - 1), 0)];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) s.w[nb] = scales4(p.sw + t.g * p.strideS, col + 4 * nb, p.N);
+#pragma unroll
+        for (int mi = 0; mi < 8; ++mi) {
+            s.x[mi] *= p.alpha;
+            asm volatile("" : "+v"(s.x[mi]));
+        }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) asm volatile("" : "+v"(s.w[nb]));
+    }
+    // C of a tile.
+    __device__ __forceinline__ void store(const Tile &t, const Acc &acc, const Scales &s) const {
         int l = threadIdx.x & 63;
         asm volatile("" : "+v"(l));         // (what follows from it is not kept in registers from tile to tile)
-        const int row0 = t.m0 + (wave >> 2) * 128 + (l & 15), col = t.n0 + (wave & 3) * 64 + 16 * (l >> 4);
-        float sx[8];
-        f32x4 sw[4];
-#pragma unroll
-        for (int mi = 0; mi < 8; ++mi) sx[mi] = p.alpha * p.sx[t.lo + max(min(row0 + mi * 16, t.rows - 1), 0)];
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) sw[nb] = scales4(p.sw + t.g * p.strideS, col + 4 * nb, p.N);
-        wait_vmcnt0();
+        const bool low = (l & 15) < 8;
+        const int row0 = t.m0 + (wave >> 2) * 128, n0 = t.n0 + (wave & 3) * 64, col = n0 + 16 * (l >> 4);
         by_result(p.dtype_c, [&](auto f16, auto out16) {
             constexpr bool F16 = decltype(f16)::value, OUT16 = decltype(out16)::value;
+            auto value = [&](int mi, int nb) { return to_float(acc[mi][nb]) * s.x[mi] * s.w[nb]; };
+            auto at = [&](int row) { return p.C + (t.lo + (long)row) * p.ldc * (OUT16 ? 2 : 4); };
+            if (OUT16 && p.beta == 0.f && t.n0 + 256 <= p.N) {
+                i32x4 o[8][2];              // all values, then all stores
+#pragma unroll
+                for (int mi = 0; mi < 8; ++mi) {
+                    __builtin_amdgcn_sched_barrier(0);  // (eight rows at once need more registers than there are)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const i32x2 x = round16<F16>(value(mi, 2 * h)), y = round16<F16>(value(mi, 2 * h + 1));
+                        o[mi][h] = i32x4{x[0], x[1], y[0], y[1]};
+                    }
+                }
+                wait_vmcnt0();
+#pragma unroll
+                for (int mi = 0; mi < 8; ++mi) {
+                    exchange(o[mi][0], o[mi][1], low);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = row0 + mi * 16 + 8 * h + (l & 7);
+                        if (row < t.rows) __builtin_memcpy(at(row) + 2l * (col + (low ? 0 : 8)), &o[mi][h], 16);
+                    }
+                }
+                return;
+            }
+            wait_vmcnt0();
 #pragma unroll
             for (int mi = 0; mi < 8; ++mi) {
-                __builtin_amdgcn_sched_barrier(0);      // (eight rows at once need more registers than there are)
-                const int row = row0 + mi * 16;
-                char *at = p.C + (t.lo + (long)row) * p.ldc * (OUT16 ? 2 : 4);
+                __builtin_amdgcn_sched_barrier(0);
                 f32x4 v[4];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) v[nb] = to_float(acc[mi][nb]) * sx[mi] * sw[nb];
-                if constexpr (!OUT16) turn(v);
-                if (row >= t.rows) continue;
-                if (OUT16 && p.beta == 0.f && col + 16 <= p.N) {
+                for (int nb = 0; nb < 4; ++nb) v[nb] = value(mi, nb);
+                if constexpr (OUT16) {
+                    const int row = row0 + mi * 16 + (l & 15);
+                    if (row >= t.rows) continue;
 #pragma unroll
-                    for (int h = 0; h < 4; h += 2) {
-                        const i32x2 x = round16<F16>(v[h]), y = round16<F16>(v[h + 1]);
-                        const i32x4 o = {x[0], x[1], y[0], y[1]};
-                        __builtin_memcpy(at + 2l * (col + 4 * h), &o, 16);
+                    for (int nb = 0; nb < 4; ++nb) store4<F16, OUT16>(at(row), col + 4 * nb, p.N, p.beta, v[nb]);
+                } else {
+                    turn(v);
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) exchange(v[i], v[i + 1], low);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = row0 + mi * 16 + 8 * (i & 1) + (l & 7);
+                        if (row >= t.rows) continue;
+                        const int c = n0 + 4 * (l >> 4) + 16 * (i & ~1) + (low ? 0 : 16);
+                        store4<F16, OUT16>(at(row), c, p.N, p.beta, v[i]);
                     }
-                } else if (OUT16) {
-#pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) store4<F16, OUT16>(at, col + 4 * nb, p.N, p.beta, v[nb]);
-                } else {                    // the four lanes of a row side by side in every store
-                    const int first = t.n0 + (wave & 3) * 64 + 4 * (l >> 4);
-#pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) store4<F16, OUT16>(at, first + 16 * nb, p.N, p.beta, v[nb]);
                 }
             }
         });
+    }
+    // The lanes of rows r (low) and r + 8 hold the pieces a and b of theirs: a becomes row r's and b row r + 8's,
+    // the first piece in the low lane and the second in the other.  A wave's store then writes whole lines of
+    // 128 bytes of eight rows, not halves of sixteen (8192 x 8192 x 2048 in 136 -> 132.5 us, 4096^3 in 60 -> 57.5).
+    template <class V> static __device__ __forceinline__ void exchange(V &a, V &b, bool low) {
+        i32x4 x = __builtin_bit_cast(i32x4, a), y = __builtin_bit_cast(i32x4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int other = __builtin_amdgcn_mov_dpp(low ? y[i] : x[i], 0x128, 0xf, 0xf, true);   // (8 lanes on)
+            const int first = low ? x[i] : other, second = low ? other : y[i];
+            x[i] = first;
+            y[i] = second;
+        }
+        a = __builtin_bit_cast(V, x);
+        b = __builtin_bit_cast(V, y);
     }
     // Lane group l/16 = j gets of lane group i (block j) as its block i.
     static __device__ __forceinline__ void turn(f32x4 (&v)[4]) {
@@ -409,7 +461,9 @@ __global__ void __launch_bounds__(Wide::NT) i8_wide_kernel(I8Args p) {
                 find(id);
                 wide.begin(t);
             }
-            wide.store(done, acc);
+            Wide::Scales s;
+            wide.load(done, s);
+            wide.store(done, acc, s);
             if (id >= upto) break;
         }
     }
