@@ -487,6 +487,7 @@ int sgemm_grouped_sort(int dtype, int T, int picks, int groups, int H, const voi
     if (offsets == nullptr || (n > 0 && (experts == nullptr || position == nullptr || source == nullptr))) return SGEMM_STATUS_NULL_POINTER;
     if (rows != nullptr && n > 0 && ((H > 0 && X == nullptr) || (dtype == SGEMM_DTYPE_I8 && (x_scales == nullptr || row_scales == nullptr))))
         return SGEMM_STATUS_NULL_POINTER;
+    if (n == 0) rows = nullptr;             // (no row to copy, and X may be NULL)
     const long long need = sgemm_grouped_sort_workspace(T, picks, groups);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -93,6 +93,16 @@ def test_order_of_views_and_empty():
         assert dy.shape == (2 * T, 0) and (dw == 0).all()
 
 
+def test_no_assignments_and_no_rows():
+    """Where there is no row to copy, X is not read."""
+    torch = torch_cuda()
+    offsets, rows = torch.full((4,), 7, dtype=torch.int32, device="cuda"), torch.full((16,), 3.0, device="cuda")
+    st = lib.capi.sgemm_grouped_sort(lib.capi.SGEMM_DTYPE_F32, 5, 0, 3, 16, None, 16, None, None, 0, 4, offsets.data_ptr(), None, None,
+                                     rows.data_ptr(), 16, None, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == lib.capi.SGEMM_STATUS_OK
+    assert offsets.tolist() == [0] * 4 and (rows == 3).all()
+
+
 # widths of one element to many pieces, whole and odd
 WIDTHS = [1, 8, 63, 64, 127, 128, 513, 1024, 2047, 4100]
 
