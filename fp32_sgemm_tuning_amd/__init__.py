@@ -778,7 +778,7 @@ def sgemm_i8_quantize(X, stream=None):
     ldv = max((K + 15) // 16, 1) * 16
     strides = (ldv, 1)
     if len(shape) == 3:
-        if shape[0] > 1 and X.stride(0) != M * ldx:
+        if shape[0] > 1 and X.numel() and X.stride(0) != M * ldx:
             raise ValueError("the matrices of a 3-D X must follow each other")
         strides = (M * ldv, ldv, 1)
         M *= shape[0]
@@ -804,7 +804,7 @@ def sgemm_i8_dequantize(Q, dtype=None, stream=None):
         raise ValueError("Q must be 2-D or 3-D")
     M, K, ldv = _i8(Q, "Q", values.dim())
     if values.dim() == 3:
-        if values.shape[0] > 1 and (values.stride(0) != M * ldv or scales.stride(0) != M):
+        if values.shape[0] > 1 and values.numel() and (values.stride(0) != M * ldv or scales.stride(0) != M):
             raise ValueError("the matrices of a 3-D Q must follow each other")
         M *= values.shape[0]
         if M > _INT:

@@ -287,6 +287,14 @@ def test_matrices_of_groups():
         lib.sgemm_i8_quantize(torch.zeros(4, 20, 45, device="cuda")[:, :10])
 
 
+@pytest.mark.parametrize("shape", [(3, 0, 8), (3, 5, 0), (3, 1, 0), (0, 5, 8), (3, 0, 0)])
+def test_empty_matrices_of_groups(shape):
+    torch = torch_cuda()
+    W = lib.sgemm_i8_quantize(torch.empty(shape, device="cuda"))
+    assert W.values.shape == shape and torch.equal(W.scales, torch.full(shape[:2], 2.0 ** -126, device="cuda"))
+    assert lib.sgemm_i8_dequantize(W).shape == shape
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_quantised_product_of_float_rows(M):
     """Quantise, multiply: off from the product of the floats by what the
