@@ -933,10 +933,11 @@ bool workspace_ok(long need, const void *workspace, long long bytes) {
 
 constexpr int kShortRow = 256, kWaveRow = 1024;    // longest rows that 16 lanes and a wave quantise (in registers; a workgroup holds 4096)
 constexpr int kMaxRows8 = 1 << 24;          // launch grid extents
+constexpr int kMaxRowQ = 1 << 30;           // (a row's last step stays in 32 bits)
 
 int check_quant(int dtype, int M, int K, int ldv, int ldx) {
     if (!dtype_ok(dtype)) return SGEMM_STATUS_INVALID_DTYPE;
-    return M < 0 || K < 0 || ldx < std::max(K, 1) || ldv < std::max(K, 1) ? SGEMM_STATUS_INVALID_DIM : SGEMM_STATUS_OK;
+    return M < 0 || K < 0 || K > kMaxRowQ || ldx < std::max(K, 1) || ldv < std::max(K, 1) ? SGEMM_STATUS_INVALID_DIM : SGEMM_STATUS_OK;
 }
 
 }  // namespace

@@ -559,7 +559,8 @@ long long sgemm_i8_grouped_workspace(int groups, int M, int N, int K, const void
  * scale for each row, s = max(max|x| / 127, 2^-126) in FP32 and
  * values = x / s rounded to the nearest integer, halves to even (-127 .. 127).  A
  * row that holds a NaN or an infinity gets s NaN and values 0, so that what is
- * made of it is NaN.  sgemm_i8_dequantize: X = values * s, rounded to `dtype`.
+ * made of it is NaN.  sgemm_i8_dequantize: X = values * s, rounded to `dtype`.  K
+ * up to 2^30.
  */
 int sgemm_i8_quantize(int dtype, int M, int K, const void *X, int ldx,
                       void *values, int ldv, float *scales, void *stream);

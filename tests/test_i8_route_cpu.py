@@ -39,10 +39,11 @@ REFUSED = [
         (SMALL, dict(ldw=65, stride_w=2080, workspace=AL, workspace_bytes=2 * 32 * 64 - 1))]),
     (capi.sgemm_i8_quantize, QUANT, [
         (TYPE, dict(dtype=0)), (TYPE, dict(dtype=4)), (DIM, dict(M=-1)), (DIM, dict(K=-1)), (DIM, dict(ldx=39)), (DIM, dict(ldv=39)),
-        (DIM, dict(M=1 << 24, K=2000, ldx=2000, ldv=2000)), (DIM, dict(M=1 << 28)), (NULL, dict(X=None)), (NULL, dict(values=None)), (NULL, dict(scales=None))]),
+        (DIM, dict(M=1 << 24, K=2000, ldx=2000, ldv=2000)), (DIM, dict(M=1 << 28)),
+        (DIM, dict(K=(1 << 30) + 1, ldx=2 ** 31 - 1, ldv=2 ** 31 - 1)), (NULL, dict(X=None)), (NULL, dict(values=None)), (NULL, dict(scales=None))]),
     (capi.sgemm_i8_dequantize, DEQUANT, [
-        (TYPE, dict(dtype=4)), (DIM, dict(M=-1)), (DIM, dict(K=-1)), (DIM, dict(ldx=39)), (DIM, dict(ldv=39)), (NULL, dict(X=None)),
-        (NULL, dict(values=None)), (NULL, dict(scales=None))]),
+        (TYPE, dict(dtype=4)), (DIM, dict(M=-1)), (DIM, dict(K=-1)), (DIM, dict(ldx=39)), (DIM, dict(ldv=39)),
+        (DIM, dict(K=(1 << 30) + 1, ldx=2 ** 31 - 1, ldv=2 ** 31 - 1)), (NULL, dict(X=None)), (NULL, dict(values=None)), (NULL, dict(scales=None))]),
     (capi.sgemm_grouped_sort, SORT, [
         (TYPE, dict(dtype=0)), (TYPE, dict(dtype=5)), (TYPE, dict(expert_bytes=2)), (DIM, dict(T=-1)), (DIM, dict(picks=-1, lde=2)), (DIM, dict(groups=-1)),
         (DIM, dict(groups=4097)), (DIM, dict(H=-1)), (DIM, dict(ldx=15)), (DIM, dict(ldr=15)), (DIM, dict(lde=1)), (DIM, dict(T=1 << 30)),
