@@ -638,14 +638,15 @@ __device__ __forceinline__ void load8(const char *row, int k, int K, float (&v)[
 // within 2^-16 of the quotient (two roundings of a value of 128 at most), so its
 // rounding is right unless it lies that near to a half; then the remainder
 // x - q * s, which FP32 holds exactly (a multiple of s's last bit or of x's,
-// below 2^24 of them), is compared with half a step.
+// below 2^24 of them), is doubled and compared with a step.  (Not halved steps:
+// half of an odd multiple of 2^-149, which an s below 2^-125 can be, is no FP32
+// value.)
 __device__ __forceinline__ int nearest(float x, float s, float inverse) {
     const float y = x * inverse;
     float q = rintf(y);
     if (fabsf(fabsf(y - q) - 0.5f) < 0x1p-12f) {
-        const float rest = __builtin_fmaf(-q, s, x), half = 0.5f * s;
-        if (fabsf(rest) > half) q += rest > 0.f ? 1.f : -1.f;
-        else if (fabsf(rest) == half && ((int)q & 1)) q += rest > 0.f ? 1.f : -1.f;
+        const float rest = __builtin_fmaf(-q, s, x), twice = 2.f * fabsf(rest);
+        if (twice > s || (twice == s && ((int)q & 1))) q += rest > 0.f ? 1.f : -1.f;
     }
     return (int)q;
 }
