@@ -637,10 +637,24 @@ def _ld_of(t, name):
     rows, cols, ld = shape[-2], shape[-1], steps[-2]
     if steps[-1] != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
-    if rows <= 1 and not ld >= cols > 0:
+    if rows <= 1 and not _INT >= ld >= cols > 0:
         ld = max(cols, 1)
     if rows | cols | ld > _INT:
         _too_large(name)
+    return ld
+
+
+def _stacked_ld(t, ld, name):
+    """Leading dimension of all rows of t [G,rows,columns] taken as one matrix; ld: that of each of its matrices."""
+    shape, step = t.shape, t.stride(0)
+    if shape[0] <= 1 or t.numel() == 0:
+        return ld
+    if shape[1] == 1:                       # (rows `step` apart, the second dimension's step not being used)
+        ld = step
+        if ld > _INT:
+            _too_large(name)
+    elif step != shape[1] * ld:
+        raise ValueError(f"the matrices of a 3-D {name} must follow each other")
     return ld
 
 
@@ -663,7 +677,7 @@ def _i8(Q, name, dims):
     if rows > 1:
         if scales.stride(-1) != 1:
             raise ValueError(f"{name}'s scales must be contiguous")
-    elif not ld >= K > 0:
+    elif not _INT >= ld >= K > 0:
         ld = max(K, 1)
     if rows | K | ld > _INT:
         _too_large(name)
@@ -767,7 +781,8 @@ def sgemm_i8_quantize(X, stream=None):
     """X [M,K] or [G,M,K] (bfloat16, float16 or float32) as an I8Matrix: for
     each row a scale max(max|x| / 127, 2^-126) and the values x / scale rounded
     to the nearest integer, halves to even.  A row that holds a NaN or an
-    infinity gets a NaN scale (and values 0)."""
+    infinity gets a NaN scale (and values 0).  The matrices of a 3-D X
+    follow each other (all rows at one distance)."""
     import torch
     code = _float_code(X.dtype, "X")
     shape = X.shape
@@ -778,8 +793,7 @@ def sgemm_i8_quantize(X, stream=None):
     ldv = max((K + 15) // 16, 1) * 16
     strides = (ldv, 1)
     if len(shape) == 3:
-        if shape[0] > 1 and X.numel() and X.stride(0) != M * ldx:
-            raise ValueError("the matrices of a 3-D X must follow each other")
+        ldx = _stacked_ld(X, ldx, "X")
         strides = (M * ldv, ldv, 1)
         M *= shape[0]
         if M > _INT:
@@ -804,8 +818,9 @@ def sgemm_i8_dequantize(Q, dtype=None, stream=None):
         raise ValueError("Q must be 2-D or 3-D")
     M, K, ldv = _i8(Q, "Q", values.dim())
     if values.dim() == 3:
-        if values.shape[0] > 1 and values.numel() and (values.stride(0) != M * ldv or scales.stride(0) != M):
-            raise ValueError("the matrices of a 3-D Q must follow each other")
+        ldv = _stacked_ld(values, ldv, "Q")
+        if values.shape[0] > 1 and values.numel() and scales.stride(0) != M:
+            raise ValueError("the scales of a 3-D Q must follow each other")
         M *= values.shape[0]
         if M > _INT:
             _too_large("Q")

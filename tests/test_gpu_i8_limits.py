@@ -33,3 +33,24 @@ def test_quantize_with_scales_next_to_the_smallest(t):
     assert torch.equal(got.scales.cpu(), s)
     want = [[round(Fraction(v) / Fraction(d)) for v in row] for row, d in zip(x.tolist(), s.tolist())]
     assert torch.equal(got.values.cpu().long(), torch.tensor(want))
+
+
+def test_matrices_of_groups_of_one_row():
+    """A group's only row has no row step of its own: rows at equal distances
+    are taken as they lie, whatever step their tensor names for that dimension."""
+    torch = torch_cuda()
+    w = torch.randn(5, 3, 45, generator=torch.Generator().manual_seed(1)).cuda()
+    flat = w.view(1, 15, 45).transpose(0, 1)                # [15,1,45], row step 15 * 45
+    far = w[:, 1:2]                                         # [5,1,45], 3 * 45 from row to row
+    for x in (flat, far, far.clone(), w[:1, :1], w[:0, :1]):
+        want = lib.sgemm_i8_quantize(x.reshape(-1, 45))
+        got = lib.sgemm_i8_quantize(x)
+        assert got.values.shape == x.shape and torch.equal(got.values.view(-1, 45), want.values)
+        assert torch.equal(got.scales.view(-1), want.scales)
+        # the same 8-bit rows, laid out as x is
+        held = torch.zeros(5, 3, 45, dtype=torch.int8, device="cuda").as_strided(x.shape, x.stride())
+        held.copy_(got.values)
+        assert torch.equal(lib.sgemm_i8_dequantize(lib.I8Matrix(held, got.scales)).view(-1, 45), lib.sgemm_i8_dequantize(want))
+    for x in (w[:, :1, ::2], w[:1, :1].expand(4, 1, 45)):   # columns apart; rows on one another
+        with pytest.raises((ValueError, lib.SgemmError)):
+            lib.sgemm_i8_quantize(x)
