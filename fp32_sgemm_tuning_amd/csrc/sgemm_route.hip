@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) sort_few_kernel(SortArgs p) {
             places[i] = place;
         }
     }
-    if (p.rows == nullptr) return;
+    if (p.rows == nullptr && p.row_scales == nullptr) return;
     __syncthreads();
     const int per = 256 / p.lanes;
     for (int t = first + threadIdx.x / p.lanes; t < last; t += per)
@@ -485,9 +485,11 @@ int sgemm_grouped_sort(int dtype, int T, int picks, int groups, int H, const voi
     if (rows != nullptr && (ldx < std::max(H, 1) || ldr < std::max(H, 1))) return SGEMM_STATUS_INVALID_DIM;
     const int n = T * picks, size = size_of(dtype);
     if (offsets == nullptr || (n > 0 && (experts == nullptr || position == nullptr || source == nullptr))) return SGEMM_STATUS_NULL_POINTER;
-    if (rows != nullptr && n > 0 && ((H > 0 && X == nullptr) || (dtype == SGEMM_DTYPE_I8 && (x_scales == nullptr || row_scales == nullptr))))
+    // (rows of no columns have scales to bring, and no address)
+    const bool copies = n > 0 && (rows != nullptr || (dtype == SGEMM_DTYPE_I8 && H == 0 && row_scales != nullptr));
+    if (copies && ((H > 0 && X == nullptr) || (dtype == SGEMM_DTYPE_I8 && (x_scales == nullptr || row_scales == nullptr))))
         return SGEMM_STATUS_NULL_POINTER;
-    if (n == 0) rows = nullptr;             // (no row to copy, and X may be NULL)
+    if (!copies) rows = nullptr, row_scales = nullptr;      // (X may be NULL)
     const long long need = sgemm_grouped_sort_workspace(T, picks, groups);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_STATUS_SCRATCH_TOO_SMALL;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -504,7 +506,7 @@ int sgemm_grouped_sort(int dtype, int T, int picks, int groups, int H, const voi
     if (e == hipSuccess)
         e = groups + 1 <= 2048 ? launch_k(sort_place_kernel<16, 2048>, dim3((unsigned)blocks), dim3(1024), s, p)
                                : launch_k(sort_place_kernel<4, kMaxBins>, dim3((unsigned)blocks), dim3(256), s, p);
-    if (e == hipSuccess && rows != nullptr) e = launch_k(sort_copy_kernel, dim3(token_blocks(T, p.lanes)), dim3(256), s, p);
+    if (e == hipSuccess && copies) e = launch_k(sort_copy_kernel, dim3(token_blocks(T, p.lanes)), dim3(256), s, p);
     return e == hipSuccess ? SGEMM_STATUS_OK : hip_status(e, "kernel launch");
 }
 

@@ -580,8 +580,9 @@ int sgemm_i8_dequantize(int dtype, int M, int K, const void *values, int ldv, co
  *   rows      [n,H]         row position[t][j] is X[t]; zeros behind
  *                           offsets[groups].  NULL: not wanted
  * X [T,H] of BF16, FP16, FP32 or SGEMM_DTYPE_I8; with the last x_scales [T] are
- * brought to row_scales [n] in the same way.  groups up to 4096, n below
- * 2^31 - 1, H up to 2^28.  The gradient with respect to X is
+ * brought to row_scales [n] in the same way (not where rows is NULL, but if H is
+ * 0: rows of no columns have no address).  groups up to 4096, n below 2^31 - 1,
+ * H up to 2^28.  The gradient with respect to X is
  * sgemm_grouped_combine() without weights.
  *
  * sgemm_grouped_combine: the way back,

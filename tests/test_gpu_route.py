@@ -333,3 +333,25 @@ def test_refusals():
     for bad in (dict(Y=rows.half(), out_dtype=torch.bfloat16), dict(Y=rows.double()), dict(weights=w.double()), dict(order=order._replace(offsets=order.offsets.long()))):
         with pytest.raises(TypeError):
             lib.sgemm_grouped_combine(**{**dict(Y=rows, order=order, weights=w), **bad})
+
+
+@pytest.mark.parametrize("T", [5, 3000])
+def test_scales_of_rows_without_columns(T):
+    """8-bit rows of no columns have scales, which are brought to their places too."""
+    torch = torch_cuda()
+    picks, groups = 2, 3
+    e = experts_of(torch, T, picks, groups, 1)
+    x = lib.I8Matrix(torch.zeros(T, 0, dtype=torch.int8, device="cuda"), torch.arange(1.0, T + 1, device="cuda"))
+    rows, order = lib.sgemm_grouped_sort(x, e, groups)
+    offsets, _, source = check_order(torch, order, e, groups)
+    kept = int(offsets[-1])
+    want = torch.zeros(T * picks, device="cuda")
+    want[:kept] = x.scales[(source[:kept] // picks).cuda()]
+    assert rows.values.shape == (T * picks, 0) and torch.equal(rows.scales, want)
+    held = torch.full((T * picks,), float("nan"), device="cuda")
+    offsets, position, source = (torch.zeros_like(o) for o in order)
+    ws = torch.empty(max(lib.capi.sgemm_grouped_sort_workspace(T, picks, groups), 16), dtype=torch.uint8, device="cuda")
+    st = lib.capi.sgemm_grouped_sort(lib.capi.SGEMM_DTYPE_I8, T, picks, groups, 0, None, 1, x.scales.data_ptr(), e.data_ptr(), picks,
+                                     e.element_size(), offsets.data_ptr(), position.data_ptr(), source.data_ptr(), None, 1, held.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == lib.capi.SGEMM_STATUS_OK and torch.equal(held, want)

@@ -177,3 +177,9 @@ def test_first_call_of_a_process(monkeypatch):
     assert lib._result(None, (2, 3), None, torch.zeros(1))[1:] == (capi.SGEMM_DTYPE_F32, 3)
     monkeypatch.setattr(lib, "_CODES", {})
     assert lib._result(torch.zeros(2, 3, dtype=torch.bfloat16), (2, 3), None, None)[1:] == (capi.SGEMM_DTYPE_BF16, 3)
+
+
+def test_scales_of_rows_without_columns_need_their_source():
+    """Rows of no columns may be NULL; their scales, if wanted, are still read from somewhere."""
+    args = dict(SORT, dtype=4, H=0, X=None, rows=None, row_scales=AL)
+    assert capi.sgemm_grouped_sort(**args) == NULL
