@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(T::NT) i8_tile_kernel(I8Args p) {
 // tile of 64 bytes) leaves half as much in flight and fetches every line twice.
 // Here a unit of K is 128 bytes, whole lines of each row (8192 x 14336 x 4096 to
 // BF16: 58 -> 29 million reads of the second-level cache, 445 -> 397 us; with all
-// that follows 372, 2590 TOPS, of which storing 235 MB is about 34).
+// that follows 364 to 390 by card and run, mostly 377, 2550 TOPS, of which storing
+// 235 MB is about 34).
 //
 // Five LDS slots of 32 KiB hold the units of A and of B in turn, A_u in slot 2u
 // mod 5 and B_u in the next.  Eight waves in two groups, one wave of each on a
@@ -547,10 +548,12 @@ __device__ __forceinline__ i32x4 row_chunk(const char *at, int left) {
 // and nothing passes through LDS but the sums at the end.  A lane's 16 bytes of a
 // row are its operand of one v_mfma_i32_16x16x64_i8 as they lie in memory; two
 // steps read a row's 128-byte line, and four lines of every row are in flight.
-// 1 x 4096 x 4096: 5.7 us, where tiles of 32 x 32 take 7.2; from two blocks per
-// compute unit on those are faster (16 x 8192 x 4096: 11.3 and 9.5).  ANY: rows of
-// any alignment, which the tiles would have to copy first (8 x 4096 x 4095 18.1 ->
-// 12.8 us, 16 x 14336 x 4095 41.4 -> 40.2).
+// 1 x 4096 x 4096: 6.3 us, where tiles of 32 x 32 take 8.1; from two blocks per
+// compute unit on those are faster for many rows (16 x 8192 x 4096: 13.1 and 10.5; not
+// for one, 9.3 and 10.3; 1 x 14336 x 4096: 15.0 and 15.7).  ANY: rows of any
+// alignment, which the tiles would have to copy first (8 x 4096 x 4095 18.1 -> 12.8
+// us, 16 x 14336 x 4095 41.4 -> 40.2), slower all the same than aligned ones (8.7 and
+// 15.9): two loads for 16 bytes.
 template <bool ANY>
 __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args p) {
     constexpr int NW = 8, AHEAD = 4;
@@ -654,8 +657,8 @@ __device__ __forceinline__ int nearest(float x, float s, float inverse) {
 // A row per NT threads, 8 values to a thread and step, PIECES steps of them in
 // registers; longer rows are read again (from the cache).  The largest
 // magnitude is taken as bits: NaN lies above infinity there, and either makes
-// the scale NaN.  16384 x 4096 in BF16: 45 us, 4.4 TB/s (four steps in registers,
-// which short rows leave empty, 52); back 34 us, 5.8 TB/s.
+// the scale NaN.  16384 x 4096 in BF16: 45 to 48 us, 4.3 TB/s (four steps in
+// registers, which short rows leave empty, 52); back 34 us, 5.8 TB/s.
 template <int DTYPE, int NT>
 __global__ void __launch_bounds__(256) i8_quantize_kernel(QuantArgs p) {
     constexpr int PIECES = 2, ROWS = 256 / NT, E = DTYPE == SGEMM_DTYPE_F32 ? 4 : 2;
@@ -754,14 +757,19 @@ hipError_t by_dtype(int dtype, F &&f) {
 
 // The forms of one weight's product.  Each but the first is priced as
 //   3.5 us + rounds over the compute units * K / 128 * its time for 128 k of a tile,
-// and the cheapest taken.  Those times (the tile alone on its compute unit, and
-// two of them at once where LDS has room) are from shapes that fill one round or
-// more at K = 4096, BF16 results, in us:
-//   32 x 32     64 x 4096     7.8    64 x 64    200 x 4096  10.6,  256 x 8192  22.8
-//   128 x 64   512 x 4096    15.0    256 x 256, whole rounds: 4096 x 4096  58;
-//   in halves 1024 x 8192    40      in quarters  1024 x 4096  22.5
-// (64 x 64 at the last two takes 67 and 30, 128 x 64 56 and 25).  A grid of 64 x 64
-// tiles that leaves most of the chip idle splits K: 100 x 1000 x 8192 15.3 -> 10.3.
+// and the cheapest taken.  Those times lie at or between those of weights that stay
+// in the caches and those of weights that come from memory.  At K = 4096, BF16
+// results, in us: priced (measured from the caches, from memory)
+//   32 x 32      64 x 4096   7.8 (7.4, 10.2)     two at once   64 x 8192  10.2 (9.9, 14.8)
+//   64 x 64     200 x 4096  10.5 (9.8, 13.8)     two at once  256 x 8192  22.1 (16.8, 23.0)
+//   128 x 64    512 x 4096  17.3 (14.9, 19.4)
+//   256 x 256, whole rounds: 4096 x 4096  56.3 (56.8, 61.8);
+//   in halves 1024 x 8192   39.7 (38.6, 39.9);   in quarters 1024 x 4096  22.7 (22.4, 25.5)
+// From memory the form taken is the fastest within 3% at 64 to 1024 rows of 4096 x
+// 4096, 8192 x 4096 and 2048 x 8192; not at 1 x 8192 x 4096 (32 x 32: 10.3, the rows'
+// kernel 9.3) and 100 x 1000 x 8192 (eight shares 12.6, 32 x 32 11.8).  A grid of 64 x
+// 64 tiles that leaves most of the chip idle splits K: 100 x 1000 x 8192 14.7 -> 9.8
+// from the caches, 21.1 -> 12.6 from memory.
 enum Form { kRows, kTile32, kTile64, kTile128x64, kWide };
 
 struct Plan {
@@ -835,9 +843,16 @@ bool dense_fits(Plan plan, int M, int N) {
     }
 }
 
-// By the rows of an average group.  In us: 512 rows in 16 groups of 2048 x 4096
-// 33 on tiles of 32 x 64, 39 on 64 x 64; 1024 rows 43 and on 64 x 128 40; 4096 rows
-// 75 on 64 x 128, 60 on 256 x 256.
+// By the rows of an average group.  In us, 16 groups of 2048 x 4096 with weights from
+// memory:
+//   rows     128    512   1024   1536   2048   2560   4096
+//   32 x 64   33.4   37.2  47.9   55.3   65.2   76.5  108
+//   64 x 128  35.6   37.2  41.2   41.7   53.2   55.3   75.4
+//   256 x 256 36.1   38.5  40.1   42.0   43.7   45.8   58.9
+// (2048 rows: groups of 112 to 148, for which the rule takes 64 x 128.)  Few groups, or
+// few columns, leave most of the chip idle, which the rule does not look at: 520 rows in
+// 2 groups of 1024 x 4096 18.4 on 256 x 256, 10.8 on 64 x 64; 200 rows by one weight of
+// 64 x 4096 17.1 and 10.4, on 32 x 64 9.1.
 hipError_t launch_grouped(const I8Args &p, hipStream_t s) {
     const int rows = p.M / std::min(p.groups, p.M);
     return rows <= 32 ? launch_tiles<Tile32x64>(p, s) : rows <= 128 ? launch_tiles<Tile64x128>(p, s) : launch_wide(p, s);

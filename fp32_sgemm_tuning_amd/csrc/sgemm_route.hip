@@ -316,7 +316,9 @@ __device__ __forceinline__ void store8(char *base, long row, long ld, int c, int
 
 // A piece of a token's row per `lanes` lanes and turn, with PICKS rows of Y in
 // flight.  8192 x 8 rows of 4096 in BF16 122 us, 4.9 TB/s (with four rows in flight
-// and a token's pieces one after another 141; 512 x 8 rows of 7168 23 and 34).
+// and a token's pieces one after another 141; 512 x 8 rows of 7168 23 and 34).  The
+// grid is sized by the tokens: where those are few their pieces follow one another
+// (16 x 8 rows of 7168 12 us).
 template <int YT, int OT>
 __global__ void __launch_bounds__(256) combine_kernel(CombineArgs p) {
     constexpr int PICKS = YT == kF32Row ? 4 : 8;

@@ -530,14 +530,16 @@ int sgemm_w4_dequantize(int dtype, int N, int K,
  * scaled in FP32, (sum * (alpha * x_scales[m])) * w_scales[n], so a result is
  * the same however K is split.  Operands whose rows do not start at multiples of
  * 16 bytes (pointer and leading dimension) are first copied into the workspace
- * (but not for M up to 16), which also takes the sums of a split K.  An aligned operand is read in whole
- * 16-byte chunks, up to 15 bytes behind the last k of a row; what they
- * hold is not used.  M up to 2^24, N up to 2^30.
+ * (but not for M up to 16 and N up to 2^27 - 16), which also takes the sums of a split
+ * K.  An aligned operand is read in whole 16-byte chunks, up to 15 bytes behind the
+ * last k of a row; what they hold is not used.  M up to 2^24, N up to 2^30.
  *
  * sgemm_i8_grouped: the same for rows offsets[g] .. offsets[g+1] - 1 of X and of
  * C with the weight at W + g*stride_w and scales at w_scales + g*stride_s;
  * offsets and rows of no group as in sgemm_lowp_grouped(), groups up to 65534,
- * N below 2^22 - 64.
+ * N below 2^22 - 64.  Weights whose rows do not start at multiples of 16 bytes are
+ * copied in every call whatever M is, those of empty groups too: lay them out in such
+ * rows once.
  */
 int sgemm_i8(int M, int N, int K, float alpha,
              const void *X, int ldx, const float *x_scales,
@@ -560,7 +562,8 @@ long long sgemm_i8_grouped_workspace(int groups, int M, int N, int K, const void
  * values = x / s rounded to the nearest integer, halves to even (-127 .. 127).  A
  * row that holds a NaN or an infinity gets s NaN and values 0, so that what is
  * made of it is NaN.  sgemm_i8_dequantize: X = values * s, rounded to `dtype`.  K
- * up to 2^30.
+ * up to 2^30; M that sgemm_i8_quantize takes: 2^24 - 1 rows, four times as many of
+ * K up to 1024, 16 times as many of K up to 256.
  */
 int sgemm_i8_quantize(int dtype, int M, int K, const void *X, int ldx,
                       void *values, int ldv, float *scales, void *stream);
