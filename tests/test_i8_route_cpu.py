@@ -183,3 +183,16 @@ def test_scales_of_rows_without_columns_need_their_source():
     """Rows of no columns may be NULL; their scales, if wanted, are still read from somewhere."""
     args = dict(SORT, dtype=4, H=0, X=None, rows=None, row_scales=AL)
     assert capi.sgemm_grouped_sort(**args) == NULL
+
+
+def test_rows_of_groups_too_far_apart():
+    """Groups of one row: the step between the groups is the rows', the unused step of a group's only row is not looked at."""
+    import torch
+
+    import fp32_sgemm_tuning_amd as lib
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        lib.sgemm_i8_quantize(_meta((3, 1, 8), torch.float32, (2 ** 31, 8, 1)))
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        lib.sgemm_i8_dequantize(lib.I8Matrix(_meta((3, 1, 8), torch.int8, (2 ** 31, 8, 1)), _meta((3, 1), torch.float32)))
+    with pytest.raises(ValueError, match="device tensors"):
+        lib.sgemm_i8_quantize(_meta((3, 1, 8), torch.float32, (8, 2 ** 31, 1)))
